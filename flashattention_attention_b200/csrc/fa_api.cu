@@ -75,6 +75,8 @@ fa_status make_ctx(fa_stream_t s, LaunchCtx* ctx) {
   return status_word(&ctx->wd.word);
 }
 
+constexpr int kMaxTopPages = 4096;  // pages one query may choose
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Head sizes of the tensor-core prefill: 32, 64, 96 or 128 (bf16 or int8 K/V);
@@ -340,7 +342,7 @@ size_t fa_decode_workspace_size(int32_t batch, int32_t hq, int32_t capacity, int
 namespace {
 // Host checks shared by the decode entry points (everything but the
 // workspace); FA_OK means launchable, or a no-op when batch == 0.
-fa_status decode_args(const fa_decode_params* p) {
+fa_status decode_args(const fa_decode_params* p, bool packed_ok = false) {
   if (p == nullptr) return FA_ERR_INVALID;
   if (p->batch < 0 || p->hq <= 0 || p->hkv <= 0 || p->hq % p->hkv != 0) return FA_ERR_INVALID;
   if (p->capacity <= 0 || p->capacity % 32 != 0) return FA_ERR_INVALID;
@@ -348,9 +350,9 @@ fa_status decode_args(const fa_decode_params* p) {
   if (p->split_keys < 0 || p->split_keys % 256 != 0) return FA_ERR_INVALID;
   if (!epilogue_ok(p->epilogue, p->n_epilogue)) return FA_ERR_INVALID;
   if (!std::isfinite(p->softmax_scale)) return FA_ERR_INVALID;
-  if (p->kv_dtype != FA_I8 && p->kv_dtype != FA_BF16) return FA_ERR_INVALID;
+  if (p->kv_dtype != FA_I8 && p->kv_dtype != FA_BF16 && !(packed_ok && p->kv_dtype == FA_I4)) return FA_ERR_INVALID;
   if (p->head_dim <= 0 || p->head_dim % 32 != 0) return FA_ERR_INVALID;
-  // int8 or bf16 cache: 32, 64, 96, 128, 256
+  // every cache type: 32, 64, 96, 128, 256
   if (!(p->head_dim == 32 || p->head_dim == 64 || p->head_dim == 96 || p->head_dim == 128 || p->head_dim == 256))
     return FA_ERR_UNSUPPORTED;
   if (p->batch == 0) return FA_OK;
@@ -359,7 +361,7 @@ fa_status decode_args(const fa_decode_params* p) {
     return FA_ERR_INVALID;
   if (!aligned16(p->q) || !aligned16(p->k_cache) || !aligned16(p->v_cache) || !aligned16(p->out))
     return FA_ERR_INVALID;
-  if (p->kv_dtype == FA_I8) {
+  if (p->kv_dtype == FA_I8 || p->kv_dtype == FA_I4) {
     if (p->k_scales == nullptr || p->v_scales == nullptr) return FA_ERR_INVALID;
     if (!aligned16(p->k_scales) || !aligned16(p->v_scales)) return FA_ERR_INVALID;
   }
@@ -378,23 +380,52 @@ fa_status fa_attention_decode(const fa_decode_params* p, fa_stream_t stream) {
   return launch_decode(*p, nullptr, p->split_keys, ctx);
 }
 
-fa_status fa_attention_decode_paged(const fa_decode_params* p, const fa_kv_pages* pages, fa_stream_t stream) {
-  fa_status st = decode_args(p);
+namespace {
+// Host checks shared by the paged decodes; *launch is false when the call has
+// nothing to do.
+fa_status decode_paged_args(const fa_decode_params* p, const fa_kv_pages* pages, bool* launch) {
+  *launch = false;
+  fa_status st = decode_args(p, true);
   if (st != FA_OK) return st;
   if (pages == nullptr || pages->max_pages < 1 || pages->num_pages < 1 || pages->page_size < 32 ||
       pages->page_size % 32 != 0)
     return FA_ERR_INVALID;
   if (static_cast<int64_t>(pages->max_pages) * pages->page_size != p->capacity) return FA_ERR_INVALID;
-  if (static_cast<int64_t>(pages->num_pages) * p->hkv * pages->page_size >= (int64_t(1) << 31))
+  if (static_cast<int64_t>(pages->num_pages) * p->hkv * pages->page_size >= (int64_t(1) << 31) ||
+      static_cast<int64_t>(p->batch) * p->hq >= (int64_t(1) << 31))
     return FA_ERR_UNSUPPORTED;
   if (p->batch == 0) return FA_OK;
   if (pages->block_table == nullptr || !aligned16(pages->block_table)) return FA_ERR_INVALID;
   const size_t need = fa_decode_workspace_size(p->batch, p->hq, p->capacity, p->head_dim);
   if (p->workspace == nullptr || p->workspace_bytes < need || !aligned16(p->workspace)) return FA_ERR_WORKSPACE;
+  *launch = true;
+  return FA_OK;
+}
+}  // namespace
+
+fa_status fa_attention_decode_paged(const fa_decode_params* p, const fa_kv_pages* pages, fa_stream_t stream) {
+  bool launch = false;
+  fa_status st = decode_paged_args(p, pages, &launch);
+  if (st != FA_OK || !launch) return st;
   LaunchCtx ctx;
   st = make_ctx(stream, &ctx);
   if (st != FA_OK) return st;
+  if (p->kv_dtype == FA_I4) return launch_decode_pages(*p, *pages, nullptr, 0, ctx);
   return launch_decode(*p, pages, p->split_keys, ctx);
+}
+
+fa_status fa_attention_decode_selected(const fa_decode_params* p, const fa_kv_pages* pages, const int32_t* selected,
+                                       int32_t top_k, fa_stream_t stream) {
+  if (p != nullptr && p->window != 0) return FA_ERR_INVALID;
+  if (top_k < 1 || top_k > kMaxTopPages) return FA_ERR_INVALID;
+  bool launch = false;
+  fa_status st = decode_paged_args(p, pages, &launch);
+  if (st != FA_OK || !launch) return st;
+  if (selected == nullptr || !aligned16(selected)) return FA_ERR_INVALID;
+  LaunchCtx ctx;
+  st = make_ctx(stream, &ctx);
+  if (st != FA_OK) return st;
+  return launch_decode_pages(*p, *pages, selected, top_k, ctx);
 }
 
 fa_status fa_attention_decode_noalloc(const fa_decode_params* p, fa_stream_t stream) {
@@ -454,6 +485,137 @@ fa_status fa_kv_append_paged(const fa_kv_append_params* p, const fa_kv_pages* pa
   st = make_ctx(stream, &ctx);
   if (st != FA_OK) return st;
   return launch_kv_append(*p, pages, ctx);
+}
+
+namespace {
+bool ranges_overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a0 < b0 + b_bytes && b0 < a0 + a_bytes;
+}
+
+// Pools of any cache type behind a block table.
+fa_status pools_args(const fa_kv_pages* pages, int32_t batch, int32_t hkv, int32_t head_dim) {
+  if (batch < 0 || hkv < 1) return FA_ERR_INVALID;
+  if (head_dim < 16 || head_dim % 16 != 0) return FA_ERR_INVALID;
+  if (head_dim > 256) return FA_ERR_UNSUPPORTED;
+  if (pages == nullptr || pages->max_pages < 1 || pages->num_pages < 1 || pages->page_size < 1) return FA_ERR_INVALID;
+  if (static_cast<int64_t>(batch) * hkv >= (int64_t(1) << 31) ||
+      static_cast<int64_t>(pages->num_pages) * hkv * pages->page_size >= (int64_t(1) << 31) ||
+      static_cast<int64_t>(pages->max_pages) * pages->page_size >= (int64_t(1) << 31))
+    return FA_ERR_UNSUPPORTED;
+  if (batch > 0 && (pages->block_table == nullptr || !aligned16(pages->block_table))) return FA_ERR_INVALID;
+  return FA_OK;
+}
+
+bool cache_type_ok(int32_t dtype, const void* k_scales, const void* v_scales) {
+  if (dtype == FA_BF16) return true;
+  if (dtype != FA_I8 && dtype != FA_I4) return false;
+  return k_scales != nullptr && v_scales != nullptr && aligned16(k_scales) && aligned16(v_scales);
+}
+}  // namespace
+
+fa_status fa_kv_append_rope_paged(const fa_kv_append_rope_params* p, const fa_kv_pages* pages, fa_stream_t stream) {
+  if (p == nullptr) return FA_ERR_INVALID;
+  fa_status st = pools_args(pages, p->batch, p->hkv, p->head_dim);
+  if (st != FA_OK) return st;
+  if (p->x_dtype != FA_BF16 && p->x_dtype != FA_F32) return FA_ERR_INVALID;
+  if (p->total < 0 || (p->cu_seqlens == nullptr && p->total != p->batch)) return FA_ERR_INVALID;
+  if (p->batch == 0) return p->total == 0 ? FA_OK : FA_ERR_INVALID;
+  if (p->rot_dim < 0 || p->rot_dim % 16 != 0 || p->rot_dim > p->head_dim) return FA_ERR_INVALID;
+  if (p->interleaved != 0 && p->interleaved != 1) return FA_ERR_INVALID;
+  if (p->rot_dim > 0 && (p->rope_table == nullptr || !aligned16(p->rope_table) || p->rope_rows < 1))
+    return FA_ERR_INVALID;
+  if (p->cur_pos == nullptr || !aligned16(p->cur_pos) || (p->cu_seqlens != nullptr && !aligned16(p->cu_seqlens)) ||
+      (p->cache_seqlens != nullptr && !aligned16(p->cache_seqlens)))
+    return FA_ERR_INVALID;
+  if (p->cache_seqlens != nullptr) {
+    const size_t n = 4ull * p->batch;  // the kernel reads the other two while it writes this one
+    if (ranges_overlap(p->cache_seqlens, n, p->cur_pos, n) ||
+        (p->cu_seqlens != nullptr && ranges_overlap(p->cache_seqlens, n, p->cu_seqlens, n + 4)))
+      return FA_ERR_INVALID;
+  }
+  if (!cache_type_ok(p->cache_dtype, p->k_scales, p->v_scales)) return FA_ERR_INVALID;
+  if (p->total > 0) {
+    const int64_t lanes = p->x_dtype == FA_BF16 ? 8 : 4;  // elements of 16 bytes
+    if (p->k_new == nullptr || p->v_new == nullptr || p->k_cache == nullptr || p->v_cache == nullptr ||
+        !aligned16(p->k_new) || !aligned16(p->v_new) || !aligned16(p->k_cache) || !aligned16(p->v_cache) ||
+        (p->key_bounds != nullptr && !aligned16(p->key_bounds)))
+      return FA_ERR_INVALID;
+    if (p->k_token_stride % lanes || p->k_head_stride % lanes || p->v_token_stride % lanes ||
+        p->v_head_stride % lanes)
+      return FA_ERR_INVALID;
+    if (p->q != nullptr) {
+      if (p->hq < 1 || p->q_out == nullptr || !aligned16(p->q) || !aligned16(p->q_out)) return FA_ERR_INVALID;
+      if (p->q_token_stride % lanes || p->q_head_stride % lanes || p->q_out_token_stride % 8 ||
+          p->q_out_head_stride % 8)
+        return FA_ERR_INVALID;
+    }
+  }
+  LaunchCtx ctx;
+  st = make_ctx(stream, &ctx);
+  if (st != FA_OK) return st;
+  return launch_kv_append_rope(*p, *pages, ctx);
+}
+
+fa_status fa_rope_table(int32_t rows, int32_t rot_dim, double base, float* table) {
+  if (rows < 0 || rot_dim < 16 || rot_dim > 256 || rot_dim % 16 != 0) return FA_ERR_INVALID;
+  if (!(base > 0.0) || !std::isfinite(base)) return FA_ERR_INVALID;
+  if (rows == 0) return FA_OK;
+  if (table == nullptr) return FA_ERR_INVALID;
+  const int half = rot_dim / 2;
+  for (int i = 0; i < half; ++i) {
+    const double w = std::pow(base, -2.0 * i / rot_dim);
+    for (int32_t r = 0; r < rows; ++r) {
+      float* row = table + static_cast<int64_t>(r) * rot_dim;
+      row[i] = static_cast<float>(std::cos(r * w));
+      row[half + i] = static_cast<float>(std::sin(r * w));
+    }
+  }
+  return FA_OK;
+}
+
+fa_status fa_kv_read_paged(const fa_kv_read_params* p, const fa_kv_pages* pages, fa_stream_t stream) {
+  if (p == nullptr) return FA_ERR_INVALID;
+  fa_status st = pools_args(pages, p->batch, p->hkv, p->head_dim);
+  if (st != FA_OK) return st;
+  if (p->out_dtype != FA_BF16 && p->out_dtype != FA_F32) return FA_ERR_INVALID;
+  if (!cache_type_ok(p->cache_dtype, p->k_scales, p->v_scales)) return FA_ERR_INVALID;
+  if (p->total < 0) return FA_ERR_INVALID;
+  if (p->batch == 0 || p->total == 0) return FA_OK;
+  const void* ptrs[] = {p->k_cache, p->v_cache, p->k_out, p->v_out, p->cu_seqlens};
+  for (const void* q : ptrs)
+    if (q == nullptr || !aligned16(q)) return FA_ERR_INVALID;
+  if (p->start != nullptr && !aligned16(p->start)) return FA_ERR_INVALID;
+  LaunchCtx ctx;
+  st = make_ctx(stream, &ctx);
+  if (st != FA_OK) return st;
+  return launch_kv_read(*p, *pages, ctx);
+}
+
+size_t fa_page_select_workspace_size(int32_t batch, int32_t hkv, int32_t max_pages) {
+  if (batch <= 0 || hkv <= 0 || max_pages <= 0) return 0;
+  return page_select_workspace_bytes(batch, hkv, max_pages);
+}
+
+fa_status fa_page_select(const fa_page_select_params* p, const fa_kv_pages* pages, fa_stream_t stream) {
+  if (p == nullptr) return FA_ERR_INVALID;
+  fa_status st = pools_args(pages, p->batch, p->hkv, p->head_dim);
+  if (st != FA_OK) return st;
+  if (p->hq < 1 || p->hq % p->hkv != 0) return FA_ERR_INVALID;
+  if (p->top_k < 1 || p->top_k > kMaxTopPages || p->n_first < 0 || p->n_recent < 0 ||
+      static_cast<int64_t>(p->n_first) + p->n_recent > p->top_k)
+    return FA_ERR_INVALID;
+  if (pages->max_pages > 65536) return FA_ERR_UNSUPPORTED;
+  if (p->batch == 0) return FA_OK;
+  const void* ptrs[] = {p->q, p->key_bounds, p->cache_seqlens, p->selected};
+  for (const void* q : ptrs)
+    if (q == nullptr || !aligned16(q)) return FA_ERR_INVALID;
+  const size_t need = fa_page_select_workspace_size(p->batch, p->hkv, pages->max_pages);
+  if (p->workspace == nullptr || p->workspace_bytes < need || !aligned16(p->workspace)) return FA_ERR_WORKSPACE;
+  LaunchCtx ctx;
+  st = make_ctx(stream, &ctx);
+  if (st != FA_OK) return st;
+  return launch_page_select(*p, *pages, ctx);
 }
 
 fa_status fa_tq_codebook(int32_t head_dim, int32_t bits, float* levels) {

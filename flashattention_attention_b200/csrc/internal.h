@@ -42,6 +42,13 @@ fa_status launch_prefill_tc(const fa_fwd_params& p, const fa_kv_pages* pages, co
 fa_status launch_merge(float* o_acc, float* lse_acc, const void* o_part, int part_dtype, const float* lse_part,
                        int64_t rows, int d, void* out, int out_dtype, const fa_epi_op* epi, int n_epi,
                        const LaunchCtx& ctx);
+fa_status launch_kv_append_rope(const fa_kv_append_rope_params& p, const fa_kv_pages& pages, const LaunchCtx& ctx);
+fa_status launch_kv_read(const fa_kv_read_params& p, const fa_kv_pages& pages, const LaunchCtx& ctx);
+size_t page_select_workspace_bytes(int batch, int hkv, int max_pages);
+fa_status launch_page_select(const fa_page_select_params& p, const fa_kv_pages& pages, const LaunchCtx& ctx);
+// FA_I4 pools, or (selected given) the chosen pages of any pool
+fa_status launch_decode_pages(const fa_decode_params& p, const fa_kv_pages& pages, const int32_t* selected, int top_k,
+                              const LaunchCtx& ctx);
 fa_status launch_decode(const fa_decode_params& p, const fa_kv_pages* pages, int split_keys, const LaunchCtx& ctx);
 // TurboQuant: keys per split of the decode, its split count, launchers and the host codebook
 constexpr int kTqSplitKeys = 2048;

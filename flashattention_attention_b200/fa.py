@@ -25,7 +25,7 @@ lib = ctypes.CDLL(_LIB_PATH)
 
 # --- fa.h mirrors -------------------------------------------------------------
 FA_OK, FA_ERR_INVALID, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT, FA_ERR_WORKSPACE = range(6)
-FA_F32, FA_BF16, FA_I8 = 0, 1, 2
+FA_F32, FA_BF16, FA_I8, FA_I4 = 0, 1, 2, 3
 FA_EPI_MUL, FA_EPI_ADD = 1, 2
 FA_MAX_EPILOGUE = 8
 FA_ACC_FIRST, FA_ACC_LAST = 1, 2
@@ -99,6 +99,44 @@ class KvAppendParams(ctypes.Structure):
                 ("head_dim", ctypes.c_int32), ("capacity", ctypes.c_int32)]
 
 
+_P, _I32, _I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+
+
+class KvAppendRopeParams(ctypes.Structure):
+    _fields_ = [("k_new", _P), ("v_new", _P), ("q", _P), ("q_out", _P),
+                ("k_token_stride", _I64), ("k_head_stride", _I64), ("v_token_stride", _I64), ("v_head_stride", _I64),
+                ("q_token_stride", _I64), ("q_head_stride", _I64),
+                ("q_out_token_stride", _I64), ("q_out_head_stride", _I64),
+                ("rope_table", _P), ("k_cache", _P), ("v_cache", _P), ("k_scales", _P), ("v_scales", _P),
+                ("key_bounds", _P), ("cu_seqlens", _P), ("cur_pos", _P), ("cache_seqlens", _P),
+                ("x_dtype", _I32), ("cache_dtype", _I32), ("batch", _I32), ("total", _I32), ("hq", _I32),
+                ("hkv", _I32), ("head_dim", _I32), ("rot_dim", _I32), ("interleaved", _I32), ("rope_rows", _I32)]
+
+
+class KvReadParams(ctypes.Structure):
+    _fields_ = [("k_cache", _P), ("v_cache", _P), ("k_scales", _P), ("v_scales", _P), ("k_out", _P), ("v_out", _P),
+                ("cu_seqlens", _P), ("start", _P), ("cache_dtype", _I32), ("out_dtype", _I32), ("batch", _I32),
+                ("total", _I32), ("hkv", _I32), ("head_dim", _I32)]
+
+
+class PageSelectParams(ctypes.Structure):
+    _fields_ = [("q", _P), ("key_bounds", _P), ("cache_seqlens", _P), ("selected", _P), ("batch", _I32), ("hq", _I32),
+                ("hkv", _I32), ("head_dim", _I32), ("top_k", _I32), ("n_first", _I32), ("n_recent", _I32),
+                ("workspace", _P), ("workspace_bytes", ctypes.c_size_t)]
+
+
+lib.fa_kv_append_rope_paged.restype = ctypes.c_int
+lib.fa_kv_append_rope_paged.argtypes = [ctypes.POINTER(KvAppendRopeParams), ctypes.POINTER(KvPages), _P]
+lib.fa_rope_table.restype = ctypes.c_int
+lib.fa_rope_table.argtypes = [_I32, _I32, ctypes.c_double, _P]
+lib.fa_kv_read_paged.restype = ctypes.c_int
+lib.fa_kv_read_paged.argtypes = [ctypes.POINTER(KvReadParams), ctypes.POINTER(KvPages), _P]
+lib.fa_page_select_workspace_size.restype = ctypes.c_size_t
+lib.fa_page_select_workspace_size.argtypes = [_I32] * 3
+lib.fa_page_select.restype = ctypes.c_int
+lib.fa_page_select.argtypes = [ctypes.POINTER(PageSelectParams), ctypes.POINTER(KvPages), _P]
+lib.fa_attention_decode_selected.restype = ctypes.c_int
+lib.fa_attention_decode_selected.argtypes = [ctypes.POINTER(DecodeParams), ctypes.POINTER(KvPages), _P, _I32, _P]
 lib.fa_compress_kv.restype = ctypes.c_int
 lib.fa_compress_kv.argtypes = [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int32,
                                ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
@@ -490,7 +528,14 @@ def attention_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
                            out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """s_q = 1 decode over page pools k_pages/v_pages [num_pages, hkv, page_size, d]
     (int8 with scales [num_pages, hkv, page_size], or bf16) through a device
-    int32 block_table [B, max_pages]; as fa_attention_decode_paged in fa.h."""
+    int32 block_table [B, max_pages]; as fa_attention_decode_paged in fa.h.
+    uint8 pools [num_pages, hkv, page_size, d/2] hold 4-bit codes, with scales
+    [num_pages, hkv, page_size, 2] of (step, offset); split_keys must be 0."""
+    if k_pages.dtype == torch.uint8:
+        if split_keys != 0:
+            raise ValueError("split_keys does not apply to a 4-bit cache")
+        return _decode_pages(q, k_pages, v_pages, cache_seqlens, block_table, None, hq, hkv, k_scales, v_scales, window,
+                             scale, epilogue, max_seqlen, workspace, out, stream)
     for name, t in (("q", q), ("k_pages", k_pages), ("v_pages", v_pages), ("cache_seqlens", cache_seqlens),
                     ("block_table", block_table)):
         _contig_cuda(t, name)
@@ -574,6 +619,299 @@ def _append_params(k_new, v_new, k_cache, v_cache, cur_pos, hkv, k_scales, v_sca
     p.batch, p.hkv = cur_pos.numel(), hkv
     p.head_dim, p.capacity = k_cache.shape[-1], k_cache.shape[1]
     return p
+
+
+# --- rotated append, page selection and attention over page pools -----------------
+
+_CACHE_DT = {torch.bfloat16: FA_BF16, torch.int8: FA_I8, torch.uint8: FA_I4}
+
+
+def _on_device(dev: torch.device, stream, what: str, fn, *args) -> None:
+    """Call fn(*args, stream) with `dev` current: on `stream`, or on dev's current stream."""
+    if stream is None:
+        raw = torch.cuda.current_stream(dev).cuda_stream
+    else:
+        if stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+        raw = stream.cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, raw)
+    if status != FA_OK:
+        raise FAError(status, what)
+
+
+def _new(shape, dtype, dev: torch.device, stream) -> torch.Tensor:
+    """A tensor for a call on `stream`: allocated on that stream, so that memory
+    freed when the call returns is only reused in its order."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _operand(t, name: str, dev: torch.device, dtype, shape) -> int:
+    """The address of a contiguous tensor on dev with this dtype and shape (0 for None)."""
+    if t is None:
+        return 0
+    if t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on {dev}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != shape:
+        _shape(t, shape, name)
+    return t.data_ptr()
+
+
+def _pool_operands(k_pages, v_pages, k_scales, v_scales, block_table, batch: int, hkv: int, d: int, dev):
+    """(cache dtype, KvPages, pool and scale addresses) of page pools; ValueError where they do not fit together."""
+    kind = _CACHE_DT.get(k_pages.dtype)
+    if kind is None:
+        raise ValueError(f"a page pool is bfloat16, int8 or uint8 (4-bit codes), not {k_pages.dtype}")
+    if len(k_pages.shape) != 4:
+        raise ValueError(f"k_pages has shape {tuple(k_pages.shape)}, expected 4 dimensions")
+    num_pages, _, page_size, _ = k_pages.shape
+    pool = (num_pages, hkv, page_size, d // 2 if kind == FA_I4 else d)
+    kp = _operand(k_pages, "k_pages", dev, k_pages.dtype, pool)
+    vp = _operand(v_pages, "v_pages", dev, k_pages.dtype, pool)
+    if kind == FA_BF16:
+        if k_scales is not None or v_scales is not None:
+            raise ValueError("a bfloat16 cache has no scales")
+        ks = vs = 0
+    else:
+        if k_scales is None or v_scales is None:
+            raise ValueError("k_scales and v_scales are required with a quantised cache")
+        rows = (num_pages, hkv, page_size, 2) if kind == FA_I4 else (num_pages, hkv, page_size)
+        ks = _operand(k_scales, "k_scales", dev, torch.float32, rows)
+        vs = _operand(v_scales, "v_scales", dev, torch.float32, rows)
+    if len(block_table.shape) != 2:
+        raise ValueError(f"block_table has shape {tuple(block_table.shape)}, expected 2 dimensions")
+    max_pages = block_table.shape[1]
+    table = _operand(block_table, "block_table", dev, torch.int32, (batch, max_pages))
+    return kind, KvPages(table, max_pages, page_size, num_pages), kp, vp, ks, vs
+
+
+def _int(x, name: str, lo: int = 0) -> int:
+    """x as an int of the C ABI's 32 bits, at least lo."""
+    x = int(x)
+    if not lo <= x < 2 ** 31:
+        raise ValueError(f"{name} = {x} is out of range")
+    return x
+
+
+def _cuda_device(t, name: str) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _rows_operand(t, name: str, dev: torch.device, dtype, shape):
+    """(address, token stride, head stride) of rows [tokens, heads, d] whose last dimension is contiguous."""
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != shape:
+        _shape(t, shape, name)
+    st = t.stride()
+    if st[2] != 1 and shape[2] > 1:
+        raise ValueError(f"{name}: the channels of a row must be contiguous")
+    # a dimension of one row has no stride of its own
+    return t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0
+
+
+def rope_table(rows: int, rot_dim: int, base: float = 10000.0) -> torch.Tensor:
+    """The rotation table [rows, rot_dim] (fp32, CPU): cos then sin of
+    p * base^(-2i/rot_dim), computed in double.  As fa_rope_table in fa.h."""
+    if rows < 0 or rot_dim < 1:
+        raise ValueError("rows must not be negative, rot_dim positive")
+    out = torch.empty((rows, rot_dim), dtype=torch.float32)
+    _check(lib.fa_rope_table(rows, rot_dim, float(base), out.data_ptr()), "fa_rope_table")
+    return out
+
+
+def kv_append_rope_paged(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                         cur_pos: torch.Tensor, block_table: torch.Tensor, *, q: Optional[torch.Tensor] = None,
+                         q_out: Optional[torch.Tensor] = None, rope_table: Optional[torch.Tensor] = None,
+                         interleaved: bool = False, k_scales=None, v_scales=None,
+                         key_bounds: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                         cache_seqlens: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """Append new tokens to page pools, keys (and the queries q) rotated to
+    their positions.  k_new, v_new [total, hkv, d] and q [total, hq, d] (bf16
+    or fp32) may be slices of one projection: any token and head strides.
+    Without cu_seqlens one token per sequence, else device int32 [B+1]; the
+    first goes to slot cur_pos[b] (device int32 [B]).  rope_table fp32
+    [rows, rot_dim] (None: no rotation).  Pools as attention_decode_paged:
+    bf16, int8 or uint8 (4-bit).  key_bounds bf16 [num_pages, hkv, 2, d] is
+    kept up to date for page_select; cache_seqlens becomes the new lengths.
+    Returns the rotated queries in bf16 in the layout the attention calls
+    take: [B*hq, d] without cu_seqlens, else [hq, total, d] (`q_out` of that
+    shape if given), or None without q.  As fa_kv_append_rope_paged in fa.h."""
+    dev = _cuda_device(k_pages, "k_pages")
+    if len(k_new.shape) != 3 or len(cur_pos.shape) != 1:
+        raise ValueError(f"k_new must be [total, hkv, d] and cur_pos [batch]; got {tuple(k_new.shape)} and "
+                         f"{tuple(cur_pos.shape)}")
+    total, hkv, d = k_new.shape
+    batch = cur_pos.shape[0]
+    xt = k_new.dtype
+    if xt != torch.bfloat16 and xt != torch.float32:
+        raise ValueError(f"k_new must be bfloat16 or float32, not {xt}")
+    if cu_seqlens is None and total != batch:
+        raise ValueError(f"without cu_seqlens there is one token per sequence: {total} tokens, {batch} sequences")
+    kn, kts, khs = _rows_operand(k_new, "k_new", dev, xt, (total, hkv, d))
+    vn, vts, vhs = _rows_operand(v_new, "v_new", dev, xt, (total, hkv, d))
+    kind, pg, kp, vp, ks, vs = _pool_operands(k_pages, v_pages, k_scales, v_scales, block_table, batch, hkv, d, dev)
+    bounds = _operand(key_bounds, "key_bounds", dev, torch.bfloat16, (k_pages.shape[0], hkv, 2, d))
+    pos = _operand(cur_pos, "cur_pos", dev, torch.int32, (batch,))
+    cu = _operand(cu_seqlens, "cu_seqlens", dev, torch.int32, (batch + 1,))
+    lens = _operand(cache_seqlens, "cache_seqlens", dev, torch.int32, (batch,))
+    table, rows, rot = 0, 0, 0
+    if rope_table is not None:
+        if len(rope_table.shape) != 2:
+            raise ValueError(f"rope_table has shape {tuple(rope_table.shape)}, expected 2 dimensions")
+        rows, rot = rope_table.shape
+        table = _operand(rope_table, "rope_table", dev, torch.float32, (rows, rot))
+    qp = qo = qts = qhs = ots = ohs = hq = 0
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+    else:
+        if len(q.shape) != 3:
+            raise ValueError(f"q must be [total, hq, d]; got {tuple(q.shape)}")
+        hq = q.shape[1]
+        qp, qts, qhs = _rows_operand(q, "q", dev, xt, (total, hq, d))
+        shape = (total * hq, d) if cu_seqlens is None else (hq, total, d)
+        if q_out is None:
+            q_out = _new(shape, torch.bfloat16, dev, stream)
+        qo = _operand(q_out, "q_out", dev, torch.bfloat16, shape)
+        ots, ohs = (hq * d, d) if cu_seqlens is None else (d, total * d)
+    p = KvAppendRopeParams(kn, vn, qp, qo, kts, khs, vts, vhs, qts, qhs, ots, ohs, table, kp, vp, ks, vs, bounds, cu, pos,
+                           lens, FA_BF16 if xt == torch.bfloat16 else FA_F32, kind, batch, total, hq, hkv, d, rot,
+                           1 if interleaved else 0, rows)
+    _on_device(dev, stream, "fa_kv_append_rope_paged", lib.fa_kv_append_rope_paged, p, pg)
+    return q_out
+
+
+def kv_read_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, cu_seqlens: torch.Tensor, block_table: torch.Tensor, *,
+                  total: int, start: Optional[torch.Tensor] = None, k_scales=None, v_scales=None,
+                  out_dtype: torch.dtype = torch.bfloat16, k_out: Optional[torch.Tensor] = None,
+                  v_out: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(k, v) [hkv, total, d] of the cached rows start[b] .. of each sequence
+    (start None: from slot 0), cu_seqlens[b+1] - cu_seqlens[b] of them, as bf16
+    or fp32 values in attention_fwd's varlen layout.  As fa_kv_read_paged in fa.h."""
+    dev = _cuda_device(k_pages, "k_pages")
+    if len(cu_seqlens.shape) != 1 or cu_seqlens.shape[0] < 1 or len(k_pages.shape) != 4:
+        raise ValueError("cu_seqlens must be [batch + 1] and k_pages [num_pages, hkv, page_size, d]")
+    batch, hkv = cu_seqlens.shape[0] - 1, k_pages.shape[1]
+    d = k_pages.shape[3] * (2 if k_pages.dtype == torch.uint8 else 1)
+    kind, pg, kp, vp, ks, vs = _pool_operands(k_pages, v_pages, k_scales, v_scales, block_table, batch, hkv, d, dev)
+    if out_dtype != torch.bfloat16 and out_dtype != torch.float32:
+        raise ValueError(f"out_dtype must be bfloat16 or float32, not {out_dtype}")
+    shape = (hkv, _int(total, "total"), d)
+    if k_out is None:
+        k_out = _new(shape, out_dtype, dev, stream)
+    if v_out is None:
+        v_out = _new(shape, out_dtype, dev, stream)
+    p = KvReadParams(kp, vp, ks, vs, _operand(k_out, "k_out", dev, out_dtype, shape),
+                     _operand(v_out, "v_out", dev, out_dtype, shape),
+                     _operand(cu_seqlens, "cu_seqlens", dev, torch.int32, (batch + 1,)),
+                     _operand(start, "start", dev, torch.int32, (batch,)), kind,
+                     FA_BF16 if out_dtype == torch.bfloat16 else FA_F32, batch, shape[1], hkv, d)
+    _on_device(dev, stream, "fa_kv_read_paged", lib.fa_kv_read_paged, p, pg)
+    return k_out, v_out
+
+
+def _decode_queries(q, cache_seqlens, hq: int, hkv: int, dev):
+    """(batch, d, address of q, address of cache_seqlens) of a decode step's operands."""
+    if hq < 1 or hkv < 1 or hq % hkv:
+        raise ValueError(f"hq = {hq} must be a positive multiple of hkv = {hkv}")
+    if len(cache_seqlens.shape) != 1:
+        raise ValueError(f"cache_seqlens has shape {tuple(cache_seqlens.shape)}, expected 1 dimension")
+    batch, d = cache_seqlens.shape[0], q.shape[-1]
+    shape = tuple(q.shape)
+    if shape != (batch * hq, d) and shape != (batch * hq, 1, d):
+        raise ValueError(f"q has shape {shape}, expected batch*hq = {batch * hq} rows")
+    return (batch, d, _operand(q, "q", dev, torch.bfloat16, shape),
+            _operand(cache_seqlens, "cache_seqlens", dev, torch.int32, (batch,)))
+
+
+def page_select(q: torch.Tensor, key_bounds: torch.Tensor, cache_seqlens: torch.Tensor, block_table: torch.Tensor, *,
+                hq: int, hkv: int, page_size: int, top_k: int, n_first: int = 1, n_recent: int = 1,
+                out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """int32 [B, hkv, top_k]: the logical pages each sequence's query (q
+    [B*hq, d] bf16) is most likely to need, by the bounds
+    kv_append_rope_paged keeps; ascending, -1 behind the last.  The first
+    n_first and last n_recent pages are always among them.  As fa_page_select
+    in fa.h."""
+    dev = _cuda_device(q, "q")
+    batch, d, qp, lens = _decode_queries(q, cache_seqlens, hq, hkv, dev)
+    if len(key_bounds.shape) != 4 or len(block_table.shape) != 2:
+        raise ValueError("key_bounds must be [num_pages, hkv, 2, d] and block_table [batch, max_pages]")
+    num_pages, max_pages = key_bounds.shape[0], block_table.shape[1]
+    bounds = _operand(key_bounds, "key_bounds", dev, torch.bfloat16, (num_pages, hkv, 2, d))
+    pg = KvPages(_operand(block_table, "block_table", dev, torch.int32, (batch, max_pages)), max_pages,
+                 _int(page_size, "page_size", 1), num_pages)
+    top_k = _int(top_k, "top_k", 1)
+    shape = (batch, hkv, top_k)
+    if out is None:
+        out = _new(shape, torch.int32, dev, stream)
+    if workspace is None:
+        nbytes = lib.fa_page_select_workspace_size(batch, hkv, max_pages)
+        workspace = _new((max(nbytes, 16),), torch.uint8, dev, stream)
+    p = PageSelectParams(qp, bounds, lens, _operand(out, "out", dev, torch.int32, shape), batch, hq, hkv, d, top_k,
+                         _int(n_first, "n_first"), _int(n_recent, "n_recent"), _workspace(workspace, dev),
+                         workspace.numel() * workspace.element_size())
+    _on_device(dev, stream, "fa_page_select", lib.fa_page_select, p, pg)
+    return out
+
+
+def _workspace(t, dev: torch.device) -> int:
+    if t.device != dev or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    return t.data_ptr()
+
+
+def attention_decode_selected(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                              cache_seqlens: torch.Tensor, block_table: torch.Tensor, selected: torch.Tensor, *,
+                              hq: int, hkv: int, k_scales=None, v_scales=None, scale: Optional[float] = None,
+                              epilogue: Sequence[Tuple[str, float]] = (), workspace: Optional[torch.Tensor] = None,
+                              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """attention_decode_paged (bf16, int8 or uint8 4-bit pools) over the pages
+    `selected` (device int32 [B, hkv, top_k] of logical page numbers; -1: none)
+    only.  As fa_attention_decode_selected in fa.h."""
+    return _decode_pages(q, k_pages, v_pages, cache_seqlens, block_table, selected, hq, hkv, k_scales, v_scales, 0, scale,
+                         epilogue, 0, workspace, out, stream)
+
+
+def _decode_pages(q, k_pages, v_pages, cache_seqlens, block_table, selected, hq, hkv, k_scales, v_scales, window, scale,
+                  epilogue, max_seqlen, workspace, out, stream):
+    dev = _cuda_device(q, "q")
+    batch, d, qp, lens = _decode_queries(q, cache_seqlens, hq, hkv, dev)
+    kind, pg, kp, vp, ks, vs = _pool_operands(k_pages, v_pages, k_scales, v_scales, block_table, batch, hkv, d, dev)
+    capacity = pg.max_pages * pg.page_size
+    if out is None:
+        out = _new(q.shape, torch.bfloat16, dev, stream)
+    if workspace is None:
+        nbytes = lib.fa_decode_workspace_size(batch, hq, capacity, d)
+        workspace = _new((max(nbytes, 16),), torch.uint8, dev, stream)
+    p = DecodeParams(qp, kp, vp, ks, vs, lens, _operand(out, "out", dev, torch.bfloat16, tuple(q.shape)), kind, batch, hq,
+                     hkv, d, capacity, _int(max_seqlen, "max_seqlen"), _int(max(0, window), "window"),
+                     1.0 / math.sqrt(d) if scale is None else float(scale), 0)
+    p.workspace, p.workspace_bytes = _workspace(workspace, dev), workspace.numel() * workspace.element_size()
+    if epilogue:
+        p.n_epilogue = _fill_epilogue(p.epilogue, epilogue)
+    if selected is None:
+        _on_device(dev, stream, "fa_attention_decode_paged", lib.fa_attention_decode_paged, p, pg)
+    else:
+        if len(selected.shape) != 3:
+            raise ValueError(f"selected must be [batch, hkv, top_k]; got {tuple(selected.shape)}")
+        top_k = selected.shape[2]
+        sel = _operand(selected, "selected", dev, torch.int32, (batch, hkv, top_k))
+        _on_device(dev, stream, "fa_attention_decode_selected", lib.fa_attention_decode_selected, p, pg, sel, top_k)
+    return out
 
 
 def check_device_error(stream=None) -> int:

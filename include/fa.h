@@ -53,7 +53,9 @@ typedef enum {
 typedef enum {
     FA_F32 = 0,  /* IEEE fp32 */
     FA_BF16 = 1, /* bfloat16 */
-    FA_I8 = 2    /* int8 codes, with one fp32 scale per row (token, kv-head) */
+    FA_I8 = 2,   /* int8 codes, with one fp32 scale per row (token, kv-head) */
+    FA_I4 = 3    /* 4-bit codes, two channels per byte, with an fp32 (step, offset) pair
+                    per row: see fa_kv_append_rope_paged */
 } fa_dtype;
 
 /* Epilogue ops (fkl_python PR #6, Summary: a list of elementwise ops that
@@ -220,6 +222,14 @@ FA_API fa_status fa_attention_decode(const fa_decode_params *p, fa_stream_t stre
  * 0 in its place (never outside the pool) and that sequence's output is
  * meaningless.  Results equal fa_attention_decode's on the same keys bit for
  * bit (same split, same arithmetic).
+ *
+ * kv_dtype FA_I4 (this call and fa_attention_decode_selected only): pools
+ * [num_pages, hkv, page_size, d/2] of packed 4-bit codes and k_scales,
+ * v_scales [num_pages, hkv, page_size, 2], the rows fa_kv_append_rope_paged
+ * writes.  Key j has the value  code * step_j + offset_j  per channel; the
+ * codes enter the tensor cores exactly, steps and offsets are applied to the
+ * scores and the probabilities in fp32.  split_keys is not used (the work is
+ * split evenly over the device).
  */
 typedef struct {
     const int32_t *block_table;
@@ -375,6 +385,174 @@ FA_API fa_status fa_kv_append(const fa_kv_append_params *p, fa_stream_t stream);
  */
 FA_API fa_status fa_kv_append_paged(const fa_kv_append_params *p, const fa_kv_pages *pages,
                                     fa_stream_t stream);
+
+/*
+ * fa_kv_append_rope_paged -- append any number of new tokens per sequence to
+ * a paged cache, rotating the keys to their positions on the way in, with the
+ * queries of the same tokens rotated in the same pass and the per-page key
+ * bounds of fa_page_select kept up to date (FlashRT QKV Cache RoPE, Kernels:
+ * norm, rotation and cache write of the new K fused in one kernel whose slot
+ * is a device-side int32).
+ *   k_new, v_new  rows of x_dtype (FA_BF16 or FA_F32): the row of (token t,
+ *             KV head g) starts at element t * token_stride + g * head_stride
+ *             of its tensor, so they can be slices of one projection's output
+ *   q, q_out  optional: q rows of x_dtype (hq heads), q_out rows of FA_BF16,
+ *             each with strides of its own; q_out may not overlap q
+ *   cu_seqlens  device int32 [batch+1], ascending from 0: tokens
+ *             cu[b] .. cu[b+1]-1 belong to sequence b; NULL: one token per
+ *             sequence (total = batch).  Tokens at or past cu[batch] are
+ *             padding: nothing is read or written for them
+ *   cur_pos   device int32 [batch]: the slot (and position) of the first new
+ *             token of sequence b; token i of the sequence goes to slot
+ *             cur_pos[b] + i
+ *   cache_seqlens  optional device int32 [batch]: set to the slot after the
+ *             sequence's last new token; must not overlap cur_pos or cu_seqlens
+ *   rope_table  device fp32 [rope_rows, rot_dim]: row p holds cos(p w_i), i <
+ *             rot_dim/2, then sin(p w_i).  rot_dim a multiple of 16, at most
+ *             head_dim; 0 (table NULL): no rotation.  interleaved = 0 rotates
+ *             channels (i, i + rot_dim/2), 1 channels (2i, 2i + 1); channels
+ *             from rot_dim on are kept:  a' = a cos - b sin, b' = b cos + a sin,
+ *             every product and sum rounded to fp32
+ *   k_cache, v_cache, k_scales, v_scales  page pools as for
+ *             fa_attention_decode_paged, cache_dtype FA_BF16, FA_I8 or FA_I4
+ *   key_bounds  optional bf16 [num_pages, hkv, 2, head_dim]: per channel the
+ *             least and the greatest of the page's stored keys, each key
+ *             rounded to bf16.  A page whose slot 0 is among the new tokens
+ *             starts afresh, any other adds the new keys to what it holds
+ * A bf16 pool gets each value rounded once.  FA_I8 rows are quantised exactly
+ * as fa_compress_kv does (from the rotated fp32 values).  FA_I4 rows: with lo
+ * and hi the row's least and greatest value and r = hi - lo, channel c's code
+ * is round_half_even(15 (x_c - lo) / r) in 0 .. 15, step = r / 15, offset = lo
+ * (each operation rounded to fp32; r = 0 gives codes 0); the code of channel
+ * 2j is the low half of byte j of the row.  Rows whose values or range are
+ * not finite give unspecified codes.
+ * A token whose slot is outside [0, capacity) (capacity = max_pages *
+ * page_size), at or past rope_rows, or in a page outside [0, num_pages) is
+ * skipped (its q_out row too) and reported by fa_check_device_error as
+ * FA_ERR_INVALID; so is a whole sequence whose cu_seqlens range is not
+ * ascending within [0, total].  Two sequences of one call must not append to
+ * the same page.
+ * Requirements: head_dim a multiple of 16 up to 256; every row, pool, table
+ * and the strides (in bytes) 16-byte aligned; num_pages * hkv * page_size <
+ * 2^31.  total = 0 enqueues nothing but the cache_seqlens update.
+ */
+typedef struct {
+    const void *k_new;
+    const void *v_new;
+    const void *q;          /* NULL: keys and values only */
+    void *q_out;
+    int64_t k_token_stride, k_head_stride; /* elements */
+    int64_t v_token_stride, v_head_stride;
+    int64_t q_token_stride, q_head_stride;
+    int64_t q_out_token_stride, q_out_head_stride;
+    const float *rope_table;
+    void *k_cache;
+    void *v_cache;
+    float *k_scales;        /* FA_I8, FA_I4 */
+    float *v_scales;
+    void *key_bounds;       /* or NULL */
+    const int32_t *cu_seqlens;
+    const int32_t *cur_pos;
+    int32_t *cache_seqlens; /* or NULL */
+    int32_t x_dtype;        /* fa_dtype: FA_BF16 or FA_F32 */
+    int32_t cache_dtype;    /* fa_dtype: FA_BF16, FA_I8 or FA_I4 */
+    int32_t batch, total, hq, hkv, head_dim;
+    int32_t rot_dim, interleaved, rope_rows;
+} fa_kv_append_rope_params;
+
+FA_API fa_status fa_kv_append_rope_paged(const fa_kv_append_rope_params *p, const fa_kv_pages *pages,
+                                         fa_stream_t stream);
+
+/*
+ * fa_rope_table -- host function: rows [0, rows) of the rotation table above
+ * for the angles p * base^(-2i/rot_dim), computed in double and rounded to
+ * fp32, into table[] (host memory, rows * rot_dim floats).  rot_dim a
+ * multiple of 16 up to 256, base > 0.
+ */
+FA_API fa_status fa_rope_table(int32_t rows, int32_t rot_dim, double base, float *table);
+
+/*
+ * fa_kv_read_paged -- rows of a paged cache as values in a contiguous varlen
+ * layout: the inverse of the append, for work that needs the cached prefix as
+ * plain K and V (a chunk of new queries over a 4-bit cache through
+ * fa_attention_fwd, a cache moved to another precision).
+ *   k_out, v_out  [hkv, total, head_dim] out_dtype (FA_BF16 or FA_F32); row
+ *             cu_seqlens[b] + i of every plane becomes slot start[b] + i of
+ *             sequence b.  Rows at or past cu_seqlens[batch] are left as they
+ *             were
+ *   start     optional device int32 [batch] (NULL: 0 for all)
+ * The values: bf16 as stored; code * scale (FA_I8) and code * step + offset
+ * (FA_I4), each operation rounded to fp32, then rounded to out_dtype.  A slot
+ * outside [0, capacity) or in a page outside the pool leaves its row as it
+ * was and is reported by fa_check_device_error as FA_ERR_INVALID.
+ * Requirements as fa_kv_append_rope_paged.
+ */
+typedef struct {
+    const void *k_cache;
+    const void *v_cache;
+    const float *k_scales;
+    const float *v_scales;
+    void *k_out;
+    void *v_out;
+    const int32_t *cu_seqlens;
+    const int32_t *start;   /* or NULL */
+    int32_t cache_dtype, out_dtype;
+    int32_t batch, total, hkv, head_dim;
+} fa_kv_read_params;
+
+FA_API fa_status fa_kv_read_paged(const fa_kv_read_params *p, const fa_kv_pages *pages, fa_stream_t stream);
+
+/*
+ * fa_page_select -- choose, for one query per sequence and KV head, the cache
+ * pages worth attending to.  Page p of sequence b (n_b = ceil(L_b /
+ * page_size) pages) has for KV head g the score
+ *   max over the group's query heads h of  sum_d max(q_hd lo_d, q_hd hi_d),
+ * an upper bound of the unscaled q . k over the page's keys, with lo and hi
+ * the page's key_bounds; the sum is taken to far more than fp32's precision
+ * and rounded to fp32 once.  The first n_first and the last n_recent pages
+ * are always kept, the rest of top_k goes to the highest scores, the lower
+ * page number first where scores are equal.
+ *   q         [batch*hq, head_dim] bf16 (a decode step's queries)
+ *   key_bounds  bf16 [num_pages, hkv, 2, head_dim] (fa_kv_append_rope_paged)
+ *   cache_seqlens device int32 [batch]; a length outside [0, capacity] is
+ *             clamped and reported by fa_check_device_error as FA_ERR_INVALID
+ *   selected  device int32 [batch, hkv, top_k] out: the chosen logical page
+ *             numbers, ascending, then -1 where n_b < top_k
+ *   workspace device, >= fa_page_select_workspace_size() bytes, 16-byte
+ *             aligned, contents need no initialisation
+ * Bounds or queries that are not finite give an unspecified choice (of pages
+ * of the sequence).  A page id outside the pool is scored as page 0 and
+ * reported as FA_ERR_INVALID.  head_dim a multiple of 16 up to 256; any hq /
+ * hkv; 1 <= top_k <= 4096, n_first + n_recent <= top_k; max_pages <= 65536.
+ */
+typedef struct {
+    const void *q;
+    const void *key_bounds;
+    const int32_t *cache_seqlens;
+    int32_t *selected;
+    int32_t batch, hq, hkv, head_dim;
+    int32_t top_k, n_first, n_recent;
+    void *workspace;
+    size_t workspace_bytes;
+} fa_page_select_params;
+
+FA_API size_t fa_page_select_workspace_size(int32_t batch, int32_t hkv, int32_t max_pages);
+FA_API fa_status fa_page_select(const fa_page_select_params *p, const fa_kv_pages *pages, fa_stream_t stream);
+
+/*
+ * fa_attention_decode_selected -- fa_attention_decode_paged (FA_I8, FA_BF16
+ * or FA_I4 pools) over chosen pages only: KV head g of sequence b attends to
+ * the keys j < L_b that lie in the logical pages selected[b][g][0 .. top_k-1].
+ *   selected  device int32 [batch, hkv, top_k] (fa_page_select's, or a
+ *             caller's own): entry i < min(top_k, ceil(L_b / page_size))
+ *             counts; one outside [0, ceil(L_b / page_size)), such as -1,
+ *             stands for no key; a page named twice counts twice
+ * A query head without any key gets the epilogue of 0.  p->window must be 0;
+ * p->split_keys and p->max_seqlen are not used; workspace as
+ * fa_attention_decode_paged's.
+ */
+FA_API fa_status fa_attention_decode_selected(const fa_decode_params *p, const fa_kv_pages *pages,
+                                              const int32_t *selected, int32_t top_k, fa_stream_t stream);
 
 /*
  * fa_attention_decode_noalloc -- fa_attention_decode for callers that cannot
