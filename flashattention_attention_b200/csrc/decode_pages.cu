@@ -1,194 +1,953 @@
 // decode_pages.cu -- single-query attention over page pools: every page of a
 // 4-bit cache, or the chosen pages of a bf16, int8 or 4-bit one.
 //
-// One warp takes every 4th key of a split of one (sequence, KV head), a lane
-// holding D / 32 channels of the key and of each query head's output; the
-// warps' and splits' softmax states (m, l, O) are merged by a second kernel.
+// The 32-key tiles of all (sequence, KV head) segments are laid end to end and
+// a grid of P warps ("workers") takes equal contiguous ranges of them.  A
+// worker looks up its next 32 tiles at a time, one lane a tile (page list,
+// block table), and keeps a ring of tiles in flight in its own shared memory.
+// Per tile, keys on the M side of mma.sync m16n8k16 and heads on N:
+//   S^T[32 keys x 8 heads] = K[32 x d] . Q^T,  online softmax per head in fp32,
+//   O^T[d x 8 heads] += V^T[d x 32] . P'
+// A segment that lies within one worker's range is normalised and stored at
+// once; one that is split leaves a record (m, l, O) per worker, which a second
+// kernel merges (launched early, it waits for the first one's end).
+//
+// 4-bit rows (value = code * step + offset): codes enter the MMA as the exact
+// fp16 numbers code - 8, so with c = offset + 8 step
+//   q . k = step (q . (code - 8)) + c sum(q),
+//   sum_j p_j v_j = sum_j (p_j step_j) (code_j - 8) + sum_j p_j c_j
+// where the second terms stay in fp32.  p_j step_j is rounded to fp16 after
+// division by the power of two below the largest step seen so far (rescaled
+// like the running maximum), so no step is too small or too large for fp16.
+// int8 rows: the same with c = 0.  A word of eight codes holds channels 0 .. 7
+// of its four bytes: the low halves of bytes 0 and 2 are channels 0 and 4, so
+// one LOP3 and one exact subtraction widen two channels, in an order that Q's
+// fragments (and the output's addresses) follow.
+#include <atomic>
+#include <type_traits>
+
+#include "decode_mma.cuh"
 #include "internal.h"
 
 namespace fa {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxBatch = 256;  // sequences per launch (their tile prefix is in shared memory)
 
-struct PageDecodeArgs {
+// Division of 0 <= x < 2^31 by a number known on the host: x / d =
+// (x * mul) >> (32 + shift) with mul = ceil(2^(32 + shift) / d), 2^shift >= d
+// (mul has up to 33 bits; its low 32 are kept and x is added back).
+struct FastDiv {
+  uint32_t d, mul, shift;
+  static FastDiv of(uint32_t d) {
+    FastDiv f{d, 0, 0};
+    while ((uint64_t(1) << f.shift) < d) ++f.shift;
+    f.mul = static_cast<uint32_t>(((uint64_t(1) << 32) * ((uint64_t(1) << f.shift) - d)) / d + 1);
+    return f;
+  }
+  __device__ __forceinline__ int div(int x) const {
+    const uint32_t u = static_cast<uint32_t>(x);
+    return static_cast<int>((static_cast<uint64_t>(__umulhi(u, mul)) + u) >> shift);
+  }
+};
+
+struct PageArgs {
   const __nv_bfloat16* q;
-  const void* k_cache;
-  const void* v_cache;
+  const uint8_t* k_cache;  // 4-bit pools (the others come through tensor maps)
+  const uint8_t* v_cache;
   const float* k_scales;
   const float* v_scales;
   const int32_t* seqlens;
-  const int32_t* selected;  // null: every page
+  const int32_t* selected;  // [batch][hkv_real][top_k]
   int top_k;
   const int32_t* block_table;
-  int max_pages, page_size, num_pages;
-  int64_t capacity;
-  float* part;  // [batch*hq][splits][D + 2]
+  int max_pages, page_size, num_pages, capacity;
+  // for the merge kernel: tile prefix [batch + 1], and per segment with tiles
+  // its first worker << 16 | its number of workers
+  int32_t* prefix;
+  uint32_t* range;
+  float* rec_o;     // [batch*hkv + P][group][D]
+  float* rec_ml;    // [batch*hkv + P][group][2]
   __nv_bfloat16* out;
-  int batch, hq, hkv, group, hkv_real, kv_split, splits, window;
+  // a group of more than 8 query heads runs as kv_split passes over its KV
+  // head: hkv counts these virtual heads, each serving `group` query heads
+  int batch, hq, hkv, group, hkv_real, kv_split, window;
+  int n_workers;
+  FastDiv by_hkv, by_split, by_page, by_page_tiles, by_group;
   float scale_log2;
   Epilogue epi;
   Watchdog wd;
 };
 
 template <int D, int kKind>
-__device__ __forceinline__ void load_key(const void* pool, const float* scales, int64_t row, int lane,
-                                         float (&x)[D / 32]) {
-  constexpr int E = D / 32;
-  if constexpr (kKind == FA_BF16) {
-    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(pool) + row * D + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = __bfloat162float(p[e]);
-  } else if constexpr (kKind == FA_I8) {
-    const int8_t* p = static_cast<const int8_t*>(pool) + row * D + lane * E;
-    const float s = scales[row];
-#pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = static_cast<float>(p[e]) * s;
+struct Tile {
+  using G = Geom<D, kKind == FA_BF16>;
+  static constexpr bool kI4 = kKind == FA_I4;
+  static constexpr int kBytes = kI4 ? kTile * D / 2 : G::kTileBytes;  // of K, and of V
+  static constexpr int kScaleBytes = kI4 ? kTile * 8 : kKind == FA_I8 ? kTile * 4 : 0;
+  static constexpr int kScaleOff = 2 * kBytes;
+  static constexpr int kStageBytes = kI4 ? kScaleOff + 2 * kScaleBytes : G::kStageBytes;
+  static constexpr int kStages = kKind == FA_BF16 && D == 256 ? 1 : 3;
+  static constexpr int kRing = kWarps * kStages * kStageBytes;
+  static constexpr int kSmem = kRing + (kI4 ? 128 : 1024) /*align*/ + kWarps * kStages * 8;
+  static constexpr int kFit = 233472 / (kSmem + (kMaxBatch + 1) * 4 + 1024);
+  // registers: 128 per thread with four CTAs per SM; 8 * D / 16 accumulators
+  // of O at D = 256 need more
+  static constexpr int kMost = D == 256 ? 2 : 4;
+  static constexpr int kCtas = kFit < 1 ? 1 : (kFit < kMost ? kFit : kMost);
+};
+
+__device__ __forceinline__ int pages_in(const PageArgs& A, int L) { return L > 0 ? A.by_page.div(L - 1) + 1 : 0; }
+
+// T tiles over P <= T workers: the first T % P take one more than the others.
+struct Split {
+  int each, more;
+  __device__ __forceinline__ Split(int T, int P) : each(T / P), more(T - T / P * P) {}
+  __device__ __forceinline__ int begin(int w) const { return w * each + min(w, more); }
+  __device__ __forceinline__ int worker_of(int x) const {
+    const int y = x - more * (each + 1);
+    return y < 0 ? x / (each + 1) : more + y / each;
+  }
+};
+// Tiles of a segment of sequence length L.
+template <bool kSel>
+__device__ __forceinline__ int tiles_in(const PageArgs& A, int L) {
+  if constexpr (kSel) return min(A.top_k, pages_in(A, L)) * static_cast<int>(A.by_page_tiles.d);
+  const int k_lo = A.window > 0 ? max(0, L - A.window) : 0;
+  return L > 0 ? (L + kTile - 1) / kTile - k_lo / kTile : 0;
+}
+__device__ __forceinline__ int length_of(const PageArgs& A, int b) { return max(0, min(A.seqlens[b], A.capacity)); }
+
+struct TileInfo {
+  int seg;   // b * hkv + g
+  int key0;  // first key's position
+  int row;   // its row in the pools, -1: no key of the tile counts
+};
+
+template <bool kSel>
+__device__ __forceinline__ TileInfo tile_info(const PageArgs& A, const int32_t* pre, int x) {
+  int lo = 0, hi = A.batch - 1;  // the last b with pre[b] <= x
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  const int b = lo, Tb = A.by_hkv.div(pre[b + 1] - pre[b]), y = x - pre[b];
+  const int g = y / Tb, t = y - g * Tb, gr = A.by_split.div(g);
+  const int L = length_of(A, b);
+  TileInfo r;
+  r.seg = b * A.hkv + g;
+  int lp, off;
+  if constexpr (kSel) {
+    const int i = A.by_page_tiles.div(t);
+    off = (t - i * A.by_page_tiles.d) * kTile;
+    lp = A.selected[(static_cast<int64_t>(b) * A.hkv_real + gr) * A.top_k + i];
+    if (lp < 0 || lp >= pages_in(A, L) || lp * A.page_size + off >= L) {
+      r.key0 = 0;
+      r.row = -1;
+      return r;
+    }
+    r.key0 = lp * A.page_size + off;
   } else {
-    const uint8_t* p = static_cast<const uint8_t*>(pool) + row * (D / 2);
-    const float s = scales[2 * row], o = scales[2 * row + 1];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int c = lane * E + e;
-      x[e] = static_cast<float>((p[c >> 1] >> (4 * (c & 1))) & 15) * s + o;
-    }
+    const int k_lo = A.window > 0 ? max(0, L - A.window) : 0;
+    r.key0 = (k_lo / kTile + t) * kTile;
+    lp = A.by_page.div(r.key0);
+    off = r.key0 - lp * A.page_size;
   }
+  int pg = A.block_table[static_cast<int64_t>(b) * A.max_pages + lp];
+  if (pg < 0 || pg >= A.num_pages) {  // reported; page 0 keeps the loads inside the pool
+    record_status(A.wd, kStatusRange);
+    pg = 0;
+  }
+  r.row = (pg * A.hkv_real + gr) * A.page_size + off;
+  return r;
 }
 
-template <int D, int kKind>
-__global__ void __launch_bounds__(kWarps * 32) decode_pages_kernel(const PageDecodeArgs A) {
-  constexpr int E = D / 32, kG = 8;
-  __shared__ float s_o[kWarps][kG][D];
-  __shared__ float s_ml[kWarps][kG][2];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int seg = blockIdx.x, split = blockIdx.y, b = seg / A.hkv, g = seg % A.hkv, gr = g / A.kv_split;
-  const int64_t Lr = A.seqlens[b];
-  const int64_t L = Lr < 0 ? 0 : (Lr > A.capacity ? A.capacity : Lr);
-  if (L != Lr && threadIdx.x == 0) record_status(A.wd, kStatusRange);
-  const int n_pages = static_cast<int>((L + A.page_size - 1) / A.page_size);
-  const int64_t lo = A.window > 0 && L > A.window ? L - A.window : 0;
-  const int64_t first = A.selected != nullptr ? 0 : lo;
-  const int64_t last =
-      A.selected != nullptr ? static_cast<int64_t>(min(A.top_k, n_pages)) * A.page_size : L;
-  const int64_t n = last - first;
-  const int64_t k0 = first + n * split / A.splits, k1 = first + n * (split + 1) / A.splits;
-  float q[kG][E], o[kG][E], m[kG], l[kG];
-#pragma unroll
-  for (int h = 0; h < kG; ++h) {
-    m[h] = -INFINITY;
-    l[h] = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      o[h][e] = 0.f;
-      q[h][e] = h < A.group ? __bfloat162float(A.q[(static_cast<int64_t>(b) * A.hq + g * A.group + h) * D + lane * E + e])
-                            : 0.f;
-    }
+// S row r of a 16-key half is key key_of(r) of it: for packed rows of 64 bytes
+// the K loads of rows (2i, 2i + 1) then fall on different banks, and so do half
+// of the V loads of a thread quad.
+template <int kKind>
+__device__ __forceinline__ int key_of(int r) {
+  return kKind == FA_I4 ? r ^ ((r >> 1) & 1) : r;
+}
+
+template <int D, int kKind, bool kSel>
+__global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
+    decode_pages_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                        const __grid_constant__ CUtensorMap tm_k32, const __grid_constant__ CUtensorMap tm_v32,
+                        const PageArgs A) {
+  using TL = Tile<D, kKind>;
+  using G = Geom<D, kKind == FA_BF16>;
+  constexpr bool kBF = kKind == FA_BF16, kI4 = kKind == FA_I4, kI8 = kKind == FA_I8;
+  constexpr int kStages = TL::kStages;
+  constexpr int kSteps = D / 16;  // k-steps of S
+  constexpr int kMT = D / 16;     // m-tiles of O^T
+  constexpr int kUnroll = 1;      // 16-key halves of a tile in a row in the code
+  constexpr bool kQuarter = D == 64 || D == 128;  // int8: see decode.cu
+  extern __shared__ uint8_t page_smem_raw[];
+  constexpr uintptr_t kAlign = kI4 ? 128 : 1024;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(page_smem_raw) + kAlign - 1) & ~(kAlign - 1));
+  uint64_t* all_bars = reinterpret_cast<uint64_t*>(smem + TL::kRing);
+  int32_t* pre = reinterpret_cast<int32_t*>(all_bars + kWarps * kStages);
+  __shared__ int32_t warp_sums[kWarps];
+
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gq = lane >> 2, qq = lane & 3;
+  uint64_t* bars = all_bars + warp * kStages;
+  if (lane == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(&bars[s], 1);
+    fence_barrier_init();
   }
-  for (int64_t v = k0 + warp; v < k1; v += kWarps) {
-    int64_t key = v;
-    if (A.selected != nullptr) {
-      const int lp = A.selected[(static_cast<int64_t>(b) * A.hkv_real + gr) * A.top_k + v / A.page_size];
-      if (lp < 0 || lp >= n_pages) continue;
-      key = static_cast<int64_t>(lp) * A.page_size + v % A.page_size;
-      if (key >= L) continue;
+  // tile prefix over the sequences
+  {
+    const int per = (A.batch + kThreads - 1) / kThreads;
+    const int b0 = min(A.batch, static_cast<int>(threadIdx.x) * per), b1 = min(A.batch, b0 + per);
+    int own = 0;
+    for (int b = b0; b < b1; ++b) {
+      const int L = A.seqlens[b];
+      if ((L < 0 || L > A.capacity) && blockIdx.x == 0) record_status(A.wd, kStatusRange);
+      own += tiles_in<kSel>(A, length_of(A, b)) * A.hkv;
     }
-    int pg = A.block_table[static_cast<int64_t>(b) * A.max_pages + key / A.page_size];
-    if (pg < 0 || pg >= A.num_pages) {
-      if (lane == 0) record_status(A.wd, kStatusRange);
-      pg = 0;
+    int incl = own;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += v;
     }
-    const int64_t row = (static_cast<int64_t>(pg) * A.hkv_real + gr) * A.page_size + key % A.page_size;
-    float kx[E], vx[E];
-    load_key<D, kKind>(A.k_cache, A.k_scales, row, lane, kx);
-    load_key<D, kKind>(A.v_cache, A.v_scales, row, lane, vx);
-#pragma unroll
-    for (int h = 0; h < kG; ++h) {
-      if (h >= A.group) break;
-      float s = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) s = fmaf(q[h][e], kx[e], s);
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-      s *= A.scale_log2;
-      const float mn = fmaxf(m[h], s);
-      const float a = exp2f(m[h] - mn), p = exp2f(s - mn);
-      m[h] = mn;
-      l[h] = l[h] * a + p;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[h][e] = o[h][e] * a + p * vx[e];
+    if (lane == 31) warp_sums[warp] = incl;
+    __syncthreads();
+    int at = incl - own;
+    for (int v = 0; v < warp; ++v) at += warp_sums[v];
+    for (int b = b0; b < b1; ++b) {
+      pre[b] = at;
+      if (blockIdx.x == 0) A.prefix[b] = at;
+      at += tiles_in<kSel>(A, length_of(A, b)) * A.hkv;
     }
+    if (threadIdx.x == 0) {
+      int total = 0;
+      for (int v = 0; v < kWarps; ++v) total += warp_sums[v];
+      pre[A.batch] = total;
+      if (blockIdx.x == 0) A.prefix[A.batch] = total;
+    }
+    __syncthreads();
   }
-#pragma unroll
-  for (int h = 0; h < kG; ++h) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) s_o[warp][h][lane * E + e] = o[h][e];
+  const int T = pre[A.batch], P = min(A.n_workers, T);
+  const int w = static_cast<int>(blockIdx.x) * kWarps + warp;
+  if (w >= P) return;
+  const Split split(T, P);
+  const int t_first = split.begin(w);
+  const int my_tiles = split.begin(w + 1) - t_first;
+
+  auto stage_ptr = [&](int s) { return smem + (warp * kStages + s) * TL::kStageBytes; };
+  auto info_of = [&](int block) {
+    TileInfo r{0, 0, -1};
+    if (block * 32 + lane < my_tiles) r = tile_info<kSel>(A, pre, t_first + block * 32 + lane);
+    return r;
+  };
+  TileInfo cur = info_of(0), nxt{0, 0, -1};
+  // 4 bits: lane j < 4 copies the K codes, V codes, K or V scales of a tile
+  const bool scales = lane & 2, of_v = lane & 1;
+  const uint8_t* src = scales ? reinterpret_cast<const uint8_t*>(of_v ? A.v_scales : A.k_scales)
+                              : (of_v ? A.v_cache : A.k_cache);
+  const int src_row = scales ? 8 : D / 2;
+  const uint32_t src_bytes = scales ? TL::kScaleBytes : TL::kBytes;
+  const uint32_t dst = scales ? TL::kScaleOff + (of_v ? TL::kScaleBytes : 0) : (of_v ? TL::kBytes : 0);
+  // tile i's loads into its stage s; i is less than 32 past the block `block`
+  auto issue = [&](int i, int s, int block) {
+    if (i >= my_tiles) return;
+    const int row = __shfl_sync(0xffffffffu, (i >> 5) == block ? cur.row : nxt.row, i & 31);
+    uint64_t* bar = &bars[s];
+    uint8_t* st = stage_ptr(s);
     if (lane == 0) {
-      s_ml[warp][h][0] = m[h];
-      s_ml[warp][h][1] = l[h];
+      if (row < 0) {
+        mbar_arrive(bar);
+      } else {
+        mbar_expect_tx(bar, 2 * TL::kBytes + 2 * TL::kScaleBytes);
+      }
+    }
+    if (row < 0) return;
+    if constexpr (kI4) {
+      __syncwarp();
+      if (lane < 4) bulk_load(st + dst, src + static_cast<int64_t>(row) * src_row, src_bytes, bar);
+      return;
+    }
+    if (lane != 0) return;
+    if constexpr (kI8) {
+#pragma unroll
+      for (int h = 0; h < G::kHalves; ++h) {
+        tma_load_2d(st + h * kTile * G::kRowBytes, &tm_k, bar, G::kRowBytes * h, row);
+        tma_load_2d(st + TL::kBytes + h * kTile * G::kRowBytes, &tm_v, bar, G::kRowBytes * h, row);
+      }
+      bulk_load(st + TL::kScaleOff, A.k_scales + row, TL::kScaleBytes, bar);
+      bulk_load(st + TL::kScaleOff + TL::kScaleBytes, A.v_scales + row, TL::kScaleBytes, bar);
+    } else if constexpr (kBF) {
+#pragma unroll
+      for (int c = 0; c < G::kNFull; ++c) {
+        tma_load_2d(st + c * G::kChunkBytes, &tm_k, bar, 64 * c, row);
+        tma_load_2d(st + TL::kBytes + c * G::kChunkBytes, &tm_v, bar, 64 * c, row);
+      }
+      if constexpr (G::kTail) {
+        tma_load_2d(st + G::kNFull * G::kChunkBytes, &tm_k32, bar, 64 * G::kNFull, row);
+        tma_load_2d(st + TL::kBytes + G::kNFull * G::kChunkBytes, &tm_v32, bar, 64 * G::kNFull, row);
+      }
+    }
+  };
+  for (int i = 0; i < kStages; ++i) issue(i, i, 0);
+  nxt = info_of(1);
+
+  // ---- per-segment state
+  uint32_t qb0[kSteps], qb1[kSteps];
+  float qs0 = 0.f, qs1 = 0.f;  // logit multipliers of heads 2qq, 2qq + 1
+  float qm0 = 0.f, qm1 = 0.f;  // 4 bits: scale * sum of q
+  float o[kMT][4];
+  float m_run[2], l_run[2];
+  float om[2];        // 4 bits: sum of p * (offset + 8 step)
+  float cap = 0.f;    // quantised: power of two below the largest V step so far
+  auto reset = [&]() {
+#pragma unroll
+    for (int m = 0; m < kMT; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
+    m_run[0] = m_run[1] = -INFINITY;
+    l_run[0] = l_run[1] = om[0] = om[1] = 0.f;
+    cap = 0.f;
+  };
+  auto load_q = [&](int b, int g) {
+    const bool head_ok = gq < A.group;
+    const __nv_bfloat16* row = A.q + (static_cast<int64_t>(b) * A.hq + g * A.group + gq) * D;
+    if constexpr (kBF) {
+      const uint32_t* qw = reinterpret_cast<const uint32_t*>(row);
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks) {
+        qb0[ks] = head_ok ? qw[8 * ks + qq] : 0u;
+        qb1[ks] = head_ok ? qw[8 * ks + 4 + qq] : 0u;
+      }
+      qs0 = qs1 = A.scale_log2;
+      return;
+    }
+    // thread (head gq, quarter qq): a quarter of the channels, in the order of
+    // its K words, as fp16 after a power of two that brings the largest |q| to
+    // [2^14, 2^15) (exact for all that fp32 sums could tell apart)
+    float qv[D / 4];
+    float amax = 0.f, sum = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      uint4 raw = make_uint4(0, 0, 0, 0);
+      const int dim0 = kI4 || kQuarter ? qq * (D / 4) + 8 * c : 32 * c + 8 * qq;
+      if (head_ok) raw = *reinterpret_cast<const uint4*>(row + dim0);
+      const uint32_t wv[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        qv[8 * c + 2 * e] = __uint_as_float(wv[e] << 16);
+        qv[8 * c + 2 * e + 1] = __uint_as_float(wv[e] & 0xffff0000u);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < D / 4; ++e) {
+      amax = fmaxf(amax, fabsf(qv[e]));
+      sum += qv[e];
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    // the power of two from amax's exponent bits, kept where it and its inverse are normal
+    const int ex = min(max(static_cast<int>(__float_as_uint(amax) >> 23), 15), 254);
+    const float up = __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);  // 2^(14 - (ex - 127))
+    const float qs_own = A.scale_log2 * __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
+    const float qm_own = A.scale_log2 * sum;
+#pragma unroll
+    for (int ks = 0; ks < kSteps; ++ks) {
+      // channels of the k-step's fragments: see i4x2_* and i8x2_*
+      const int c0 = kI4 ? 8 * (ks / 2) + 2 * (ks % 2) : 4 * ks, far = kI4 ? 4 : 2;
+      qb0[ks] = pack_f16x2(qv[c0] * up, qv[c0 + far] * up);
+      qb1[ks] = pack_f16x2(qv[c0 + 1] * up, qv[c0 + far + 1] * up);
+    }
+    qs0 = __shfl_sync(0xffffffffu, qs_own, (2 * qq) * 4);
+    qs1 = __shfl_sync(0xffffffffu, qs_own, (2 * qq + 1) * 4);
+    qm0 = __shfl_sync(0xffffffffu, qm_own, (2 * qq) * 4);
+    qm1 = __shfl_sync(0xffffffffu, qm_own, (2 * qq + 1) * 4);
+  };
+  // First channel of the run of consecutive ones that o[mi][j], o[mi][j + 2]
+  // (and, for 4 bits, the same of m-tile mi + 1) hold.
+  auto dim_of = [&](int mi) {
+    if constexpr (kBF) return 16 * mi + gq;
+    if constexpr (kI8) return 4 * (8 * (mi / 2) + gq) + 2 * (mi % 2);
+    return 4 * (gq * (D / 32) + mi / 2) + 2 * (mi % 2);
+  };
+  // The segment's state: the output rows where this worker saw all of it, else
+  // its record (segment + worker).
+  auto finish = [&](int seg, bool whole) {
+    float l0 = l_run[0], l1 = l_run[1], m0 = om[0], m1 = om[1];
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, off);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, off);
+      if constexpr (kI4) {
+        m0 += __shfl_xor_sync(0xffffffffu, m0, off);
+        m1 += __shfl_xor_sync(0xffffffffu, m1, off);
+      }
+    }
+    const float unit = kBF ? 1.f : cap;
+    const int64_t rec = static_cast<int64_t>(seg) + w;
+    const int b = A.by_hkv.div(seg), g = seg - b * A.hkv;
+#pragma unroll 1
+    for (int j = 0; j < 2; ++j) {
+      const int h = 2 * qq + j;
+      if (h >= A.group) break;
+      const float add = j ? m1 : m0, l = j ? l1 : l0;
+      float y[2 * kMT];
+#pragma unroll
+      for (int mi = 0; mi < kMT; ++mi) {
+        y[2 * mi] = fmaf(j ? o[mi][1] : o[mi][0], unit, add);
+        y[2 * mi + 1] = fmaf(j ? o[mi][3] : o[mi][2], unit, add);
+      }
+      if (!whole) {
+        if (gq == 0)
+          *reinterpret_cast<float2*>(A.rec_ml + (rec * A.group + h) * 2) = make_float2(j ? m_run[1] : m_run[0], l);
+        float* ro = A.rec_o + (rec * A.group + h) * D;
+#pragma unroll
+        for (int mi = 0; mi < kMT; ++mi) {
+          if constexpr (kBF) {
+            ro[dim_of(mi)] = y[2 * mi];
+            ro[dim_of(mi) + 8] = y[2 * mi + 1];
+          } else {
+            *reinterpret_cast<float2*>(ro + dim_of(mi)) = make_float2(y[2 * mi], y[2 * mi + 1]);
+          }
+        }
+      } else {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+        for (int mi = 0; mi < 2 * kMT; ++mi) y[mi] *= inv;
+        apply_epilogue_vec(y, A.epi);
+        __nv_bfloat16* oo = A.out + (static_cast<int64_t>(b) * A.hq + g * A.group + h) * D;
+#pragma unroll
+        for (int mi = 0; mi < kMT; ++mi) {
+          if constexpr (kBF) {
+            oo[dim_of(mi)] = __float2bfloat16_rn(y[2 * mi]);
+            oo[dim_of(mi) + 8] = __float2bfloat16_rn(y[2 * mi + 1]);
+          } else {
+            *reinterpret_cast<uint32_t*>(oo + dim_of(mi)) = pack_bf16x2(y[2 * mi], y[2 * mi + 1]);
+          }
+        }
+      }
+    }
+  };
+
+  int seg = 0, left = 0, key_end = 0, k_lo = 0;  // left: tiles until this worker leaves the segment
+  bool whole = false;
+  int s = 0;
+  uint32_t parity = 0;
+#pragma unroll 1
+  for (int i = 0; i < my_tiles; ++i) {
+    if ((i & 31) == 0 && i > 0) {
+      cur = nxt;
+      nxt = info_of((i >> 5) + 1);
+    }
+    if (left == 0) {
+      seg = __shfl_sync(0xffffffffu, cur.seg, i & 31);
+      const int b = A.by_hkv.div(seg), g = seg - b * A.hkv, Tb = A.by_hkv.div(pre[b + 1] - pre[b]);
+      reset();
+      load_q(b, g);
+      const int done = t_first + i - (pre[b] + g * Tb);  // tiles of the segment before this worker's first
+      left = min(Tb - done, my_tiles - i);
+      whole = left == Tb;
+      if (done == 0 && lane == 0) {
+        const int n = split.worker_of(pre[b] + g * Tb + Tb - 1) - w + 1;
+        A.range[seg] = static_cast<uint32_t>(w) << 16 | static_cast<uint32_t>(n);
+      }
+      key_end = length_of(A, b);
+      k_lo = !kSel && A.window > 0 ? max(0, key_end - A.window) : 0;
+    }
+    const int key0 = __shfl_sync(0xffffffffu, cur.key0, i & 31);
+    const bool any = !kSel || __shfl_sync(0xffffffffu, cur.row, i & 31) >= 0;
+    // every lane polls; whether to go on is a decision of the whole warp
+    const bool ready = wait_parity(&bars[s], parity, A.wd);
+    if (!__all_sync(0xffffffffu, ready)) break;
+    if (any) {
+      const uint32_t kt = smem_u32(stage_ptr(s));
+      const uint32_t vt = kt + TL::kBytes;
+      const float* ksc = reinterpret_cast<const float*>(stage_ptr(s) + TL::kScaleOff);
+      const float* vsc = ksc + TL::kScaleBytes / 4;
+
+      // ---- S^T = K . Q^T
+      float sc[2][4];
+#pragma unroll kUnroll
+      for (int mt = 0; mt < 2; ++mt) {
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (kBF) {
+          const int mi = lane >> 3, mr = lane & 7;
+#pragma unroll
+          for (int ks = 0; ks < kSteps; ++ks) {
+            uint32_t a[4];
+            ldsm_x4(bf_addr<D>(kt, 16 * mt + 8 * (mi % 2) + mr, 16 * ks + 8 * (mi / 2)), a);
+            mma16816_bf16(acc, a, qb0[ks], qb1[ks]);
+          }
+        } else {
+          const int r0 = 16 * mt + key_of<kKind>(gq), r1 = r0 + 8;
+          constexpr int kWords = kI4 ? D / 32 : D / 16;  // of 4 bytes per thread and row
+          uint32_t wa[kWords], wb[kWords];
+          if constexpr (kI4) {
+            const uint32_t a0 = kt + r0 * (D / 2) + qq * (D / 8), a1 = a0 + 8 * (D / 2);
+            if constexpr (kWords % 4 == 0) {
+#pragma unroll
+              for (int c = 0; c < kWords / 4; ++c) {
+                const uint4 x = lds128(a0 + 16 * c), y = lds128(a1 + 16 * c);
+                wa[4 * c] = x.x; wa[4 * c + 1] = x.y; wa[4 * c + 2] = x.z; wa[4 * c + 3] = x.w;
+                wb[4 * c] = y.x; wb[4 * c + 1] = y.y; wb[4 * c + 2] = y.z; wb[4 * c + 3] = y.w;
+              }
+            } else if constexpr (kWords == 2) {
+              const uint2 x = lds64(a0), y = lds64(a1);
+              wa[0] = x.x; wa[1] = x.y;
+              wb[0] = y.x; wb[1] = y.y;
+            } else {
+#pragma unroll
+              for (int c = 0; c < kWords; ++c) {
+                wa[c] = lds32(a0 + 4 * c);
+                wb[c] = lds32(a1 + 4 * c);
+              }
+            }
+#pragma unroll
+            for (int c = 0; c < kWords; ++c) {
+              const uint32_t x = wa[c], y = wb[c];
+              mma16816(acc, i4x2_low(x), i4x2_low(y), i4x2_high(x), i4x2_high(y), qb0[2 * c], qb1[2 * c]);
+              mma16816(acc, i4x2_low(x >> 8), i4x2_low(y >> 8), i4x2_high(x >> 8), i4x2_high(y >> 8), qb0[2 * c + 1],
+                       qb1[2 * c + 1]);
+            }
+          } else {
+            if constexpr (kQuarter) {
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c) {
+                const uint32_t off = (qq * (D / 64) + c) * 16;
+                const uint4 x = lds128(kt + swz<D, false>(r0 * D + off)), y = lds128(kt + swz<D, false>(r1 * D + off));
+                wa[4 * c] = x.x; wa[4 * c + 1] = x.y; wa[4 * c + 2] = x.z; wa[4 * c + 3] = x.w;
+                wb[4 * c] = y.x; wb[4 * c + 1] = y.y; wb[4 * c + 2] = y.z; wb[4 * c + 3] = y.w;
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                const uint2 x = lds64(kt + i8_off<D>(r0, 32 * c + 8 * qq)), y = lds64(kt + i8_off<D>(r1, 32 * c + 8 * qq));
+                wa[2 * c] = x.x; wa[2 * c + 1] = x.y;
+                wb[2 * c] = y.x; wb[2 * c + 1] = y.y;
+              }
+            }
+#pragma unroll
+            for (int ks = 0; ks < kSteps; ++ks)
+              mma16816(acc, i8x2_to_f16x2_even(wa[ks]), i8x2_to_f16x2_even(wb[ks]), i8x2_to_f16x2_odd(wa[ks]),
+                       i8x2_to_f16x2_odd(wb[ks]), qb0[ks], qb1[ks]);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (mt == 0) {
+            sc[0][e] = acc[e];
+          } else {
+            sc[1][e] = acc[e];
+          }
+        }
+      }
+
+      // ---- online softmax per head; positions are looked at only in tiles
+      // that reach past [k_lo, key_end)
+      uint32_t pb[2][2];
+      auto softmax = [&](auto masked_tag) {
+        constexpr bool kMasked = decltype(masked_tag)::value;
+        float x[2][4];
+        [[maybe_unused]] float vs[2][2], vc[2][2];  // quantised: V step, 4 bits: offset + 8 step
+        float mx0 = -INFINITY, mx1 = -INFINITY;
+        [[maybe_unused]] float top = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const int kl = 16 * mt + 8 * hf + key_of<kKind>(gq);
+            const bool ok = !kMasked || (key0 + kl >= k_lo && key0 + kl < key_end);
+            float x0, x1;
+            if constexpr (kI4) {
+              const float2 ss = *reinterpret_cast<const float2*>(ksc + 2 * kl);
+              const float2 sv = *reinterpret_cast<const float2*>(vsc + 2 * kl);
+              const float c = fmaf(8.f, ss.x, ss.y);
+              x0 = fmaf(sc[mt][2 * hf], ss.x * qs0, c * qm0);
+              x1 = fmaf(sc[mt][2 * hf + 1], ss.x * qs1, c * qm1);
+              vs[mt][hf] = ok ? sv.x : 0.f;
+              vc[mt][hf] = ok ? fmaf(8.f, sv.x, sv.y) : 0.f;
+              top = fmaxf(top, vs[mt][hf]);
+            } else if constexpr (kI8) {
+              const float s = ksc[kl];
+              x0 = sc[mt][2 * hf] * (s * qs0);
+              x1 = sc[mt][2 * hf + 1] * (s * qs1);
+              vs[mt][hf] = ok ? vsc[kl] : 0.f;
+              top = fmaxf(top, vs[mt][hf]);
+            } else {
+              x0 = sc[mt][2 * hf] * qs0;
+              x1 = sc[mt][2 * hf + 1] * qs1;
+            }
+            x[mt][2 * hf] = ok ? x0 : -INFINITY;
+            x[mt][2 * hf + 1] = ok ? x1 : -INFINITY;
+            mx0 = fmaxf(mx0, x[mt][2 * hf]);
+            mx1 = fmaxf(mx1, x[mt][2 * hf + 1]);
+          }
+        }
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
+          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
+        }
+        // the running maxima and the V unit move only when a tile raises them,
+        // and O is rescaled only when one of them moved
+        bool up = mx0 > m_run[0] || mx1 > m_run[1];
+        if constexpr (!kBF) up |= top >= 2.f * cap && top > 0.f;
+        if (__any_sync(0xffffffffu, up)) {
+          const float mn0 = fmaxf(m_run[0], mx0), mn1 = fmaxf(m_run[1], mx1);
+          const float r0 = mn0 == -INFINITY ? 0.f : mn0, r1 = mn1 == -INFINITY ? 0.f : mn1;
+          const float al0 = ex2_approx(m_run[0] - r0), al1 = ex2_approx(m_run[1] - r1);
+          m_run[0] = mn0;
+          m_run[1] = mn1;
+          l_run[0] *= al0;
+          l_run[1] *= al1;
+          float a0 = al0, a1 = al1;
+          if constexpr (!kBF) {
+            // steps are not negative, so their bits order like the numbers
+            const unsigned bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+            const float unit = fmaxf(cap, __uint_as_float(bits & 0x7f800000u));
+            const float ratio = unit > 0.f ? cap / unit : 0.f;
+            om[0] *= al0;
+            om[1] *= al1;
+            a0 *= ratio;
+            a1 *= ratio;
+            cap = unit;
+          }
+#pragma unroll
+          for (int m = 0; m < kMT; ++m) {
+            o[m][0] *= a0; o[m][2] *= a0;
+            o[m][1] *= a1; o[m][3] *= a1;
+          }
+        }
+        const float ref0 = m_run[0] == -INFINITY ? 0.f : m_run[0];
+        const float ref1 = m_run[1] == -INFINITY ? 0.f : m_run[1];
+        [[maybe_unused]] const float to_unit = cap > 0.f ? 1.f / cap : 0.f;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          uint32_t packed[2];
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const float p0 = ex2_approx(x[mt][2 * hf] - ref0);
+            const float p1 = ex2_approx(x[mt][2 * hf + 1] - ref1);
+            l_run[0] += p0;
+            l_run[1] += p1;
+            if constexpr (kBF) {
+              packed[hf] = pack_bf16x2(p0, p1);
+            } else {
+              const float u = vs[mt][hf] * to_unit;
+              packed[hf] = pack_f16x2(p0 * u, p1 * u);
+              if constexpr (kI4) {
+                om[0] = fmaf(p0, vc[mt][hf], om[0]);
+                om[1] = fmaf(p1, vc[mt][hf], om[1]);
+              }
+            }
+          }
+          pb[mt][0] = transpose8x8(packed[0]);  // (head gq; S rows 2qq, 2qq+1)
+          pb[mt][1] = transpose8x8(packed[1]);  // (head gq; S rows 8+2qq, 8+2qq+1)
+        }
+      };
+      const bool inside = key0 >= k_lo && key0 + kTile <= key_end;
+      if (inside) {
+        softmax(std::false_type{});
+      } else {
+        softmax(std::true_type{});
+      }
+
+      // ---- O^T += V^T . P'
+      if constexpr (kBF) {
+        if (!inside) {
+          // rows outside may hold NaN or Inf: zero them (P is 0 there)
+          const int key = key0 + lane;
+          if (key < k_lo || key >= key_end) {
+#pragma unroll
+            for (int c = 0; c < D; c += 8)
+              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(bf_addr<D>(vt, lane, c)), "r"(0u) : "memory");
+            fence_proxy_async_smem();  // ordered before the copy that refills this stage
+          }
+          __syncwarp();
+        }
+        const int mi4 = lane >> 3, mr = lane & 7;
+#pragma unroll kUnroll
+        for (int mt = 0; mt < 2; ++mt) {
+          const uint32_t pf[2] = {mt ? pb[1][0] : pb[0][0], mt ? pb[1][1] : pb[0][1]};
+#pragma unroll
+          for (int mi = 0; mi < kMT; ++mi) {
+            uint32_t a[4];
+            ldsm_x4_trans(bf_addr<D>(vt, 16 * mt + 8 * (mi4 / 2) + mr, 16 * mi + 8 * (mi4 % 2)), a);
+            mma16816_bf16(o[mi], a, pf[0], pf[1]);
+          }
+        }
+      } else if constexpr (kI8) {
+#pragma unroll kUnroll
+        for (int mt = 0; mt < 2; ++mt) {
+          const uint32_t pf[2] = {mt ? pb[1][0] : pb[0][0], mt ? pb[1][1] : pb[0][1]};
+          const int kk0 = 16 * mt + 2 * qq;
+#pragma unroll
+          for (int pr = 0; pr < D / 32; ++pr) {
+            const uint32_t xw = (8 * pr + gq) * 4;
+            const uint32_t w0 = lds32(vt + i8_off<D>(kk0 + 0, xw)), w1 = lds32(vt + i8_off<D>(kk0 + 1, xw));
+            const uint32_t w2 = lds32(vt + i8_off<D>(kk0 + 8, xw)), w3 = lds32(vt + i8_off<D>(kk0 + 9, xw));
+            const uint32_t t01l = prmt(w0, w1, 0x5410), t01h = prmt(w0, w1, 0x7632);
+            const uint32_t t23l = prmt(w2, w3, 0x5410), t23h = prmt(w2, w3, 0x7632);
+            mma16816(o[2 * pr], i8x2_to_f16x2_even(t01l), i8x2_to_f16x2_odd(t01l), i8x2_to_f16x2_even(t23l),
+                     i8x2_to_f16x2_odd(t23l), pf[0], pf[1]);
+            mma16816(o[2 * pr + 1], i8x2_to_f16x2_even(t01h), i8x2_to_f16x2_odd(t01h), i8x2_to_f16x2_even(t23h),
+                     i8x2_to_f16x2_odd(t23h), pf[0], pf[1]);
+          }
+        }
+      } else {
+        // thread (gq, qq): channels [gq D/8, (gq+1) D/8) of four keys a half
+        // tile; `half` holds four channels of a key pair in its two 16-bit halves
+        constexpr int kH = D / 32;
+        auto four = [&](float (&lo)[4], float (&hi)[4], uint32_t t01, uint32_t t23, const uint32_t (&p)[2]) {
+          mma16816(lo, i4x2_low(t01), i4x2_high(t01), i4x2_low(t23), i4x2_high(t23), p[0], p[1]);
+          mma16816(hi, i4x2_low(t01 >> 8), i4x2_high(t01 >> 8), i4x2_low(t23 >> 8), i4x2_high(t23 >> 8), p[0], p[1]);
+        };
+#pragma unroll kUnroll
+        for (int mt = 0; mt < 2; ++mt) {
+          const uint32_t pf[2] = {mt ? pb[1][0] : pb[0][0], mt ? pb[1][1] : pb[0][1]};
+          const uint32_t a0 = vt + gq * (D / 16) + 16 * mt * (D / 2);
+          uint32_t at[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            at[e] = a0 + (key_of<kKind>(2 * qq + (e & 1)) + 8 * (e >> 1)) * (D / 2);
+          if constexpr (kH % 2 == 0) {
+            uint32_t wv[4][kH / 2];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if constexpr (kH == 8) {
+                const uint4 x = lds128(at[e]);
+                wv[e][0] = x.x; wv[e][1] = x.y; wv[e][2] = x.z; wv[e][3] = x.w;
+              } else if constexpr (kH == 4) {
+                const uint2 x = lds64(at[e]);
+                wv[e][0] = x.x; wv[e][1] = x.y;
+              } else {
+                wv[e][0] = lds32(at[e]);
+              }
+            }
+#pragma unroll
+            for (int c = 0; c < kH / 2; ++c) {
+              four(o[4 * c], o[4 * c + 1], prmt(wv[0][c], wv[1][c], 0x5410), prmt(wv[2][c], wv[3][c], 0x5410), pf);
+              four(o[4 * c + 2], o[4 * c + 3], prmt(wv[0][c], wv[1][c], 0x7632), prmt(wv[2][c], wv[3][c], 0x7632), pf);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < kH; ++c) {
+              uint32_t v[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint16_t hw;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(hw) : "r"(at[e] + 2 * c));
+                v[e] = hw;
+              }
+              four(o[2 * c], o[2 * c + 1], v[0] | (v[1] << 16), v[2] | (v[3] << 16), pf);
+            }
+          }
+        }
+      }
+    }
+    // the stage is free: the tile kStages on goes there
+    __syncwarp();
+    fence_proxy_async_smem();
+    issue(i + kStages, s, i >> 5);
+    if (++s == kStages) {
+      s = 0;
+      parity ^= 1;
+    }
+    if (--left == 0) finish(seg, whole);
+  }
+}
+
+// One query head's split records into its output row; the rows of segments
+// without a tile.  Four warps take every fourth record.
+constexpr int kMergeRecords = 512;  // weights held at a time
+template <int D>
+__global__ void __launch_bounds__(128) decode_pages_merge_kernel(const PageArgs A) {
+  constexpr int E = D / 32;
+  __shared__ float s_w[kMergeRecords];
+  __shared__ float s_red[4];
+  __shared__ float s_o[4][D];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int seg = A.by_group.div(blockIdx.x), h = blockIdx.x - seg * A.group;
+  const int b = A.by_hkv.div(seg), g = seg - b * A.hkv;
+  griddep_wait();
+  const int p0 = __ldcg(A.prefix + b), p1 = __ldcg(A.prefix + b + 1);
+  const uint32_t range = __ldcg(A.range + seg);
+  __nv_bfloat16* out = A.out + (static_cast<int64_t>(b) * A.hq + g * A.group + h) * D;
+  if (p0 == p1) {  // no tile: nobody wrote the range
+    const __nv_bfloat16 zero = __float2bfloat16_rn(apply_epilogue(0.f, A.epi));
+    for (int c = tid; c < D; c += 128) out[c] = zero;
+    return;
+  }
+  const int n = range & 0xffffu;
+  if (n == 1) return;  // stored by its worker
+  const int64_t rec0 = static_cast<int64_t>(seg) + (range >> 16);
+  auto ml = [&](int r) { return __ldcg(reinterpret_cast<const float2*>(A.rec_ml) + (rec0 + r) * A.group + h); };
+  auto block_reduce = [&](float v, bool maximum) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      const float u = __shfl_xor_sync(0xffffffffu, v, off);
+      v = maximum ? fmaxf(v, u) : v + u;
+    }
+    __syncthreads();
+    if (lane == 0) s_red[warp] = v;
+    __syncthreads();
+    return maximum ? fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]))
+                   : (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]);
+  };
+  float m = -INFINITY;
+  for (int r = tid; r < n; r += 128) m = fmaxf(m, ml(r).x);
+  m = block_reduce(m, true);
+  const float ref = m == -INFINITY ? 0.f : m;
+  float l = 0.f, acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int r0 = 0; r0 < n; r0 += kMergeRecords) {
+    const int count = min(kMergeRecords, n - r0);
+    __syncthreads();
+    for (int r = tid; r < count; r += 128) {
+      const float2 v = ml(r0 + r);
+      const float wt = ex2_approx(v.x - ref);
+      s_w[r] = wt;
+      l += wt * v.y;
+    }
+    __syncthreads();
+#pragma unroll 8
+    for (int r = warp; r < count; r += 4) {
+      const float wt = s_w[r];
+      const float* src = A.rec_o + ((rec0 + r0 + r) * A.group + h) * D;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, __ldcg(src + 32 * e + lane), acc[e]);
     }
   }
+  l = block_reduce(l, false);
+#pragma unroll
+  for (int e = 0; e < E; ++e) s_o[warp][32 * e + lane] = acc[e];
   __syncthreads();
-  for (int i = threadIdx.x; i < A.group * D; i += kWarps * 32) {
-    const int h = i / D, c = i % D;
-    float M = -INFINITY;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w][h][0]);
-    const float ref = M == -INFINITY ? 0.f : M;
-    float sum = 0.f, acc = 0.f;
-    for (int w = 0; w < kWarps; ++w) {
-      const float a = exp2f(s_ml[w][h][0] - ref);
-      sum += a * s_ml[w][h][1];
-      acc += a * s_o[w][h][c];
-    }
-    float* rec = A.part + ((static_cast<int64_t>(b) * A.hq + g * A.group + h) * A.splits + split) * (D + 2);
-    rec[c] = acc;
-    if (c == 0) {
-      rec[D] = M;
-      rec[D + 1] = sum;
-    }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  for (int c = tid; c < D; c += 128) {
+    const float y = ((s_o[0][c] + s_o[1][c]) + (s_o[2][c] + s_o[3][c])) * inv;
+    out[c] = __float2bfloat16_rn(apply_epilogue(y, A.epi));
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(D) decode_pages_merge_kernel(const PageDecodeArgs A) {
-  const float* rec = A.part + static_cast<int64_t>(blockIdx.x) * A.splits * (D + 2);
-  float M = -INFINITY;
-  for (int s = 0; s < A.splits; ++s) M = fmaxf(M, rec[s * (D + 2) + D]);
-  const float ref = M == -INFINITY ? 0.f : M;
-  float sum = 0.f, acc = 0.f;
-  for (int s = 0; s < A.splits; ++s) {
-    const float a = exp2f(rec[s * (D + 2) + D] - ref);
-    sum += a * rec[s * (D + 2) + D + 1];
-    acc += a * rec[s * (D + 2) + threadIdx.x];
+struct Maps {
+  CUtensorMap k, v, k32, v32;
+};
+
+// Tensor maps of the bf16 or int8 pools, as the contiguous decode's.
+template <int D, bool kBF>
+fa_status encode_maps(const fa_decode_params& p, const fa_kv_pages& pg, Maps* m) {
+  using G = Geom<D, kBF>;
+  const uint64_t dims[2] = {static_cast<uint64_t>(D), static_cast<uint64_t>(pg.num_pages) * p.hkv * pg.page_size};
+  const uint64_t strides[1] = {static_cast<uint64_t>(D) * (kBF ? 2 : 1)};
+  const uint32_t box[2] = {static_cast<uint32_t>(kBF ? 64 : G::kRowBytes), static_cast<uint32_t>(kTile)};
+  const CUtensorMapSwizzle sw = G::kSwzMask == 0x70   ? CU_TENSOR_MAP_SWIZZLE_128B
+                                : G::kSwzMask == 0x30 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                      : CU_TENSOR_MAP_SWIZZLE_NONE;
+  const CUtensorMapDataType dt = kBF ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  fa_status st = encode_tensor_map(&m->k, dt, 2, p.k_cache, dims, strides, box, sw);
+  if (st == FA_OK) st = encode_tensor_map(&m->v, dt, 2, p.v_cache, dims, strides, box, sw);
+  if (st != FA_OK) return st;
+  if constexpr (G::kTail) {
+    const uint32_t box32[2] = {32, static_cast<uint32_t>(kTile)};
+    st = encode_tensor_map(&m->k32, dt, 2, p.k_cache, dims, strides, box32, CU_TENSOR_MAP_SWIZZLE_64B);
+    if (st == FA_OK) st = encode_tensor_map(&m->v32, dt, 2, p.v_cache, dims, strides, box32, CU_TENSOR_MAP_SWIZZLE_64B);
   }
-  const float y = apply_epilogue(sum > 0.f ? acc / sum : 0.f, A.epi);
-  A.out[static_cast<int64_t>(blockIdx.x) * D + threadIdx.x] = __float2bfloat16_rn(y);
+  return st;
 }
 
-template <int D, int kKind>
-fa_status launch_typed(PageDecodeArgs& A, const LaunchCtx& ctx) {
-  note_variant(reinterpret_cast<const void*>(decode_pages_kernel<D, kKind>));
-  decode_pages_kernel<D, kKind><<<dim3(A.batch * A.hkv, A.splits), kWarps * 32, 0, ctx.stream>>>(A);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  note_variant(reinterpret_cast<const void*>(decode_pages_merge_kernel<D>));
-  decode_pages_merge_kernel<D><<<A.batch * A.hq, D, 0, ctx.stream>>>(A);
-  return cuda_status(cudaGetLastError());
+// Lets one kernel use this much shared memory; set once per device (`done` is
+// that kernel's own).
+fa_status allow_smem(const void* kern, int bytes, std::atomic<bool> (&done)[64]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FA_ERR_CUDA;
+  if (done[dev].load(std::memory_order_acquire)) return FA_OK;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return FA_ERR_CUDA;
+  done[dev].store(true, std::memory_order_release);
+  return FA_OK;
 }
+
+template <int D, int kKind, bool kSel>
+fa_status launch_typed(const fa_decode_params& p, const fa_kv_pages& pg, PageArgs A, const LaunchCtx& ctx) {
+  using TL = Tile<D, kKind>;
+  auto kern = decode_pages_kernel<D, kKind, kSel>;
+  auto merge = decode_pages_merge_kernel<D>;
+  static std::atomic<bool> allowed[64];
+  static_assert(TL::kSmem + (kMaxBatch + 1) * 4 <= 232448, "shared memory of a CTA");
+  fa_status st = allow_smem(reinterpret_cast<const void*>(kern), TL::kSmem + (kMaxBatch + 1) * 4, allowed);
+  if (st != FA_OK) return st;
+  Maps maps = {};
+  if constexpr (kKind != FA_I4) {
+    st = encode_maps<D, kKind == FA_BF16>(p, pg, &maps);
+    if (st != FA_OK) return st;
+  }
+  // Workers: four per CTA, as many CTAs as fit, as far as the caller's
+  // workspace holds their records (it is sized for eight workers per SM that
+  // serve min(hq, 8) heads each).
+  const int sms = device_sm_count();
+  const int room = sms * 8 * (p.hq < 8 ? p.hq : 8) / A.group;
+  int workers = sms * TL::kCtas * kWarps;
+  if (workers > room) workers = room / kWarps * kWarps;
+  const size_t plan = (static_cast<size_t>(p.batch + 1 + static_cast<size_t>(p.batch) * p.hq) * 4 + 255) / 256 * 256;
+  uint8_t* ws = static_cast<uint8_t*>(p.workspace);
+  A.prefix = reinterpret_cast<int32_t*>(ws);
+  A.range = reinterpret_cast<uint32_t*>(ws) + (p.batch < kMaxBatch ? p.batch : kMaxBatch) + 1;
+  const PageArgs all = A;
+  for (int b0 = 0; b0 < p.batch; b0 += kMaxBatch) {
+    A.batch = p.batch - b0 < kMaxBatch ? p.batch - b0 : kMaxBatch;
+    A.q = all.q + static_cast<int64_t>(b0) * A.hq * D;
+    A.out = all.out + static_cast<int64_t>(b0) * A.hq * D;
+    A.seqlens = all.seqlens + b0;
+    A.block_table = all.block_table + static_cast<int64_t>(b0) * A.max_pages;
+    if (kSel) A.selected = all.selected + static_cast<int64_t>(b0) * A.hkv_real * A.top_k;
+    // no more workers than there can be tiles
+    const int64_t seg_tiles = kSel ? static_cast<int64_t>(A.top_k < A.max_pages ? A.top_k : A.max_pages) *
+                                         (A.page_size / kTile)
+                                   : A.capacity / kTile;
+    const int64_t most = seg_tiles * A.batch * A.hkv;
+    if (most >= (int64_t(1) << 31)) return FA_ERR_UNSUPPORTED;
+    A.n_workers = most < workers ? static_cast<int>((most + kWarps - 1) / kWarps * kWarps) : workers;
+    A.rec_o = reinterpret_cast<float*>(ws + plan);
+    A.rec_ml = A.rec_o + (static_cast<size_t>(A.batch) * A.hkv + A.n_workers) * A.group * D;
+    note_variant(reinterpret_cast<const void*>(kern));
+    kern<<<A.n_workers / kWarps, kThreads, TL::kSmem + (A.batch + 1) * 4, ctx.stream>>>(maps.k, maps.v, maps.k32,
+                                                                                        maps.v32, A);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    note_variant(reinterpret_cast<const void*>(merge));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(A.batch * A.hkv * A.group));
+    cfg.blockDim = dim3(128);
+    cfg.stream = ctx.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, merge, A) != cudaSuccess) return FA_ERR_CUDA;
+  }
+  return FA_OK;
+}
+
 template <int D>
-fa_status launch_dim(PageDecodeArgs& A, int kind, const LaunchCtx& ctx) {
-  if (kind == FA_I4) return launch_typed<D, FA_I4>(A, ctx);
-  if (kind == FA_I8) return launch_typed<D, FA_I8>(A, ctx);
-  return launch_typed<D, FA_BF16>(A, ctx);
+fa_status launch_dim(const fa_decode_params& p, const fa_kv_pages& pg, const PageArgs& A, const LaunchCtx& ctx) {
+  if (A.selected == nullptr) return launch_typed<D, FA_I4, false>(p, pg, A, ctx);
+  if (p.kv_dtype == FA_I4) return launch_typed<D, FA_I4, true>(p, pg, A, ctx);
+  if (p.kv_dtype == FA_I8) return launch_typed<D, FA_I8, true>(p, pg, A, ctx);
+  return launch_typed<D, FA_BF16, true>(p, pg, A, ctx);
 }
 
 }  // namespace
 
 fa_status launch_decode_pages(const fa_decode_params& p, const fa_kv_pages& pages, const int32_t* selected, int top_k,
                               const LaunchCtx& ctx) {
-  PageDecodeArgs A;
+  PageArgs A = {};
   A.q = static_cast<const __nv_bfloat16*>(p.q);
-  A.k_cache = p.k_cache;
-  A.v_cache = p.v_cache;
+  A.k_cache = static_cast<const uint8_t*>(p.k_cache);
+  A.v_cache = static_cast<const uint8_t*>(p.v_cache);
   A.k_scales = p.k_scales;
   A.v_scales = p.v_scales;
   A.seqlens = p.cache_seqlens;
@@ -199,29 +958,30 @@ fa_status launch_decode_pages(const fa_decode_params& p, const fa_kv_pages& page
   A.page_size = pages.page_size;
   A.num_pages = pages.num_pages;
   A.capacity = p.capacity;
-  A.part = static_cast<float*>(p.workspace);
   A.out = static_cast<__nv_bfloat16*>(p.out);
   const int full_group = p.hq / p.hkv;
-  int split = (full_group + 7) / 8;  // a group of more than 8 heads runs in passes
+  int split = (full_group + 7) / 8;
   while (full_group % split != 0) ++split;
-  A.batch = p.batch;
   A.hq = p.hq;
   A.hkv_real = p.hkv;
   A.kv_split = split;
   A.hkv = p.hkv * split;
   A.group = full_group / split;
   A.window = p.window;
+  A.by_hkv = FastDiv::of(A.hkv);
+  A.by_split = FastDiv::of(A.kv_split);
+  A.by_page = FastDiv::of(A.page_size);
+  A.by_page_tiles = FastDiv::of(A.page_size / kTile);
+  A.by_group = FastDiv::of(A.group);
   A.scale_log2 = p.softmax_scale * kLog2e;
   A.epi = make_epilogue(p.epilogue, p.n_epilogue);
   A.wd = ctx.wd;
-  const int segs = A.batch * A.hkv;
-  A.splits = 1 + device_sm_count() * 4 / segs;
   switch (p.head_dim) {
-    case 32: return launch_dim<32>(A, p.kv_dtype, ctx);
-    case 64: return launch_dim<64>(A, p.kv_dtype, ctx);
-    case 96: return launch_dim<96>(A, p.kv_dtype, ctx);
-    case 128: return launch_dim<128>(A, p.kv_dtype, ctx);
-    case 256: return launch_dim<256>(A, p.kv_dtype, ctx);
+    case 32: return launch_dim<32>(p, pages, A, ctx);
+    case 64: return launch_dim<64>(p, pages, A, ctx);
+    case 96: return launch_dim<96>(p, pages, A, ctx);
+    case 128: return launch_dim<128>(p, pages, A, ctx);
+    case 256: return launch_dim<256>(p, pages, A, ctx);
   }
   return FA_ERR_UNSUPPORTED;
 }
