@@ -1,13 +1,14 @@
 // decode_pages.cu -- single-query attention over page pools: every page of a
 // 4-bit cache, or the chosen pages of a bf16, int8 or 4-bit one.
 //
-// The 32-key tiles of all (sequence, KV head) segments are laid end to end and
-// a grid of P warps ("workers") takes equal contiguous ranges of them.  A
+// The tiles (64 keys of a 4-bit cache, else 32) of all (sequence, KV head)
+// segments are laid end to end and a grid of P warps ("workers") takes equal
+// contiguous ranges of them.  A
 // worker looks up its next 32 tiles at a time, one lane a tile (page list,
 // block table), and keeps a ring of tiles in flight in its own shared memory.
 // Per tile, keys on the M side of mma.sync m16n8k16 and heads on N:
-//   S^T[32 keys x 8 heads] = K[32 x d] . Q^T,  online softmax per head in fp32,
-//   O^T[d x 8 heads] += V^T[d x 32] . P'
+//   S^T[keys x 8 heads] = K[keys x d] . Q^T,  online softmax per head in fp32,
+//   O^T[d x 8 heads] += V^T[d x keys] . P'
 // A segment that lies within one worker's range is normalised and stored at
 // once; one that is split leaves a record (m, l, O) per worker, which a second
 // kernel merges (launched early, it waits for the first one's end).
@@ -74,7 +75,7 @@ struct PageArgs {
   // head: hkv counts these virtual heads, each serving `group` query heads
   int batch, hq, hkv, group, hkv_real, kv_split, window;
   int n_workers;
-  FastDiv by_hkv, by_split, by_page, by_page_tiles, by_group;
+  FastDiv by_hkv, by_split, by_page, by_page_runs, by_group;
   float scale_log2;
   Epilogue epi;
   Watchdog wd;
@@ -84,17 +85,20 @@ template <int D, int kKind>
 struct Tile {
   using G = Geom<D, kKind == FA_BF16>;
   static constexpr bool kI4 = kKind == FA_I4;
-  static constexpr int kBytes = kI4 ? kTile * D / 2 : G::kTileBytes;  // of K, and of V
-  static constexpr int kScaleBytes = kI4 ? kTile * 8 : kKind == FA_I8 ? kTile * 4 : 0;
+  // A tile is one or two runs of 32 keys, each within one page.  A 4-bit run is
+  // small, and what a tile costs beside its keys' arithmetic is spread over two.
+  static constexpr int kRuns = kI4 ? 2 : 1;
+  static constexpr int kKeys = kTile * kRuns;
+  static constexpr int kBytes = kI4 ? kKeys * D / 2 : G::kTileBytes;  // of K, and of V
+  static constexpr int kScaleBytes = kI4 ? kKeys * 8 : kKind == FA_I8 ? kTile * 4 : 0;
   static constexpr int kScaleOff = 2 * kBytes;
   static constexpr int kStageBytes = kI4 ? kScaleOff + 2 * kScaleBytes : G::kStageBytes;
-  static constexpr int kStages = kKind == FA_BF16 && D == 256 ? 1 : 3;
+  static constexpr int kStages = kKind == FA_BF16 && D == 256 ? 1 : kI4 ? 2 : 3;
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   static constexpr int kSmem = kRing + (kI4 ? 128 : 1024) /*align*/ + kWarps * kStages * 8;
   static constexpr int kFit = 233472 / (kSmem + (kMaxBatch + 1) * 4 + 1024);
-  // registers: 128 per thread with four CTAs per SM; 8 * D / 16 accumulators
-  // of O at D = 256 need more
-  static constexpr int kMost = D == 256 ? 2 : 4;
+  // up to three CTAs per SM (168 registers a thread), two at D = 256
+  static constexpr int kMost = D == 256 ? 2 : 3;
   static constexpr int kCtas = kFit < 1 ? 1 : (kFit < kMost ? kFit : kMost);
 };
 
@@ -110,23 +114,36 @@ struct Split {
     return y < 0 ? x / (each + 1) : more + y / each;
   }
 };
-// Tiles of a segment of sequence length L.
+// First key a sequence of length L attends to.
 template <bool kSel>
+__device__ __forceinline__ int first_key(const PageArgs& A, int L) {
+  return !kSel && A.window > 0 ? max(0, L - A.window) : 0;
+}
+// Tiles of a segment of sequence length L.
+template <int kKeys, bool kSel>
 __device__ __forceinline__ int tiles_in(const PageArgs& A, int L) {
-  if constexpr (kSel) return min(A.top_k, pages_in(A, L)) * static_cast<int>(A.by_page_tiles.d);
-  const int k_lo = A.window > 0 ? max(0, L - A.window) : 0;
-  return L > 0 ? (L + kTile - 1) / kTile - k_lo / kTile : 0;
+  if constexpr (kSel)
+    return (min(A.top_k, pages_in(A, L)) * static_cast<int>(A.by_page_runs.d) + kKeys / kTile - 1) / (kKeys / kTile);
+  return L > 0 ? (L + kKeys - 1) / kKeys - first_key<kSel>(A, L) / kKeys : 0;
 }
 __device__ __forceinline__ int length_of(const PageArgs& A, int b) { return max(0, min(A.seqlens[b], A.capacity)); }
 
+constexpr int kNoKey = 0x7fffffff;
+template <int kRuns>
 struct TileInfo {
-  int seg;   // b * hkv + g
-  int key0;  // first key's position
-  int row;   // its row in the pools, -1: no key of the tile counts
+  int seg = 0;  // b * hkv + g
+  int key0[kRuns], row[kRuns];  // each run's first position and its pool row; kNoKey, -1: nothing there counts
+  __device__ __forceinline__ TileInfo() {
+#pragma unroll
+    for (int r = 0; r < kRuns; ++r) {
+      key0[r] = kNoKey;
+      row[r] = -1;
+    }
+  }
 };
 
-template <bool kSel>
-__device__ __forceinline__ TileInfo tile_info(const PageArgs& A, const int32_t* pre, int x) {
+template <int kRuns, bool kSel>
+__device__ __forceinline__ TileInfo<kRuns> tile_info(const PageArgs& A, const int32_t* pre, int x) {
   int lo = 0, hi = A.batch - 1;  // the last b with pre[b] <= x
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -134,33 +151,34 @@ __device__ __forceinline__ TileInfo tile_info(const PageArgs& A, const int32_t* 
   }
   const int b = lo, Tb = A.by_hkv.div(pre[b + 1] - pre[b]), y = x - pre[b];
   const int g = y / Tb, t = y - g * Tb, gr = A.by_split.div(g);
-  const int L = length_of(A, b);
-  TileInfo r;
-  r.seg = b * A.hkv + g;
-  int lp, off;
-  if constexpr (kSel) {
-    const int i = A.by_page_tiles.div(t);
-    off = (t - i * A.by_page_tiles.d) * kTile;
-    lp = A.selected[(static_cast<int64_t>(b) * A.hkv_real + gr) * A.top_k + i];
-    if (lp < 0 || lp >= pages_in(A, L) || lp * A.page_size + off >= L) {
-      r.key0 = 0;
-      r.row = -1;
-      return r;
+  const int L = length_of(A, b), n_pages = pages_in(A, L);
+  TileInfo<kRuns> info;
+  info.seg = b * A.hkv + g;
+#pragma unroll
+  for (int r = 0; r < kRuns; ++r) {
+    int lp, off, key0;
+    if constexpr (kSel) {
+      const int run = kRuns * t + r, i = A.by_page_runs.div(run);
+      off = (run - i * static_cast<int>(A.by_page_runs.d)) * kTile;
+      if (i >= A.top_k || i >= n_pages) continue;
+      lp = A.selected[(static_cast<int64_t>(b) * A.hkv_real + gr) * A.top_k + i];
+      if (lp < 0 || lp >= n_pages) continue;
+      key0 = lp * A.page_size + off;
+    } else {
+      key0 = (first_key<kSel>(A, L) / (kRuns * kTile) + t) * (kRuns * kTile) + r * kTile;
+      lp = A.by_page.div(key0);
+      off = key0 - lp * A.page_size;
     }
-    r.key0 = lp * A.page_size + off;
-  } else {
-    const int k_lo = A.window > 0 ? max(0, L - A.window) : 0;
-    r.key0 = (k_lo / kTile + t) * kTile;
-    lp = A.by_page.div(r.key0);
-    off = r.key0 - lp * A.page_size;
+    if (key0 >= L) continue;
+    int pg = A.block_table[static_cast<int64_t>(b) * A.max_pages + lp];
+    if (pg < 0 || pg >= A.num_pages) {  // reported; page 0 keeps the loads inside the pool
+      record_status(A.wd, kStatusRange);
+      pg = 0;
+    }
+    info.key0[r] = key0;
+    info.row[r] = (pg * A.hkv_real + gr) * A.page_size + off;
   }
-  int pg = A.block_table[static_cast<int64_t>(b) * A.max_pages + lp];
-  if (pg < 0 || pg >= A.num_pages) {  // reported; page 0 keeps the loads inside the pool
-    record_status(A.wd, kStatusRange);
-    pg = 0;
-  }
-  r.row = (pg * A.hkv_real + gr) * A.page_size + off;
-  return r;
+  return info;
 }
 
 // S row r of a 16-key half is key key_of(r) of it: for packed rows of 64 bytes
@@ -182,7 +200,6 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
   constexpr int kStages = TL::kStages;
   constexpr int kSteps = D / 16;  // k-steps of S
   constexpr int kMT = D / 16;     // m-tiles of O^T
-  constexpr int kUnroll = 1;      // 16-key halves of a tile in a row in the code
   constexpr bool kQuarter = D == 64 || D == 128;  // int8: see decode.cu
   extern __shared__ uint8_t page_smem_raw[];
   constexpr uintptr_t kAlign = kI4 ? 128 : 1024;
@@ -207,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
     for (int b = b0; b < b1; ++b) {
       const int L = A.seqlens[b];
       if ((L < 0 || L > A.capacity) && blockIdx.x == 0) record_status(A.wd, kStatusRange);
-      own += tiles_in<kSel>(A, length_of(A, b)) * A.hkv;
+      own += tiles_in<TL::kKeys, kSel>(A, length_of(A, b)) * A.hkv;
     }
     int incl = own;
 #pragma unroll
@@ -222,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
     for (int b = b0; b < b1; ++b) {
       pre[b] = at;
       if (blockIdx.x == 0) A.prefix[b] = at;
-      at += tiles_in<kSel>(A, length_of(A, b)) * A.hkv;
+      at += tiles_in<TL::kKeys, kSel>(A, length_of(A, b)) * A.hkv;
     }
     if (threadIdx.x == 0) {
       int total = 0;
@@ -241,55 +258,70 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
 
   auto stage_ptr = [&](int s) { return smem + (warp * kStages + s) * TL::kStageBytes; };
   auto info_of = [&](int block) {
-    TileInfo r{0, 0, -1};
-    if (block * 32 + lane < my_tiles) r = tile_info<kSel>(A, pre, t_first + block * 32 + lane);
-    return r;
+    if (block * 32 + lane < my_tiles) return tile_info<TL::kRuns, kSel>(A, pre, t_first + block * 32 + lane);
+    return TileInfo<TL::kRuns>();
   };
-  TileInfo cur = info_of(0), nxt{0, 0, -1};
-  // 4 bits: lane j < 4 copies the K codes, V codes, K or V scales of a tile
-  const bool scales = lane & 2, of_v = lane & 1;
-  const uint8_t* src = scales ? reinterpret_cast<const uint8_t*>(of_v ? A.v_scales : A.k_scales)
-                              : (of_v ? A.v_cache : A.k_cache);
-  const int src_row = scales ? 8 : D / 2;
-  const uint32_t src_bytes = scales ? TL::kScaleBytes : TL::kBytes;
-  const uint32_t dst = scales ? TL::kScaleOff + (of_v ? TL::kScaleBytes : 0) : (of_v ? TL::kBytes : 0);
+  TileInfo<TL::kRuns> cur = info_of(0), nxt;
+  auto cur_key0 = [&](int r) {
+    if constexpr (TL::kRuns == 1) return cur.key0[0];
+    return r ? cur.key0[TL::kRuns - 1] : cur.key0[0];
+  };
   // tile i's loads into its stage s; i is less than 32 past the block `block`
   auto issue = [&](int i, int s, int block) {
     if (i >= my_tiles) return;
-    const int row = __shfl_sync(0xffffffffu, (i >> 5) == block ? cur.row : nxt.row, i & 31);
+    int row[TL::kRuns];
+#pragma unroll
+    for (int r = 0; r < TL::kRuns; ++r)
+      row[r] = __shfl_sync(0xffffffffu, (i >> 5) == block ? cur.row[r] : nxt.row[r], i & 31);
+    if (!elect_one()) return;
     uint64_t* bar = &bars[s];
     uint8_t* st = stage_ptr(s);
-    if (lane == 0) {
-      if (row < 0) {
-        mbar_arrive(bar);
-      } else {
-        mbar_expect_tx(bar, 2 * TL::kBytes + 2 * TL::kScaleBytes);
-      }
-    }
-    if (row < 0) return;
     if constexpr (kI4) {
-      __syncwarp();
-      if (lane < 4) bulk_load(st + dst, src + static_cast<int64_t>(row) * src_row, src_bytes, bar);
+      // the runs of one page are copied as one
+      const bool one = row[1] == row[0] + kTile && row[0] >= 0;
+      const int n = one ? 2 : (row[0] >= 0) + (row[1] >= 0);
+      if (n == 0) {
+        mbar_arrive(bar);
+        return;
+      }
+      mbar_expect_tx(bar, n * ((2 * TL::kBytes + 2 * TL::kScaleBytes) / 2));
+#pragma unroll 1
+      for (int r = 0; r < 2; ++r) {
+        const int from = r ? row[1] : row[0];
+        if (from < 0 || (r == 1 && one)) continue;
+        const uint32_t bytes = TL::kBytes / (one ? 1 : 2), scale_bytes = TL::kScaleBytes / (one ? 1 : 2);
+        uint8_t* codes = st + r * (TL::kBytes / 2);
+        uint8_t* steps = st + TL::kScaleOff + r * (TL::kScaleBytes / 2);
+        const int64_t at = static_cast<int64_t>(from);
+        bulk_load(codes, A.k_cache + at * (D / 2), bytes, bar);
+        bulk_load(steps, A.k_scales + at * 2, scale_bytes, bar);
+        bulk_load(codes + TL::kBytes, A.v_cache + at * (D / 2), bytes, bar);
+        bulk_load(steps + TL::kScaleBytes, A.v_scales + at * 2, scale_bytes, bar);
+      }
       return;
     }
-    if (lane != 0) return;
+    if (row[0] < 0) {
+      mbar_arrive(bar);
+      return;
+    }
+    mbar_expect_tx(bar, 2 * TL::kBytes + 2 * TL::kScaleBytes);
     if constexpr (kI8) {
 #pragma unroll
       for (int h = 0; h < G::kHalves; ++h) {
-        tma_load_2d(st + h * kTile * G::kRowBytes, &tm_k, bar, G::kRowBytes * h, row);
-        tma_load_2d(st + TL::kBytes + h * kTile * G::kRowBytes, &tm_v, bar, G::kRowBytes * h, row);
+        tma_load_2d(st + h * kTile * G::kRowBytes, &tm_k, bar, G::kRowBytes * h, row[0]);
+        tma_load_2d(st + TL::kBytes + h * kTile * G::kRowBytes, &tm_v, bar, G::kRowBytes * h, row[0]);
       }
-      bulk_load(st + TL::kScaleOff, A.k_scales + row, TL::kScaleBytes, bar);
-      bulk_load(st + TL::kScaleOff + TL::kScaleBytes, A.v_scales + row, TL::kScaleBytes, bar);
+      bulk_load(st + TL::kScaleOff, A.k_scales + row[0], TL::kScaleBytes, bar);
+      bulk_load(st + TL::kScaleOff + TL::kScaleBytes, A.v_scales + row[0], TL::kScaleBytes, bar);
     } else if constexpr (kBF) {
 #pragma unroll
       for (int c = 0; c < G::kNFull; ++c) {
-        tma_load_2d(st + c * G::kChunkBytes, &tm_k, bar, 64 * c, row);
-        tma_load_2d(st + TL::kBytes + c * G::kChunkBytes, &tm_v, bar, 64 * c, row);
+        tma_load_2d(st + c * G::kChunkBytes, &tm_k, bar, 64 * c, row[0]);
+        tma_load_2d(st + TL::kBytes + c * G::kChunkBytes, &tm_v, bar, 64 * c, row[0]);
       }
       if constexpr (G::kTail) {
-        tma_load_2d(st + G::kNFull * G::kChunkBytes, &tm_k32, bar, 64 * G::kNFull, row);
-        tma_load_2d(st + TL::kBytes + G::kNFull * G::kChunkBytes, &tm_v32, bar, 64 * G::kNFull, row);
+        tma_load_2d(st + G::kNFull * G::kChunkBytes, &tm_k32, bar, 64 * G::kNFull, row[0]);
+        tma_load_2d(st + TL::kBytes + G::kNFull * G::kChunkBytes, &tm_v32, bar, 64 * G::kNFull, row[0]);
       }
     }
   };
@@ -303,13 +335,14 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
   float o[kMT][4];
   float m_run[2], l_run[2];
   float om[2];        // 4 bits: sum of p * (offset + 8 step)
-  float cap = 0.f;    // quantised: power of two below the largest V step so far
+  float cap = 0.f;    // quantised: power of two below the largest V step so far,
+  float to_unit = 0.f;  // and its inverse
   auto reset = [&]() {
 #pragma unroll
     for (int m = 0; m < kMT; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
     m_run[0] = m_run[1] = -INFINITY;
     l_run[0] = l_run[1] = om[0] = om[1] = 0.f;
-    cap = 0.f;
+    cap = to_unit = 0.f;
   };
   auto load_q = [&](int b, int g) {
     const bool head_ok = gq < A.group;
@@ -456,24 +489,26 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
         A.range[seg] = static_cast<uint32_t>(w) << 16 | static_cast<uint32_t>(n);
       }
       key_end = length_of(A, b);
-      k_lo = !kSel && A.window > 0 ? max(0, key_end - A.window) : 0;
+      k_lo = first_key<kSel>(A, key_end);
     }
-    const int key0 = __shfl_sync(0xffffffffu, cur.key0, i & 31);
-    const bool any = !kSel || __shfl_sync(0xffffffffu, cur.row, i & 31) >= 0;
     // every lane polls; whether to go on is a decision of the whole warp
     const bool ready = wait_parity(&bars[s], parity, A.wd);
     if (!__all_sync(0xffffffffu, ready)) break;
-    if (any) {
-      const uint32_t kt = smem_u32(stage_ptr(s));
+#pragma unroll 1
+    for (int r = 0; r < TL::kRuns; ++r) {
+      const int key0 = __shfl_sync(0xffffffffu, cur_key0(r), i & 31);
+      if (key0 == kNoKey) continue;
+      const uint32_t kt = smem_u32(stage_ptr(s)) + r * (TL::kBytes / TL::kRuns);
       const uint32_t vt = kt + TL::kBytes;
-      const float* ksc = reinterpret_cast<const float*>(stage_ptr(s) + TL::kScaleOff);
-      const float* vsc = ksc + TL::kScaleBytes / 4;
+      const uint32_t ksc = smem_u32(stage_ptr(s)) + TL::kScaleOff + r * (TL::kScaleBytes / TL::kRuns);
+      const uint32_t vsc = ksc + TL::kScaleBytes;
 
       // ---- S^T = K . Q^T
       float sc[2][4];
-#pragma unroll kUnroll
+#pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        float(&acc)[4] = sc[mt];
+        acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
         if constexpr (kBF) {
           const int mi = lane >> 3, mr = lane & 7;
 #pragma unroll
@@ -536,14 +571,6 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
                        i8x2_to_f16x2_odd(wb[ks]), qb0[ks], qb1[ks]);
           }
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (mt == 0) {
-            sc[0][e] = acc[e];
-          } else {
-            sc[1][e] = acc[e];
-          }
-        }
       }
 
       // ---- online softmax per head; positions are looked at only in tiles
@@ -551,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
       uint32_t pb[2][2];
       auto softmax = [&](auto masked_tag) {
         constexpr bool kMasked = decltype(masked_tag)::value;
-        float x[2][4];
+        float (&x)[2][4] = sc;
         [[maybe_unused]] float vs[2][2], vc[2][2];  // quantised: V step, 4 bits: offset + 8 step
         float mx0 = -INFINITY, mx1 = -INFINITY;
         [[maybe_unused]] float top = 0.f;
@@ -563,19 +590,19 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
             const bool ok = !kMasked || (key0 + kl >= k_lo && key0 + kl < key_end);
             float x0, x1;
             if constexpr (kI4) {
-              const float2 ss = *reinterpret_cast<const float2*>(ksc + 2 * kl);
-              const float2 sv = *reinterpret_cast<const float2*>(vsc + 2 * kl);
-              const float c = fmaf(8.f, ss.x, ss.y);
-              x0 = fmaf(sc[mt][2 * hf], ss.x * qs0, c * qm0);
-              x1 = fmaf(sc[mt][2 * hf + 1], ss.x * qs1, c * qm1);
-              vs[mt][hf] = ok ? sv.x : 0.f;
-              vc[mt][hf] = ok ? fmaf(8.f, sv.x, sv.y) : 0.f;
+              const uint2 sk = lds64(ksc + 8 * kl), sv = lds64(vsc + 8 * kl);
+              const float step = __uint_as_float(sk.x), v_step = __uint_as_float(sv.x);
+              const float c = fmaf(8.f, step, __uint_as_float(sk.y));
+              x0 = fmaf(sc[mt][2 * hf], step * qs0, c * qm0);
+              x1 = fmaf(sc[mt][2 * hf + 1], step * qs1, c * qm1);
+              vs[mt][hf] = ok ? v_step : 0.f;
+              vc[mt][hf] = ok ? fmaf(8.f, v_step, __uint_as_float(sv.y)) : 0.f;
               top = fmaxf(top, vs[mt][hf]);
             } else if constexpr (kI8) {
-              const float s = ksc[kl];
-              x0 = sc[mt][2 * hf] * (s * qs0);
-              x1 = sc[mt][2 * hf + 1] * (s * qs1);
-              vs[mt][hf] = ok ? vsc[kl] : 0.f;
+              const float step = __uint_as_float(lds32(ksc + 4 * kl));
+              x0 = sc[mt][2 * hf] * (step * qs0);
+              x1 = sc[mt][2 * hf + 1] * (step * qs1);
+              vs[mt][hf] = ok ? __uint_as_float(lds32(vsc + 4 * kl)) : 0.f;
               top = fmaxf(top, vs[mt][hf]);
             } else {
               x0 = sc[mt][2 * hf] * qs0;
@@ -615,6 +642,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
             a0 *= ratio;
             a1 *= ratio;
             cap = unit;
+            to_unit = unit > 0.f ? 1.f / unit : 0.f;
           }
 #pragma unroll
           for (int m = 0; m < kMT; ++m) {
@@ -624,7 +652,6 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
         }
         const float ref0 = m_run[0] == -INFINITY ? 0.f : m_run[0];
         const float ref1 = m_run[1] == -INFINITY ? 0.f : m_run[1];
-        [[maybe_unused]] const float to_unit = cap > 0.f ? 1.f / cap : 0.f;
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
           uint32_t packed[2];
@@ -670,20 +697,18 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
           __syncwarp();
         }
         const int mi4 = lane >> 3, mr = lane & 7;
-#pragma unroll kUnroll
+#pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
-          const uint32_t pf[2] = {mt ? pb[1][0] : pb[0][0], mt ? pb[1][1] : pb[0][1]};
 #pragma unroll
           for (int mi = 0; mi < kMT; ++mi) {
             uint32_t a[4];
             ldsm_x4_trans(bf_addr<D>(vt, 16 * mt + 8 * (mi4 / 2) + mr, 16 * mi + 8 * (mi4 % 2)), a);
-            mma16816_bf16(o[mi], a, pf[0], pf[1]);
+            mma16816_bf16(o[mi], a, pb[mt][0], pb[mt][1]);
           }
         }
       } else if constexpr (kI8) {
-#pragma unroll kUnroll
+#pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
-          const uint32_t pf[2] = {mt ? pb[1][0] : pb[0][0], mt ? pb[1][1] : pb[0][1]};
           const int kk0 = 16 * mt + 2 * qq;
 #pragma unroll
           for (int pr = 0; pr < D / 32; ++pr) {
@@ -693,9 +718,9 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
             const uint32_t t01l = prmt(w0, w1, 0x5410), t01h = prmt(w0, w1, 0x7632);
             const uint32_t t23l = prmt(w2, w3, 0x5410), t23h = prmt(w2, w3, 0x7632);
             mma16816(o[2 * pr], i8x2_to_f16x2_even(t01l), i8x2_to_f16x2_odd(t01l), i8x2_to_f16x2_even(t23l),
-                     i8x2_to_f16x2_odd(t23l), pf[0], pf[1]);
+                     i8x2_to_f16x2_odd(t23l), pb[mt][0], pb[mt][1]);
             mma16816(o[2 * pr + 1], i8x2_to_f16x2_even(t01h), i8x2_to_f16x2_odd(t01h), i8x2_to_f16x2_even(t23h),
-                     i8x2_to_f16x2_odd(t23h), pf[0], pf[1]);
+                     i8x2_to_f16x2_odd(t23h), pb[mt][0], pb[mt][1]);
           }
         }
       } else {
@@ -706,9 +731,8 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
           mma16816(lo, i4x2_low(t01), i4x2_high(t01), i4x2_low(t23), i4x2_high(t23), p[0], p[1]);
           mma16816(hi, i4x2_low(t01 >> 8), i4x2_high(t01 >> 8), i4x2_low(t23 >> 8), i4x2_high(t23 >> 8), p[0], p[1]);
         };
-#pragma unroll kUnroll
+#pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
-          const uint32_t pf[2] = {mt ? pb[1][0] : pb[0][0], mt ? pb[1][1] : pb[0][1]};
           const uint32_t a0 = vt + gq * (D / 16) + 16 * mt * (D / 2);
           uint32_t at[4];
 #pragma unroll
@@ -730,8 +754,8 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
             }
 #pragma unroll
             for (int c = 0; c < kH / 2; ++c) {
-              four(o[4 * c], o[4 * c + 1], prmt(wv[0][c], wv[1][c], 0x5410), prmt(wv[2][c], wv[3][c], 0x5410), pf);
-              four(o[4 * c + 2], o[4 * c + 3], prmt(wv[0][c], wv[1][c], 0x7632), prmt(wv[2][c], wv[3][c], 0x7632), pf);
+              four(o[4 * c], o[4 * c + 1], prmt(wv[0][c], wv[1][c], 0x5410), prmt(wv[2][c], wv[3][c], 0x5410), pb[mt]);
+              four(o[4 * c + 2], o[4 * c + 3], prmt(wv[0][c], wv[1][c], 0x7632), prmt(wv[2][c], wv[3][c], 0x7632), pb[mt]);
             }
           } else {
 #pragma unroll
@@ -743,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
                 asm volatile("ld.shared.u16 %0, [%1];" : "=h"(hw) : "r"(at[e] + 2 * c));
                 v[e] = hw;
               }
-              four(o[2 * c], o[2 * c + 1], v[0] | (v[1] << 16), v[2] | (v[3] << 16), pf);
+              four(o[2 * c], o[2 * c + 1], v[0] | (v[1] << 16), v[2] | (v[3] << 16), pb[mt]);
             }
           }
         }
@@ -971,7 +995,7 @@ fa_status launch_decode_pages(const fa_decode_params& p, const fa_kv_pages& page
   A.by_hkv = FastDiv::of(A.hkv);
   A.by_split = FastDiv::of(A.kv_split);
   A.by_page = FastDiv::of(A.page_size);
-  A.by_page_tiles = FastDiv::of(A.page_size / kTile);
+  A.by_page_runs = FastDiv::of(A.page_size / kTile);
   A.by_group = FastDiv::of(A.group);
   A.scale_log2 = p.softmax_scale * kLog2e;
   A.epi = make_epilogue(p.epilogue, p.n_epilogue);

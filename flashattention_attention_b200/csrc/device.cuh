@@ -115,6 +115,18 @@ __device__ __forceinline__ bool wait_parity(uint64_t* bar, uint32_t parity, cons
   }
 }
 
+// One lane of a converged warp (the compiler then knows that a single thread
+// issues what follows).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // ---------------------------------------------------------------- TMA
 // Tiled tensor loads (no multicast).  Coordinates are innermost first.
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0,
