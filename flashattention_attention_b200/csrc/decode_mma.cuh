@@ -100,22 +100,15 @@ __device__ __forceinline__ void i8x4_to_f16x2_biased(uint32_t w, uint32_t& even,
 }
 constexpr float kCodeBias = 1152.0f;
 
-// fp16x2 of (code - 8) for the 4-bit codes in the low halves of bytes 0 and 2
-// of w, and in the high halves (exact): a code in mantissa bits 0-3 under the
-// exponent of 1024, or in bits 4-7 under that of 64, is the fp16 number
-// 1024 + code or 64 + code, and the difference is exact.
-__device__ __forceinline__ uint32_t i4x2_low(uint32_t w) {
-  uint32_t t, r;
-  asm("lop3.b32 %0, %1, 0x000f000f, 0x64006400, 0xea;" : "=r"(t) : "r"(w));
-  asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(t), "r"(0x64086408u));  // 1032
-  return r;
-}
-__device__ __forceinline__ uint32_t i4x2_high(uint32_t w) {
-  uint32_t t, r;
-  asm("lop3.b32 %0, %1, 0x00f000f0, 0x54005400, 0xea;" : "=r"(t) : "r"(w));
-  asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(t), "r"(0x54805480u));  // 72
-  return r;
-}
+// fp16x2 of 4-bit codes as subnormal numbers: a code in mantissa bits 0-3 of
+// an otherwise empty half is exactly code * 2^-24, one in bits 4-7 is
+// code * 2^-20, and the MMA multiplies subnormal inputs exactly.  So one AND
+// widens two codes: those in the low halves of bytes 0 and 2 of w, and those
+// in the high halves.
+__device__ __forceinline__ uint32_t i4x2_low(uint32_t w) { return w & 0x000f000fu; }
+__device__ __forceinline__ uint32_t i4x2_high(uint32_t w) { return w & 0x00f000f0u; }
+constexpr float kLowUnit = 16777216.f;  // 2^24
+constexpr float kHighUnit = 1048576.f;  // 2^20
 
 // Four 8x8 b16 matrices; lane l gives the row address of matrix l / 8, row l % 8.
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {

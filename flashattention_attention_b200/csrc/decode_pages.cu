@@ -13,17 +13,20 @@
 // once; one that is split leaves a record (m, l, O) per worker, which a second
 // kernel merges (launched early, it waits for the first one's end).
 //
-// 4-bit rows (value = code * step + offset): codes enter the MMA as the exact
-// fp16 numbers code - 8, so with c = offset + 8 step
-//   q . k = step (q . (code - 8)) + c sum(q),
-//   sum_j p_j v_j = sum_j (p_j step_j) (code_j - 8) + sum_j p_j c_j
+// 4-bit rows (value = code * step + offset): codes enter the MMA exactly, as
+// subnormal fp16 numbers (one AND for two of them), and
+//   q . k = step (q . code) + offset sum(q),
+//   sum_j p_j v_j = sum_j (p_j step_j) code_j + sum_j p_j offset_j
 // where the second terms stay in fp32.  p_j step_j is rounded to fp16 after
 // division by the power of two below the largest step seen so far (rescaled
 // like the running maximum), so no step is too small or too large for fp16.
-// int8 rows: the same with c = 0.  A word of eight codes holds channels 0 .. 7
-// of its four bytes: the low halves of bytes 0 and 2 are channels 0 and 4, so
-// one LOP3 and one exact subtraction widen two channels, in an order that Q's
-// fragments (and the output's addresses) follow.
+// int8 rows: the same without offsets.  A word of eight codes holds channels
+// 0 .. 7 of its four bytes: the low halves of bytes 0 and 2 are channels 0 and
+// 4, in an order that Q's fragments (and the output's addresses) follow.
+// Codes are not centred, so sum (p step) code grows with the number of keys
+// whatever the values are, and the tensor core's additions to a large number
+// lose bits to one side: every 16 tiles the part all channels share is moved
+// from the accumulators into one number per head.
 #include <atomic>
 #include <type_traits>
 
@@ -333,15 +336,17 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
   float qs0 = 0.f, qs1 = 0.f;  // logit multipliers of heads 2qq, 2qq + 1
   float qm0 = 0.f, qm1 = 0.f;  // 4 bits: scale * sum of q
   float o[kMT][4];
-  float m_run[2], l_run[2];
-  float om[2];        // 4 bits: sum of p * (offset + 8 step)
+  float m_run[2];
+  float2 l_run;
+  float2 om;          // 4 bits: sum of p * offset (heads 2qq, 2qq + 1)
+  float2 moved;       // 4 bits: what was taken from this thread's accumulators of low codes
   float cap = 0.f;    // quantised: power of two below the largest V step so far,
   float to_unit = 0.f;  // and its inverse
   auto reset = [&]() {
 #pragma unroll
     for (int m = 0; m < kMT; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
     m_run[0] = m_run[1] = -INFINITY;
-    l_run[0] = l_run[1] = om[0] = om[1] = 0.f;
+    l_run = om = moved = make_float2(0.f, 0.f);
     cap = to_unit = 0.f;
   };
   auto load_q = [&](int b, int g) {
@@ -386,14 +391,17 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
     // the power of two from amax's exponent bits, kept where it and its inverse are normal
     const int ex = min(max(static_cast<int>(__float_as_uint(amax) >> 23), 15), 254);
     const float up = __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);  // 2^(14 - (ex - 127))
-    const float qs_own = A.scale_log2 * __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
+    float qs_own = A.scale_log2 * __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
+    if constexpr (kI4) qs_own *= kLowUnit;
     const float qm_own = A.scale_log2 * sum;
 #pragma unroll
     for (int ks = 0; ks < kSteps; ++ks) {
       // channels of the k-step's fragments: see i4x2_* and i8x2_*
       const int c0 = kI4 ? 8 * (ks / 2) + 2 * (ks % 2) : 4 * ks, far = kI4 ? 4 : 2;
+      // (4 bits: odd channels are the high codes, 16 times as large as the low ones)
+      const float up1 = kI4 ? up * (1.f / 16.f) : up;
       qb0[ks] = pack_f16x2(qv[c0] * up, qv[c0 + far] * up);
-      qb1[ks] = pack_f16x2(qv[c0 + 1] * up, qv[c0 + far + 1] * up);
+      qb1[ks] = pack_f16x2(qv[c0 + 1] * up1, qv[c0 + far + 1] * up1);
     }
     qs0 = __shfl_sync(0xffffffffu, qs_own, (2 * qq) * 4);
     qs1 = __shfl_sync(0xffffffffu, qs_own, (2 * qq + 1) * 4);
@@ -410,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
   // The segment's state: the output rows where this worker saw all of it, else
   // its record (segment + worker).
   auto finish = [&](int seg, bool whole) {
-    float l0 = l_run[0], l1 = l_run[1], m0 = om[0], m1 = om[1];
+    float l0 = l_run.x, l1 = l_run.y, m0 = om.x, m1 = om.y;
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {
       l0 += __shfl_xor_sync(0xffffffffu, l0, off);
@@ -420,7 +428,6 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
         m1 += __shfl_xor_sync(0xffffffffu, m1, off);
       }
     }
-    const float unit = kBF ? 1.f : cap;
     const int64_t rec = static_cast<int64_t>(seg) + w;
     const int b = A.by_hkv.div(seg), g = seg - b * A.hkv;
 #pragma unroll 1
@@ -431,8 +438,15 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
       float y[2 * kMT];
 #pragma unroll
       for (int mi = 0; mi < kMT; ++mi) {
-        y[2 * mi] = fmaf(j ? o[mi][1] : o[mi][0], unit, add);
-        y[2 * mi + 1] = fmaf(j ? o[mi][3] : o[mi][2], unit, add);
+        const float lo = j ? o[mi][1] : o[mi][0], hi = j ? o[mi][3] : o[mi][2];
+        if constexpr (kI4) {
+          const float back = j ? moved.y : moved.x;
+          y[2 * mi] = fmaf((lo + back) * kLowUnit, cap, add);
+          y[2 * mi + 1] = fmaf((hi + 16.f * back) * kHighUnit, cap, add);
+        } else {
+          y[2 * mi] = kI8 ? lo * cap : lo;
+          y[2 * mi + 1] = kI8 ? hi * cap : hi;
+        }
       }
       if (!whole) {
         if (gq == 0)
@@ -578,40 +592,36 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
       uint32_t pb[2][2];
       auto softmax = [&](auto masked_tag) {
         constexpr bool kMasked = decltype(masked_tag)::value;
-        float (&x)[2][4] = sc;
-        [[maybe_unused]] float vs[2][2], vc[2][2];  // quantised: V step, 4 bits: offset + 8 step
+        float2 x[2][2];                             // [mt][key half], heads 2qq and 2qq + 1
+        [[maybe_unused]] float vs[2][2], vo[2][2];  // quantised: V step, 4 bits: V offset
         float mx0 = -INFINITY, mx1 = -INFINITY;
         [[maybe_unused]] float top = 0.f;
+        const float2 qs = make_float2(qs0, qs1);
+        [[maybe_unused]] const float2 qm = make_float2(qm0, qm1);
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const int kl = 16 * mt + 8 * hf + key_of<kKind>(gq);
             const bool ok = !kMasked || (key0 + kl >= k_lo && key0 + kl < key_end);
-            float x0, x1;
+            float2 v = mul2(make_float2(sc[mt][2 * hf], sc[mt][2 * hf + 1]), qs);
             if constexpr (kI4) {
               const uint2 sk = lds64(ksc + 8 * kl), sv = lds64(vsc + 8 * kl);
-              const float step = __uint_as_float(sk.x), v_step = __uint_as_float(sv.x);
-              const float c = fmaf(8.f, step, __uint_as_float(sk.y));
-              x0 = fmaf(sc[mt][2 * hf], step * qs0, c * qm0);
-              x1 = fmaf(sc[mt][2 * hf + 1], step * qs1, c * qm1);
-              vs[mt][hf] = ok ? v_step : 0.f;
-              vc[mt][hf] = ok ? fmaf(8.f, v_step, __uint_as_float(sv.y)) : 0.f;
+              const float step = __uint_as_float(sk.x), off = __uint_as_float(sk.y);
+              v = fma2(v, make_float2(step, step), mul2(make_float2(off, off), qm));
+              vs[mt][hf] = ok ? __uint_as_float(sv.x) : 0.f;
+              vo[mt][hf] = ok ? __uint_as_float(sv.y) : 0.f;
               top = fmaxf(top, vs[mt][hf]);
             } else if constexpr (kI8) {
               const float step = __uint_as_float(lds32(ksc + 4 * kl));
-              x0 = sc[mt][2 * hf] * (step * qs0);
-              x1 = sc[mt][2 * hf + 1] * (step * qs1);
+              v = mul2(v, make_float2(step, step));
               vs[mt][hf] = ok ? __uint_as_float(lds32(vsc + 4 * kl)) : 0.f;
               top = fmaxf(top, vs[mt][hf]);
-            } else {
-              x0 = sc[mt][2 * hf] * qs0;
-              x1 = sc[mt][2 * hf + 1] * qs1;
             }
-            x[mt][2 * hf] = ok ? x0 : -INFINITY;
-            x[mt][2 * hf + 1] = ok ? x1 : -INFINITY;
-            mx0 = fmaxf(mx0, x[mt][2 * hf]);
-            mx1 = fmaxf(mx1, x[mt][2 * hf + 1]);
+            if (kMasked && !ok) v = make_float2(-INFINITY, -INFINITY);
+            x[mt][hf] = v;
+            mx0 = fmaxf(mx0, v.x);
+            mx1 = fmaxf(mx1, v.y);
           }
         }
 #pragma unroll
@@ -626,50 +636,43 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
         if (__any_sync(0xffffffffu, up)) {
           const float mn0 = fmaxf(m_run[0], mx0), mn1 = fmaxf(m_run[1], mx1);
           const float r0 = mn0 == -INFINITY ? 0.f : mn0, r1 = mn1 == -INFINITY ? 0.f : mn1;
-          const float al0 = ex2_approx(m_run[0] - r0), al1 = ex2_approx(m_run[1] - r1);
+          float2 al = make_float2(ex2_approx(m_run[0] - r0), ex2_approx(m_run[1] - r1));
           m_run[0] = mn0;
           m_run[1] = mn1;
-          l_run[0] *= al0;
-          l_run[1] *= al1;
-          float a0 = al0, a1 = al1;
+          l_run = mul2(l_run, al);
           if constexpr (!kBF) {
             // steps are not negative, so their bits order like the numbers
             const unsigned bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
             const float unit = fmaxf(cap, __uint_as_float(bits & 0x7f800000u));
             const float ratio = unit > 0.f ? cap / unit : 0.f;
-            om[0] *= al0;
-            om[1] *= al1;
-            a0 *= ratio;
-            a1 *= ratio;
+            om = mul2(om, al);
+            al = mul2(al, make_float2(ratio, ratio));
+            moved = mul2(moved, al);
             cap = unit;
             to_unit = unit > 0.f ? 1.f / unit : 0.f;
           }
 #pragma unroll
           for (int m = 0; m < kMT; ++m) {
-            o[m][0] *= a0; o[m][2] *= a0;
-            o[m][1] *= a1; o[m][3] *= a1;
+            o[m][0] *= al.x; o[m][2] *= al.x;
+            o[m][1] *= al.y; o[m][3] *= al.y;
           }
         }
-        const float ref0 = m_run[0] == -INFINITY ? 0.f : m_run[0];
-        const float ref1 = m_run[1] == -INFINITY ? 0.f : m_run[1];
+        const float2 ref = make_float2(m_run[0] == -INFINITY ? 0.f : -m_run[0], m_run[1] == -INFINITY ? 0.f : -m_run[1]);
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
           uint32_t packed[2];
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            const float p0 = ex2_approx(x[mt][2 * hf] - ref0);
-            const float p1 = ex2_approx(x[mt][2 * hf + 1] - ref1);
-            l_run[0] += p0;
-            l_run[1] += p1;
+            const float2 y = add2(x[mt][hf], ref);
+            float2 p = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+            l_run = add2(l_run, p);
             if constexpr (kBF) {
-              packed[hf] = pack_bf16x2(p0, p1);
+              packed[hf] = pack_bf16x2(p.x, p.y);
             } else {
+              if constexpr (kI4) om = fma2(p, make_float2(vo[mt][hf], vo[mt][hf]), om);
               const float u = vs[mt][hf] * to_unit;
-              packed[hf] = pack_f16x2(p0 * u, p1 * u);
-              if constexpr (kI4) {
-                om[0] = fmaf(p0, vc[mt][hf], om[0]);
-                om[1] = fmaf(p1, vc[mt][hf], om[1]);
-              }
+              p = mul2(p, make_float2(u, u));
+              packed[hf] = pack_f16x2(p.x, p.y);
             }
           }
           pb[mt][0] = transpose8x8(packed[0]);  // (head gq; S rows 2qq, 2qq+1)
@@ -770,6 +773,24 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
               four(o[2 * c], o[2 * c + 1], v[0] | (v[1] << 16), v[2] | (v[3] << 16), pb[mt]);
             }
           }
+        }
+      }
+    }
+    if constexpr (kI4) {
+      if ((i & 15) == 15) {
+        // what the channels share: the mean over this thread's low codes
+        // (about 7.5 2^-24 sum of P'; 16 times that in the high ones)
+        float2 mean = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int mi = 0; mi < kMT; ++mi) mean = add2(mean, make_float2(o[mi][0], o[mi][1]));
+        mean = mul2(mean, make_float2(1.f / kMT, 1.f / kMT));
+        moved = add2(moved, mean);
+#pragma unroll
+        for (int mi = 0; mi < kMT; ++mi) {
+          o[mi][0] -= mean.x;
+          o[mi][1] -= mean.y;
+          o[mi][2] = fmaf(-16.f, mean.x, o[mi][2]);
+          o[mi][3] = fmaf(-16.f, mean.y, o[mi][3]);
         }
       }
     }
