@@ -37,6 +37,7 @@ namespace fa {
 namespace {
 
 constexpr int kThreads = kWarps * 32;
+constexpr float kSlack = 8.f;    // binary orders a weight may pass its reference by
 constexpr int kMaxBatch = 256;  // sequences per launch (their tile prefix is in shared memory)
 
 // Division of 0 <= x < 2^31 by a number known on the host: x / d =
@@ -336,7 +337,8 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
   float qs0 = 0.f, qs1 = 0.f;  // logit multipliers of heads 2qq, 2qq + 1
   float qm0 = 0.f, qm1 = 0.f;  // 4 bits: scale * sum of q
   float o[kMT][4];
-  float m_run[2];
+  float m_run[2];                         // reference of each head's weights
+  float2 nref = make_float2(0.f, 0.f);  // its negative, 0 where there is none
   float2 l_run;
   float2 om;          // 4 bits: sum of p * offset (heads 2qq, 2qq + 1)
   float2 moved;       // 4 bits: what was taken from this thread's accumulators of low codes
@@ -346,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
 #pragma unroll
     for (int m = 0; m < kMT; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
     m_run[0] = m_run[1] = -INFINITY;
+    nref = make_float2(0.f, 0.f);
     l_run = om = moved = make_float2(0.f, 0.f);
     cap = to_unit = 0.f;
   };
@@ -624,19 +627,21 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
             mx1 = fmaxf(mx1, v.y);
           }
         }
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
-          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
-        }
-        // the running maxima and the V unit move only when a tile raises them,
-        // and O is rescaled only when one of them moved
-        bool up = mx0 > m_run[0] || mx1 > m_run[1];
-        if constexpr (!kBF) up |= top >= 2.f * cap && top > 0.f;
+        // A head's reference moves, and O is rescaled, only when a logit passes
+        // it by more than 8 (weights then reach 2^8, far inside fp16's range
+        // and exact as factors); likewise the V unit when a step reaches 16 of
+        // it.  So most tiles need no maximum across lanes.
+        bool up = mx0 > m_run[0] + kSlack || mx1 > m_run[1] + kSlack;
+        if constexpr (!kBF) up |= top >= 16.f * cap && top > 0.f;
         if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) {
+            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
+          }
           const float mn0 = fmaxf(m_run[0], mx0), mn1 = fmaxf(m_run[1], mx1);
-          const float r0 = mn0 == -INFINITY ? 0.f : mn0, r1 = mn1 == -INFINITY ? 0.f : mn1;
-          float2 al = make_float2(ex2_approx(m_run[0] - r0), ex2_approx(m_run[1] - r1));
+          nref = make_float2(mn0 == -INFINITY ? 0.f : -mn0, mn1 == -INFINITY ? 0.f : -mn1);
+          float2 al = make_float2(ex2_approx(m_run[0] + nref.x), ex2_approx(m_run[1] + nref.y));
           m_run[0] = mn0;
           m_run[1] = mn1;
           l_run = mul2(l_run, al);
@@ -657,13 +662,12 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
             o[m][1] *= al.y; o[m][3] *= al.y;
           }
         }
-        const float2 ref = make_float2(m_run[0] == -INFINITY ? 0.f : -m_run[0], m_run[1] == -INFINITY ? 0.f : -m_run[1]);
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
           uint32_t packed[2];
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            const float2 y = add2(x[mt][hf], ref);
+            const float2 y = add2(x[mt][hf], nref);
             float2 p = make_float2(ex2_approx(y.x), ex2_approx(y.y));
             l_run = add2(l_run, p);
             if constexpr (kBF) {
