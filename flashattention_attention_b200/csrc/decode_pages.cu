@@ -811,14 +811,16 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
 }
 
 // One query head's split records into its output row; the rows of segments
-// without a tile.  Four warps take every fourth record.
-constexpr int kMergeRecords = 512;  // weights held at a time
+// without a tile.  A warp takes every eighth record, a lane D / 32 consecutive
+// channels of it; the weights of up to 1024 records are held at a time.
+constexpr int kMergeThreads = 256;
+constexpr int kMergeRecords = 1024;
 template <int D>
-__global__ void __launch_bounds__(128) decode_pages_merge_kernel(const PageArgs A) {
-  constexpr int E = D / 32;
-  __shared__ float s_w[kMergeRecords];
-  __shared__ float s_red[4];
-  __shared__ float s_o[4][D];
+__global__ void __launch_bounds__(kMergeThreads) decode_pages_merge_kernel(const PageArgs A) {
+  constexpr int E = D / 32, kMergeWarps = kMergeThreads / 32;
+  __shared__ float2 s_ml[kMergeRecords];
+  __shared__ float s_red[2][kMergeWarps];
+  __shared__ float s_o[kMergeWarps][D];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int seg = A.by_group.div(blockIdx.x), h = blockIdx.x - seg * A.group;
   const int b = A.by_hkv.div(seg), g = seg - b * A.hkv;
@@ -828,58 +830,72 @@ __global__ void __launch_bounds__(128) decode_pages_merge_kernel(const PageArgs 
   __nv_bfloat16* out = A.out + (static_cast<int64_t>(b) * A.hq + g * A.group + h) * D;
   if (p0 == p1) {  // no tile: nobody wrote the range
     const __nv_bfloat16 zero = __float2bfloat16_rn(apply_epilogue(0.f, A.epi));
-    for (int c = tid; c < D; c += 128) out[c] = zero;
+    for (int c = tid; c < D; c += kMergeThreads) out[c] = zero;
     return;
   }
   const int n = range & 0xffffu;
   if (n == 1) return;  // stored by its worker
   const int64_t rec0 = static_cast<int64_t>(seg) + (range >> 16);
-  auto ml = [&](int r) { return __ldcg(reinterpret_cast<const float2*>(A.rec_ml) + (rec0 + r) * A.group + h); };
-  auto block_reduce = [&](float v, bool maximum) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      const float u = __shfl_xor_sync(0xffffffffu, v, off);
-      v = maximum ? fmaxf(v, u) : v + u;
-    }
-    __syncthreads();
-    if (lane == 0) s_red[warp] = v;
-    __syncthreads();
-    return maximum ? fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]))
-                   : (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]);
-  };
-  float m = -INFINITY;
-  for (int r = tid; r < n; r += 128) m = fmaxf(m, ml(r).x);
-  m = block_reduce(m, true);
-  const float ref = m == -INFINITY ? 0.f : m;
-  float l = 0.f, acc[E];
+  float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
   for (int r0 = 0; r0 < n; r0 += kMergeRecords) {
     const int count = min(kMergeRecords, n - r0);
-    __syncthreads();
-    for (int r = tid; r < count; r += 128) {
-      const float2 v = ml(r0 + r);
-      const float wt = ex2_approx(v.x - ref);
-      s_w[r] = wt;
-      l += wt * v.y;
+    float mine = -INFINITY;
+    for (int r = tid; r < count; r += kMergeThreads) {
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(A.rec_ml) + (rec0 + r0 + r) * A.group + h);
+      s_ml[r] = v;
+      mine = fmaxf(mine, v.x);
     }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mine = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, off));
+    if (lane == 0) s_red[0][warp] = mine;
     __syncthreads();
+    float top = m;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) top = fmaxf(top, s_red[0][w]);
+    const float ref = top == -INFINITY ? 0.f : top;
+    if (r0 > 0) {
+      const float a = ex2_approx(m - ref);
+      l *= a;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= a;
+    }
+    m = top;
 #pragma unroll 8
-    for (int r = warp; r < count; r += 4) {
-      const float wt = s_w[r];
-      const float* src = A.rec_o + ((rec0 + r0 + r) * A.group + h) * D;
+    for (int r = warp; r < count; r += kMergeWarps) {
+      const float2 v = s_ml[r];
+      const float wt = ex2_approx(v.x - ref);
+      l = fmaf(wt, v.y, l);  // the same in every lane
+      const float* src = A.rec_o + ((rec0 + r0 + r) * A.group + h) * D + lane * E;
+      float y[E];
+      if constexpr (E % 4 == 0) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, __ldcg(src + 32 * e + lane), acc[e]);
+        for (int e = 0; e < E; e += 4) *reinterpret_cast<float4*>(y + e) = __ldcg(reinterpret_cast<const float4*>(src + e));
+      } else if constexpr (E == 2) {
+        *reinterpret_cast<float2*>(y) = __ldcg(reinterpret_cast<const float2*>(src));
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = __ldcg(src + e);
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, y[e], acc[e]);
     }
+    __syncthreads();
   }
-  l = block_reduce(l, false);
+  if (lane == 0) s_red[1][warp] = l;
 #pragma unroll
-  for (int e = 0; e < E; ++e) s_o[warp][32 * e + lane] = acc[e];
+  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];
   __syncthreads();
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) l += s_red[1][w];
   const float inv = l > 0.f ? 1.f / l : 0.f;
-  for (int c = tid; c < D; c += 128) {
-    const float y = ((s_o[0][c] + s_o[1][c]) + (s_o[2][c] + s_o[3][c])) * inv;
-    out[c] = __float2bfloat16_rn(apply_epilogue(y, A.epi));
+  for (int c = tid; c < D; c += kMergeThreads) {
+    float y = 0.f;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) y += s_o[w][c];
+    out[c] = __float2bfloat16_rn(apply_epilogue(y * inv, A.epi));
   }
 }
 
@@ -969,7 +985,7 @@ fa_status launch_typed(const fa_decode_params& p, const fa_kv_pages& pg, PageArg
     note_variant(reinterpret_cast<const void*>(merge));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(A.batch * A.hkv * A.group));
-    cfg.blockDim = dim3(128);
+    cfg.blockDim = dim3(kMergeThreads);
     cfg.stream = ctx.stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -2,24 +2,44 @@
 // the scores that each page's per-channel key bounds give.
 //
 //   score(b, g, p) = max_h sum_d max(q_hd lo_d, q_hd hi_d)
+//                  = max_h (q_h+ . hi + q_h- . lo),   q+ = max(q, 0), q- = min(q, 0)
 //
-// Two kernels: the scores of every (sequence, KV head, page), as unsigned keys
-// of the same order, and per (sequence, KV head) the top_k of them.  A product
-// of two bf16 numbers is exact in fp32 (16 bits), and the sum is taken in
-// fp64, so which of two near pages is better does not depend on rounding.
+// Which of two near pages is better must not depend on rounding, so the sum is
+// defined far more exactly than fp32; but only pages next to the k-th best need
+// that.  A cluster of eight CTAs serves one (sequence, KV head):
+//   1. every warp scores 16 pages at a time on mma.sync m16n8k16 (pages on M,
+//      query heads on N, bf16 operands, fp32 sums) together with
+//      A = |q| . max(|lo|, |hi|), which bounds the terms' absolute sum;
+//   2. CTA 0 finds the k-th largest score t.  With e = kError max A every
+//      score is within e of the exact one, so pages above t + 2e are in, pages
+//      below t - 2e are out, and the few between are summed again in fp64
+//      (products of two bf16 numbers are exact) and rounded to fp32 once;
+//   3. the rest of the k is taken from those, the lower page first where
+//      rounded sums are equal, and the pages are written in order.
+// One pass over the bounds, 4 d bytes a page; the selection works on 4 bytes a
+// page out of L2.
+#include "decode_mma.cuh"
 #include "internal.h"
 
 namespace fa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kSelWarps = kThreads / 32;
+constexpr int kCluster = 8;
+constexpr int kBins = 2048;
+// Of A: an fp32 sum on the tensor cores over at most 32 k-steps (d = 256, hi
+// and lo) whose 17 addends may each lose 2^-22 of the largest partial sum
+// (which is at most A): 32 * 17 * 2^-22 < 2^-12.
+constexpr float kError = 1.f / 4096.f;
 
 struct SelectArgs {
   const __nv_bfloat16* q;
   const __nv_bfloat16* bounds;
   const int32_t* seqlens;
   int32_t* selected;
-  uint32_t* keys;  // [batch*hkv][max_pages]
+  float* scores;    // [batch*hkv][max_pages]
+  float* absolute;  // [batch*hkv][kCluster]: largest A of each CTA
   int batch, hq, hkv, group, d, top_k, n_first, n_recent;
   const int32_t* block_table;
   int max_pages, page_size, num_pages;
@@ -27,141 +47,332 @@ struct SelectArgs {
   Watchdog wd;
 };
 
-__device__ __forceinline__ int pages_of(const SelectArgs& A, int b, bool& bad) {
-  const int64_t L = A.seqlens[b];
-  const int64_t c = L < 0 ? 0 : (L > A.capacity ? A.capacity : L);
-  bad = c != L;
-  return static_cast<int>((c + A.page_size - 1) / A.page_size);
-}
-
 // Unsigned key with the order of the float (-0 and +0 equal).
 __device__ __forceinline__ uint32_t order_key(float x) {
   const uint32_t u = __float_as_uint(x + 0.0f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__global__ void __launch_bounds__(kThreads) page_score_kernel(const SelectArgs A) {
-  const int lane = threadIdx.x & 31;
-  const int u = blockIdx.x;  // b * hkv + g
-  const int b = u / A.hkv, g = u % A.hkv;
-  bool bad;
-  const int n = pages_of(A, b, bad);
-  if (bad && threadIdx.x == 0) record_status(A.wd, kStatusRange);
-  const int warps = gridDim.y * (kThreads / 32);
-  for (int p = blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5); p < n; p += warps) {
-    uint32_t key = 0xffffffffu;
-    if (p >= A.n_first && p < n - A.n_recent) {
-      int pg = A.block_table[static_cast<int64_t>(b) * A.max_pages + p];
-      if (pg < 0 || pg >= A.num_pages) {
-        if (lane == 0) record_status(A.wd, kStatusRange);
-        pg = 0;
-      }
-      const __nv_bfloat16* row = A.bounds + (static_cast<int64_t>(pg) * A.hkv + g) * 2 * A.d;
-      float best = -INFINITY;
-      for (int h = 0; h < A.group; ++h) {
-        const __nv_bfloat16* q = A.q + (static_cast<int64_t>(b) * A.hq + g * A.group + h) * A.d;
-        double sum = 0.0;
-        for (int c = lane; c < A.d; c += 32) {
-          const float qv = __bfloat162float(q[c]);
-          sum += fmaxf(qv * __bfloat162float(row[c]), qv * __bfloat162float(row[A.d + c]));
-        }
+__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2_min(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Page ids of a row of the block table; one outside the pool is reported and read as page 0.
+__device__ __forceinline__ int page_id(const SelectArgs& A, int b, int p) {
+  const int pg = A.block_table[static_cast<int64_t>(b) * A.max_pages + p];
+  if (pg >= 0 && pg < A.num_pages) return pg;
+  record_status(A.wd, kStatusRange);
+  return 0;
+}
+
+// Scores of pages first + 16 i .. for one unit; kJ = ceil(d / 32): lane quarter
+// qq holds channels [8 qq + 32 j, +8) of rows gq and gq + 8.
+template <int kJ>
+__device__ __forceinline__ void score_pages(const SelectArgs& A, int u, int b, int g, int lo_page, int hi_page) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, qq = lane & 3;
+  const int rank = static_cast<int>(cluster_ctarank());
+  float most = 0.f;
+  const __nv_bfloat16* q_unit = A.q + (static_cast<int64_t>(b) * A.hq + static_cast<int64_t>(g) * A.group) * A.d;
+  for (int p0 = lo_page + 16 * (rank * kSelWarps + warp); p0 < hi_page; p0 += 16 * kCluster * kSelWarps) {
+    const uint4* row[2];
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        best = fmaxf(best, static_cast<float>(sum));
-      }
-      key = order_key(best);
+    for (int i = 0; i < 2; ++i) {
+      const int p = p0 + gq + 8 * i;
+      row[i] = p < hi_page ? reinterpret_cast<const uint4*>(
+                                 A.bounds + (static_cast<int64_t>(page_id(A, b, p)) * A.hkv + g) * 2 * A.d)
+                           : nullptr;
     }
-    if (lane == 0) A.keys[static_cast<int64_t>(u) * A.max_pages + p] = key;
+    uint4 lo[2][kJ], hi[2][kJ];
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) {
+      const int chunk = qq + 4 * j;
+      const bool there = 8 * chunk < A.d;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bool ok = there && row[i] != nullptr;
+        lo[i][j] = ok ? __ldcs(row[i] + chunk) : make_uint4(0, 0, 0, 0);
+        hi[i][j] = ok ? __ldcs(row[i] + A.d / 8 + chunk) : make_uint4(0, 0, 0, 0);
+      }
+    }
+    float best[2] = {-INFINITY, -INFINITY};
+    for (int h0 = 0; h0 < A.group; h0 += 8) {  // eight query heads at a time
+      float s[4] = {0.f, 0.f, 0.f, 0.f}, t[4] = {0.f, 0.f, 0.f, 0.f};
+      const bool head_ok = h0 + gq < A.group;
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) {
+        const int chunk = qq + 4 * j;
+        uint4 qv = make_uint4(0, 0, 0, 0);
+        if (head_ok && 8 * chunk < A.d)
+          qv = *(reinterpret_cast<const uint4*>(q_unit + static_cast<int64_t>(h0 + gq) * A.d) + chunk);
+        const uint32_t qr[4] = {qv.x, qv.y, qv.z, qv.w};
+        const uint32_t lr[2][4] = {{lo[0][j].x, lo[0][j].y, lo[0][j].z, lo[0][j].w},
+                                   {lo[1][j].x, lo[1][j].y, lo[1][j].z, lo[1][j].w}};
+        const uint32_t hr[2][4] = {{hi[0][j].x, hi[0][j].y, hi[0][j].z, hi[0][j].w},
+                                   {hi[1][j].x, hi[1][j].y, hi[1][j].z, hi[1][j].w}};
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          const uint32_t h4[4] = {hr[0][e], hr[1][e], hr[0][e + 1], hr[1][e + 1]};
+          const uint32_t l4[4] = {lr[0][e], lr[1][e], lr[0][e + 1], lr[1][e + 1]};
+          mma16816_bf16(s, h4, bf16x2_max(qr[e], 0u), bf16x2_max(qr[e + 1], 0u));
+          mma16816_bf16(s, l4, bf16x2_min(qr[e], 0u), bf16x2_min(qr[e + 1], 0u));
+          uint32_t a4[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) a4[x] = bf16x2_max(h4[x] & 0x7fff7fffu, l4[x] & 0x7fff7fffu);
+          mma16816_bf16(t, a4, qr[e] & 0x7fff7fffu, qr[e + 1] & 0x7fff7fffu);
+        }
+      }
+      // rows gq, gq + 8; heads h0 + 2 qq, + 1
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if (h0 + 2 * qq + (x & 1) < A.group) best[x >> 1] = fmaxf(best[x >> 1], s[x]);
+        most = fmaxf(most, t[x]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      best[i] = fmaxf(best[i], __shfl_xor_sync(0xffffffffu, best[i], 1));
+      best[i] = fmaxf(best[i], __shfl_xor_sync(0xffffffffu, best[i], 2));
+      const int p = p0 + gq + 8 * i;
+      if (qq == 0 && p < hi_page) A.scores[static_cast<int64_t>(u) * A.max_pages + p] = best[i];
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+  __shared__ float s_most[kSelWarps];
+  if (lane == 0) s_most[warp] = most;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kSelWarps; ++w) most = fmaxf(most, s_most[w]);
+    A.absolute[static_cast<int64_t>(u) * kCluster + rank] = most;
   }
 }
 
-// The top_k keys of one (sequence, KV head): radix selection of the k-th
-// largest key, eight bits a pass, then the pages above it and the first of
-// those equal to it, in page order.
-__global__ void __launch_bounds__(kThreads) page_pick_kernel(const SelectArgs A) {
-  __shared__ int hist[256];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_need;
-  __shared__ int s_above[kThreads / 32], s_equal[kThreads / 32];
+// The exact score of page p by one warp: fp64 sums of exact products, rounded once.
+__device__ float exact_score(const SelectArgs& A, int b, int g, int p) {
+  const int lane = threadIdx.x & 31;
+  const __nv_bfloat16* row = A.bounds + (static_cast<int64_t>(page_id(A, b, p)) * A.hkv + g) * 2 * A.d;
+  float best = -INFINITY;
+  for (int h = 0; h < A.group; ++h) {
+    const __nv_bfloat16* q = A.q + (static_cast<int64_t>(b) * A.hq + static_cast<int64_t>(g) * A.group + h) * A.d;
+    double sum = 0.0;
+    for (int c = lane; c < A.d; c += 32) {
+      const float qv = __bfloat162float(q[c]);
+      sum += fmaxf(qv * __bfloat162float(row[c]), qv * __bfloat162float(row[A.d + c]));
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    best = fmaxf(best, static_cast<float>(sum));
+  }
+  return best;
+}
+
+struct PickShared {
+  int hist[kBins];
+  int warp_sum[kSelWarps];
+  uint32_t warp_lo[kSelWarps], warp_hi[kSelWarps];
+  int bin, above;
+};
+
+// Exclusive sum over the block's threads, and the total.
+__device__ __forceinline__ int block_scan(PickShared& S, int v, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += x;
+  }
+  __syncthreads();
+  if (lane == 31) S.warp_sum[warp] = incl;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kSelWarps; ++w) {
+    if (w < warp) before += S.warp_sum[w];
+    total += S.warp_sum[w];
+  }
+  return before + incl - v;
+}
+
+// The need-th largest (1-based) of m keys key(i), and how many keys are above
+// it: rounds of a histogram over the range that holds it, 2048 bins each (at
+// most three rounds), the whole block together.
+template <typename K>
+__device__ __forceinline__ uint32_t kth_largest(PickShared& S, int m, int need, K key, int& above) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int u = blockIdx.x;
-  bool bad;
-  const int n = pages_of(A, u / A.hkv, bad);
-  const uint32_t* keys = A.keys + static_cast<int64_t>(u) * A.max_pages;
+  uint32_t lo = 0xffffffffu, hi = 0;
+  for (int i = tid; i < m; i += kThreads) {
+    const uint32_t k = key(i);
+    lo = min(lo, k);
+    hi = max(hi, k);
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) {
+    S.warp_lo[warp] = lo;
+    S.warp_hi[warp] = hi;
+  }
+  __syncthreads();
+  for (int w = 0; w < kSelWarps; ++w) {
+    lo = min(lo, S.warp_lo[w]);
+    hi = max(hi, S.warp_hi[w]);
+  }
+  above = 0;
+  while (true) {
+    const int bits = 32 - __clz(hi - lo);
+    const int shift = bits > 11 ? bits - 11 : 0;
+    for (int i = tid; i < kBins; i += kThreads) S.hist[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < m; i += kThreads) {
+      const uint32_t k = key(i);
+      if (k >= lo && k <= hi) atomicAdd(&S.hist[(k - lo) >> shift], 1);
+    }
+    __syncthreads();
+    // the bin of the need-th key, counted from the top: thread t has bins
+    // [kBins - 8 (t + 1), kBins - 8 t)
+    constexpr int kPer = kBins / kThreads;
+    int own = 0;
+    const int top = kBins - kPer * tid;
+#pragma unroll
+    for (int j = 1; j <= kPer; ++j) own += S.hist[top - j];
+    int total, before = above + block_scan(S, own, total);
+    if (before < need && before + own >= need) {
+      int j = 1;
+      while (before + S.hist[top - j] < need) before += S.hist[top - j++];
+      S.bin = top - j;
+      S.above = before;
+    }
+    __syncthreads();
+    above = S.above;
+    lo += static_cast<uint32_t>(S.bin) << shift;
+    if (shift == 0) return lo;
+    const uint32_t width = (1u << shift) - 1u;
+    if (hi - lo > width) hi = lo + width;
+    __syncthreads();
+  }
+}
+
+// CTA 0 of the cluster: the top_k of pages 0 .. n - 1, of which [lo, hi) have scores.
+__device__ __forceinline__ void pick_pages(const SelectArgs& A, PickShared& S, int u, int b, int g, int n, int lo,
+                                           int hi) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int m = hi - lo, need = A.top_k - (n - m);  // of the pages with scores
+  float* scores = A.scores + static_cast<int64_t>(u) * A.max_pages + lo;
   int32_t* out = A.selected + static_cast<int64_t>(u) * A.top_k;
-  if (n <= A.top_k) {
-    for (int i = tid; i < A.top_k; i += kThreads) out[i] = i < n ? i : -1;
+  uint32_t kth = 0xffffffffu;
+  int ties = 0;
+  if (need > 0) {
+    float e = 0.f;
+    for (int r = 0; r < kCluster; ++r) e = fmaxf(e, __ldcg(A.absolute + static_cast<int64_t>(u) * kCluster + r));
+    e *= 2.f * kError;
+    int above;
+    const uint32_t near = kth_largest(S, m, need, [&](int i) { return order_key(__ldcg(scores + i)); }, above);
+    const float t = __uint_as_float((near & 0x80000000u) ? near ^ 0x80000000u : ~near);
+    // in: +inf, out: -inf, between: the exact score (infinite bounds leave every page between)
+    __syncthreads();
+    for (int i0 = 32 * warp; i0 < m; i0 += kThreads) {
+      const int i = i0 + lane;
+      float v = i < m ? __ldcg(scores + i) : -INFINITY;
+      const bool in = v > t + e, gone = i >= m || v < t - e;
+      unsigned between = __ballot_sync(0xffffffffu, !in && !gone);
+      if (in) v = INFINITY;
+      if (gone) v = -INFINITY;
+      while (between != 0) {
+        const int l = __ffs(between) - 1;
+        between &= between - 1;
+        const float x = exact_score(A, b, g, lo + i0 + l);
+        if (lane == l) v = x;
+      }
+      if (i < m) __stcg(scores + i, v);
+    }
+    __syncthreads();
+    kth = kth_largest(S, m, need, [&](int i) { return order_key(__ldcg(scores + i)); }, above);
+    ties = need - above;
+  }
+  // in page order: the pages without scores, those above the k-th, and the first `ties` equal to it
+  __syncthreads();
+  const int per = (n + kThreads - 1) / kThreads;
+  const int p0 = min(n, tid * per), p1 = min(n, p0 + per);
+  int above = 0, equal = 0, total;
+  for (int p = p0; p < p1; ++p) {
+    if (p < lo || p >= hi) {
+      ++above;
+    } else if (need > 0) {
+      const uint32_t k = order_key(__ldcg(scores + p - lo));
+      above += k > kth;
+      equal += k == kth;
+    }
+  }
+  int at = block_scan(S, above, total);
+  int tied = block_scan(S, equal, total);
+  at += min(tied, ties);
+  for (int p = p0; p < p1; ++p) {
+    bool take = p < lo || p >= hi;
+    if (!take && need > 0) {
+      const uint32_t k = order_key(__ldcg(scores + p - lo));
+      take = k > kth || (k == kth && tied++ < ties);
+    }
+    if (take) out[at++] = p;
+  }
+}
+
+template <int kJ>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) page_select_kernel(const SelectArgs A) {
+  __shared__ PickShared S;
+  const int u = blockIdx.x / kCluster, b = u / A.hkv, g = u % A.hkv;
+  const int64_t Lr = A.seqlens[b];
+  const int64_t L = Lr < 0 ? 0 : (Lr > A.capacity ? A.capacity : Lr);
+  const int n = static_cast<int>((L + A.page_size - 1) / A.page_size);
+  const bool first = cluster_ctarank() == 0;
+  if (L != Lr && first && threadIdx.x == 0) record_status(A.wd, kStatusRange);
+  if (n <= A.top_k) {  // the same for the whole cluster
+    if (first) {
+      int32_t* out = A.selected + static_cast<int64_t>(u) * A.top_k;
+      for (int i = threadIdx.x; i < A.top_k; i += kThreads) out[i] = i < n ? i : -1;
+    }
     return;
   }
-  if (tid == 0) {
-    s_prefix = 0;
-    s_need = A.top_k;
-  }
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kThreads) hist[i] = 0;
-    __syncthreads();
-    const uint32_t prefix = s_prefix;
-    const uint32_t above = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-    for (int i = tid; i < n; i += kThreads) {
-      const uint32_t k = keys[i];
-      if ((k & above) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1);
-    }
-    __syncthreads();
-    if (tid == 0) {
-      int need = s_need, bin = 255;
-      while (bin > 0 && hist[bin] < need) need -= hist[bin--];
-      s_need = need;
-      s_prefix = prefix | (static_cast<uint32_t>(bin) << shift);
-    }
-    __syncthreads();
-  }
-  const uint32_t kth = s_prefix;
-  const int ties = s_need;  // pages equal to the k-th key that are kept
-  int written = 0, tied = 0;
-  for (int i0 = 0; i0 < n; i0 += kThreads) {
-    const int i = i0 + tid;
-    const uint32_t k = i < n ? keys[i] : 0u;
-    const bool above = i < n && k > kth, equal = i < n && k == kth;
-    const unsigned ma = __ballot_sync(0xffffffffu, above), me = __ballot_sync(0xffffffffu, equal);
-    if (lane == 0) {
-      s_above[warp] = __popc(ma);
-      s_equal[warp] = __popc(me);
-    }
-    __syncthreads();
-    int na = 0, ne = 0, ta = 0, te = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) {
-        na += s_above[w];
-        ne += s_equal[w];
-      }
-      ta += s_above[w];
-      te += s_equal[w];
-    }
-    const unsigned below = (1u << lane) - 1u;
-    na += __popc(ma & below);
-    ne += __popc(me & below);
-    const int room = ties - tied;  // ties still kept before this block
-    const int at = written + na + min(ne, room);
-    if (above || (equal && ne < room)) out[at] = i;
-    written += ta + min(te, room);
-    tied += min(te, room);
-    __syncthreads();
-  }
+  const int lo = A.n_first, hi = n - A.n_recent;  // lo + n_recent <= top_k < n
+  score_pages<kJ>(A, u, b, g, lo, hi);
+  cluster_sync_all();  // the cluster's scores are visible to CTA 0
+  if (first) pick_pages(A, S, u, b, g, n, lo, hi);
+}
+
+template <int kJ>
+fa_status launch_width(const SelectArgs& A, const LaunchCtx& ctx) {
+  note_variant(reinterpret_cast<const void*>(page_select_kernel<kJ>));
+  page_select_kernel<kJ><<<static_cast<unsigned>(A.batch * A.hkv * kCluster), kThreads, 0, ctx.stream>>>(A);
+  return cuda_status(cudaGetLastError());
+}
+
+size_t scores_bytes(int batch, int hkv, int max_pages) {
+  return (static_cast<size_t>(batch) * hkv * max_pages * sizeof(float) + 15) / 16 * 16;
 }
 
 }  // namespace
 
 size_t page_select_workspace_bytes(int batch, int hkv, int max_pages) {
-  return (static_cast<size_t>(batch) * hkv * max_pages * sizeof(uint32_t) + 15) / 16 * 16;
+  return scores_bytes(batch, hkv, max_pages) + static_cast<size_t>(batch) * hkv * kCluster * sizeof(float);
 }
 
 fa_status launch_page_select(const fa_page_select_params& p, const fa_kv_pages& pages, const LaunchCtx& ctx) {
+  if (static_cast<int64_t>(p.batch) * p.hkv * kCluster >= (int64_t(1) << 31)) return FA_ERR_UNSUPPORTED;
   SelectArgs A;
   A.q = static_cast<const __nv_bfloat16*>(p.q);
   A.bounds = static_cast<const __nv_bfloat16*>(p.key_bounds);
   A.seqlens = p.cache_seqlens;
   A.selected = p.selected;
-  A.keys = static_cast<uint32_t*>(p.workspace);
+  A.scores = static_cast<float*>(p.workspace);
+  A.absolute = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) +
+                                        scores_bytes(p.batch, p.hkv, pages.max_pages));
   A.batch = p.batch;
   A.hq = p.hq;
   A.hkv = p.hkv;
@@ -176,16 +387,10 @@ fa_status launch_page_select(const fa_page_select_params& p, const fa_kv_pages& 
   A.num_pages = pages.num_pages;
   A.capacity = static_cast<int64_t>(pages.max_pages) * pages.page_size;
   A.wd = ctx.wd;
-  const int units = p.batch * p.hkv;
-  int chunks = (pages.max_pages + kThreads / 32 - 1) / (kThreads / 32);
-  const int most = (device_sm_count() * 16 + units - 1) / units;
-  if (chunks > most) chunks = most;
-  note_variant(reinterpret_cast<const void*>(page_score_kernel));
-  page_score_kernel<<<dim3(units, chunks), kThreads, 0, ctx.stream>>>(A);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  note_variant(reinterpret_cast<const void*>(page_pick_kernel));
-  page_pick_kernel<<<units, kThreads, 0, ctx.stream>>>(A);
-  return cuda_status(cudaGetLastError());
+  if (p.head_dim <= 32) return launch_width<1>(A, ctx);
+  if (p.head_dim <= 64) return launch_width<2>(A, ctx);
+  if (p.head_dim <= 128) return launch_width<4>(A, ctx);
+  return launch_width<8>(A, ctx);
 }
 
 }  // namespace fa
