@@ -10,10 +10,11 @@
 //   1. every warp scores 16 pages at a time on mma.sync m16n8k16 (pages on M,
 //      query heads on N, bf16 operands, fp32 sums) together with
 //      A = |q| . max(|lo|, |hi|), which bounds the terms' absolute sum;
-//   2. CTA 0 finds the k-th largest score t.  With e = kError max A every
-//      score is within e of the exact one, so pages above t + 2e are in, pages
-//      below t - 2e are out, and the few between are summed again in fp64
-//      (products of two bf16 numbers are exact) and rounded to fp32 once;
+//   2. CTA 0 finds a narrow range [t0, t1] that holds the k-th largest score.
+//      With e = kError max A every score is within e of the exact one, so pages
+//      above t1 + 2e are in, pages below t0 - 2e are out, and the few between
+//      are summed again in fp64 (products of two bf16 numbers are exact) and
+//      rounded to fp32 once;
 //   3. the rest of the k is taken from those, the lower page first where
 //      rounded sums are equal, and the pages are written in order.
 // One pass over the bounds, 4 d bytes a page; the selection works on 4 bytes a
@@ -173,11 +174,17 @@ __device__ float exact_score(const SelectArgs& A, int b, int g, int p) {
   return best;
 }
 
+constexpr int kHeld = 4096;    // scores CTA 0 holds in shared memory (more stay in L2)
+constexpr int kBetween = 256;  // pages next to the border that are ranked directly
+
 struct PickShared {
   int hist[kBins];
+  float scores[kHeld];
+  int between[kBetween];
+  uint32_t exact[kBetween];
   int warp_sum[kSelWarps];
   uint32_t warp_lo[kSelWarps], warp_hi[kSelWarps];
-  int bin, above;
+  int bin, above, inside, n_between;
 };
 
 // Exclusive sum over the block's threads, and the total.
@@ -202,13 +209,16 @@ __device__ __forceinline__ int block_scan(PickShared& S, int v, int& total) {
   return before + incl - v;
 }
 
-// The need-th largest (1-based) of m keys key(i), and how many keys are above
-// it: rounds of a histogram over the range that holds it, 2048 bins each (at
-// most three rounds), the whole block together.
+// A range [lo, hi] of keys that holds the need-th largest (1-based) of m keys
+// key(i), and how many keys are above it: rounds of a histogram over the range
+// found so far, 2048 bins each, the whole block together, until at most
+// `few` keys are left in it or it is one key wide (at most three rounds).
 template <typename K>
-__device__ __forceinline__ uint32_t kth_largest(PickShared& S, int m, int need, K key, int& above) {
+__device__ __forceinline__ void kth_range(PickShared& S, int m, int need, int few, K key, uint32_t& lo, uint32_t& hi,
+                                          int& above) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint32_t lo = 0xffffffffu, hi = 0;
+  lo = 0xffffffffu;
+  hi = 0;
   for (int i = tid; i < m; i += kThreads) {
     const uint32_t k = key(i);
     lo = min(lo, k);
@@ -220,7 +230,9 @@ __device__ __forceinline__ uint32_t kth_largest(PickShared& S, int m, int need, 
     S.warp_lo[warp] = lo;
     S.warp_hi[warp] = hi;
   }
+  for (int i = tid; i < kBins; i += kThreads) S.hist[i] = 0;
   __syncthreads();
+#pragma unroll
   for (int w = 0; w < kSelWarps; ++w) {
     lo = min(lo, S.warp_lo[w]);
     hi = max(hi, S.warp_hi[w]);
@@ -229,8 +241,6 @@ __device__ __forceinline__ uint32_t kth_largest(PickShared& S, int m, int need, 
   while (true) {
     const int bits = 32 - __clz(hi - lo);
     const int shift = bits > 11 ? bits - 11 : 0;
-    for (int i = tid; i < kBins; i += kThreads) S.hist[i] = 0;
-    __syncthreads();
     for (int i = tid; i < m; i += kThreads) {
       const uint32_t k = key(i);
       if (k >= lo && k <= hi) atomicAdd(&S.hist[(k - lo) >> shift], 1);
@@ -249,15 +259,21 @@ __device__ __forceinline__ uint32_t kth_largest(PickShared& S, int m, int need, 
       while (before + S.hist[top - j] < need) before += S.hist[top - j++];
       S.bin = top - j;
       S.above = before;
+      S.inside = S.hist[top - j];
     }
     __syncthreads();
     above = S.above;
     lo += static_cast<uint32_t>(S.bin) << shift;
-    if (shift == 0) return lo;
     const uint32_t width = (1u << shift) - 1u;
     if (hi - lo > width) hi = lo + width;
+    if (shift == 0 || S.inside <= few) return;
+    for (int i = tid; i < kBins; i += kThreads) S.hist[i] = 0;
     __syncthreads();
   }
+}
+
+__device__ __forceinline__ float key_float(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
 }
 
 // CTA 0 of the cluster: the top_k of pages 0 .. n - 1, of which [lo, hi) have scores.
@@ -265,40 +281,74 @@ __device__ __forceinline__ void pick_pages(const SelectArgs& A, PickShared& S, i
                                            int hi) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int m = hi - lo, need = A.top_k - (n - m);  // of the pages with scores
-  float* scores = A.scores + static_cast<int64_t>(u) * A.max_pages + lo;
+  float* stored = A.scores + static_cast<int64_t>(u) * A.max_pages + lo;
+  float* sc = m <= kHeld ? S.scores : stored;
   int32_t* out = A.selected + static_cast<int64_t>(u) * A.top_k;
-  uint32_t kth = 0xffffffffu;
+  uint32_t kth = 0xffffffffu;  // pages above this key are taken, and the first `ties` equal to it
   int ties = 0;
   if (need > 0) {
     float e = 0.f;
+#pragma unroll
     for (int r = 0; r < kCluster; ++r) e = fmaxf(e, __ldcg(A.absolute + static_cast<int64_t>(u) * kCluster + r));
     e *= 2.f * kError;
-    int above;
-    const uint32_t near = kth_largest(S, m, need, [&](int i) { return order_key(__ldcg(scores + i)); }, above);
-    const float t = __uint_as_float((near & 0x80000000u) ? near ^ 0x80000000u : ~near);
-    // in: +inf, out: -inf, between: the exact score (infinite bounds leave every page between)
+    if (sc != stored) {
+      for (int i = tid; i < m; i += kThreads) sc[i] = __ldcg(stored + i);
+    }
+    if (tid == 0) S.n_between = 0;
     __syncthreads();
-    for (int i0 = 32 * warp; i0 < m; i0 += kThreads) {
-      const int i = i0 + lane;
-      float v = i < m ? __ldcg(scores + i) : -INFINITY;
-      const bool in = v > t + e, gone = i >= m || v < t - e;
-      unsigned between = __ballot_sync(0xffffffffu, !in && !gone);
-      if (in) v = INFINITY;
-      if (gone) v = -INFINITY;
-      while (between != 0) {
-        const int l = __ffs(between) - 1;
-        between &= between - 1;
-        const float x = exact_score(A, b, g, lo + i0 + l);
-        if (lane == l) v = x;
+    uint32_t k0, k1;
+    int above;
+    kth_range(S, m, need, 8, [&](int i) { return order_key(sc[i]); }, k0, k1, above);
+    // in: +inf, out: -inf, between: to be summed exactly
+    const float in_from = key_float(k1) + e, out_to = key_float(k0) - e;
+    int in = 0;
+    for (int i = tid; i < m; i += kThreads) {
+      const float v = sc[i];
+      if (v > in_from) {
+        ++in;
+        sc[i] = INFINITY;
+      } else if (v < out_to) {
+        sc[i] = -INFINITY;
+      } else {
+        const int at = atomicAdd(&S.n_between, 1);
+        if (at < kBetween) S.between[at] = i;
       }
-      if (i < m) __stcg(scores + i, v);
+    }
+    int taken;
+    block_scan(S, in, taken);
+    const int n_between = S.n_between;
+    if (n_between <= kBetween) {
+      for (int c = warp; c < n_between; c += kSelWarps) {
+        const float x = exact_score(A, b, g, lo + S.between[c]);
+        if (lane == 0) S.exact[c] = order_key(x);
+      }
+      __syncthreads();
+      for (int c = tid; c < n_between; c += kThreads) {
+        const uint32_t k = S.exact[c];
+        const int i = S.between[c];
+        int better = 0;
+        for (int o = 0; o < n_between; ++o) better += S.exact[o] > k || (S.exact[o] == k && S.between[o] < i);
+        sc[i] = better < need - taken ? INFINITY : -INFINITY;
+      }
+      kth = order_key(0.f);
+    } else {
+      // many equal or nearly equal pages: all exactly, then a second selection
+      for (int i0 = 32 * warp; i0 < m; i0 += kThreads) {
+        const float v = i0 + lane < m ? sc[i0 + lane] : INFINITY;
+        for (unsigned left = __ballot_sync(0xffffffffu, fabsf(v) != INFINITY); left != 0; left &= left - 1) {
+          const int i = i0 + __ffs(left) - 1;
+          const float x = exact_score(A, b, g, lo + i);
+          if (lane == 0) sc[i] = x;
+        }
+      }
+      __syncthreads();
+      kth_range(S, m, need, 0, [&](int i) { return order_key(sc[i]); }, k0, k1, above);
+      kth = k0;
+      ties = need - above;
     }
     __syncthreads();
-    kth = kth_largest(S, m, need, [&](int i) { return order_key(__ldcg(scores + i)); }, above);
-    ties = need - above;
   }
   // in page order: the pages without scores, those above the k-th, and the first `ties` equal to it
-  __syncthreads();
   const int per = (n + kThreads - 1) / kThreads;
   const int p0 = min(n, tid * per), p1 = min(n, p0 + per);
   int above = 0, equal = 0, total;
@@ -306,18 +356,20 @@ __device__ __forceinline__ void pick_pages(const SelectArgs& A, PickShared& S, i
     if (p < lo || p >= hi) {
       ++above;
     } else if (need > 0) {
-      const uint32_t k = order_key(__ldcg(scores + p - lo));
+      const uint32_t k = order_key(sc[p - lo]);
       above += k > kth;
       equal += k == kth;
     }
   }
-  int at = block_scan(S, above, total);
-  int tied = block_scan(S, equal, total);
-  at += min(tied, ties);
+  int at = block_scan(S, above, total), tied = 0;
+  if (ties > 0) {  // the same for the whole block
+    tied = block_scan(S, equal, total);
+    at += min(tied, ties);
+  }
   for (int p = p0; p < p1; ++p) {
     bool take = p < lo || p >= hi;
     if (!take && need > 0) {
-      const uint32_t k = order_key(__ldcg(scores + p - lo));
+      const uint32_t k = order_key(sc[p - lo]);
       take = k > kth || (k == kth && tied++ < ties);
     }
     if (take) out[at++] = p;

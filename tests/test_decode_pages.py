@@ -163,6 +163,35 @@ def test_select_ties_go_to_the_lowest_page():
     assert got.cpu().tolist() == [[[0, 1, 2, 3, 38, 39]]]
 
 
+@pytest.mark.parametrize("pages,top", [(700, 300), (5000, 40), (5000, 4000)])
+def test_select_among_many_equal_pages(pages, top):
+    """More pages next to the border than are ranked directly, and more than are held in shared memory."""
+    fa = _fa()
+    c = plain.Cache(122, "bf16", [32], 1, 64, 32, spare=1).cuda()
+    c.lens = [32 * pages]
+    g = torch.Generator().manual_seed(pages)
+    c.bounds = (torch.randint(0, 3, (pages, 1, 2, 64), generator=g) == 0).bfloat16()
+    c.bounds[:, :, 0] = -c.bounds[:, :, 0]
+    c.bounds[::3] = c.bounds[0]
+    c.table = torch.randperm(pages, generator=g).int()[None]
+    q = torch.where(torch.arange(64) % 2 == 0, 1.0, -1.0).bfloat16()[None]
+    got = fa.page_select(q.cuda(), c.bounds.cuda(), torch.tensor(c.lens, dtype=torch.int32).cuda(), c.table.cuda(), hq=1,
+                         hkv=1, page_size=32, top_k=top, n_first=1, n_recent=1)
+    assert np.array_equal(got.cpu().numpy(), plain.select(c, q.double().numpy().reshape(1, 1, 64), 1, top, 1, 1))
+
+
+def test_select_with_infinite_bounds_stays_inside():
+    """An unspecified choice, but of the sequence's pages, ascending and distinct."""
+    fa = _fa()
+    c = plain.Cache(123, "bf16", [32 * 300], 2, 64, 32)
+    c.bounds[::5, 0, 1] = float("inf")
+    c.bounds[::7, 1] = float("nan")
+    c.cuda()
+    got = fa.page_select(_queries(123, 1, 4, 64).cuda(), c.bounds_, c.lens_, c.table_, hq=4, hkv=2, page_size=32, top_k=50)
+    for row in got[0].tolist():
+        assert row == sorted(set(row)) and 0 <= row[0] and row[-1] == 299 and len(row) == 50
+
+
 def test_select_near_ties_are_told_apart():
     """Two pages whose scores differ by less than fp32 sums of their terms are good for."""
     fa = _fa()
