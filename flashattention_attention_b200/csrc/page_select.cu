@@ -6,7 +6,7 @@
 //
 // Which of two near pages is better must not depend on rounding, so the sum is
 // defined far more exactly than fp32; but only pages next to the k-th best need
-// that.  A cluster of eight CTAs serves one (sequence, KV head):
+// that.  A cluster of one to eight CTAs serves one (sequence, KV head):
 //   1. every warp scores 16 pages at a time on mma.sync m16n8k16 (pages on M,
 //      query heads on N, bf16 operands, fp32 sums) together with
 //      A = |q| . max(|lo|, |hi|), which bounds the terms' absolute sum;
@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kSelWarps = kThreads / 32;
-constexpr int kCluster = 8;
+constexpr int kMaxCluster = 8;
 constexpr int kBins = 2048;
 // Of A: an fp32 sum on the tensor cores over at most 32 k-steps (d = 256, hi
 // and lo) whose 17 addends may each lose 2^-22 of the largest partial sum
@@ -40,7 +40,7 @@ struct SelectArgs {
   const int32_t* seqlens;
   int32_t* selected;
   float* scores;    // [batch*hkv][max_pages]
-  float* absolute;  // [batch*hkv][kCluster]: largest A of each CTA
+  float* absolute;  // [batch*hkv][kMaxCluster]: largest A of each CTA
   int batch, hq, hkv, group, d, top_k, n_first, n_recent;
   const int32_t* block_table;
   int max_pages, page_size, num_pages;
@@ -79,17 +79,19 @@ template <int kJ>
 __device__ __forceinline__ void score_pages(const SelectArgs& A, int u, int b, int g, int lo_page, int hi_page) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, qq = lane & 3;
   const int rank = static_cast<int>(cluster_ctarank());
+  const int stride = 16 * static_cast<int>(cluster_size()) * kSelWarps;
   float most = 0.f;
   const __nv_bfloat16* q_unit = A.q + (static_cast<int64_t>(b) * A.hq + static_cast<int64_t>(g) * A.group) * A.d;
-  for (int p0 = lo_page + 16 * (rank * kSelWarps + warp); p0 < hi_page; p0 += 16 * kCluster * kSelWarps) {
+  int p0 = lo_page + 16 * (rank * kSelWarps + warp);
+  int pg[2];  // the lane's two pages, looked up one round ahead
+#pragma unroll
+  for (int i = 0; i < 2; ++i) pg[i] = p0 + gq + 8 * i < hi_page ? page_id(A, b, p0 + gq + 8 * i) : -1;
+  for (; p0 < hi_page; p0 += stride) {
     const uint4* row[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int p = p0 + gq + 8 * i;
-      row[i] = p < hi_page ? reinterpret_cast<const uint4*>(
-                                 A.bounds + (static_cast<int64_t>(page_id(A, b, p)) * A.hkv + g) * 2 * A.d)
-                           : nullptr;
-    }
+    for (int i = 0; i < 2; ++i)
+      row[i] = pg[i] >= 0 ? reinterpret_cast<const uint4*>(A.bounds + (static_cast<int64_t>(pg[i]) * A.hkv + g) * 2 * A.d)
+                          : nullptr;
     uint4 lo[2][kJ], hi[2][kJ];
 #pragma unroll
     for (int j = 0; j < kJ; ++j) {
@@ -101,6 +103,11 @@ __device__ __forceinline__ void score_pages(const SelectArgs& A, int u, int b, i
         lo[i][j] = ok ? __ldcs(row[i] + chunk) : make_uint4(0, 0, 0, 0);
         hi[i][j] = ok ? __ldcs(row[i] + A.d / 8 + chunk) : make_uint4(0, 0, 0, 0);
       }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int p = p0 + stride + gq + 8 * i;
+      pg[i] = p < hi_page ? page_id(A, b, p) : -1;
     }
     float best[2] = {-INFINITY, -INFINITY};
     for (int h0 = 0; h0 < A.group; h0 += 8) {  // eight query heads at a time
@@ -151,7 +158,7 @@ __device__ __forceinline__ void score_pages(const SelectArgs& A, int u, int b, i
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int w = 1; w < kSelWarps; ++w) most = fmaxf(most, s_most[w]);
-    A.absolute[static_cast<int64_t>(u) * kCluster + rank] = most;
+    A.absolute[static_cast<int64_t>(u) * kMaxCluster + rank] = most;
   }
 }
 
@@ -288,8 +295,8 @@ __device__ __forceinline__ void pick_pages(const SelectArgs& A, PickShared& S, i
   int ties = 0;
   if (need > 0) {
     float e = 0.f;
-#pragma unroll
-    for (int r = 0; r < kCluster; ++r) e = fmaxf(e, __ldcg(A.absolute + static_cast<int64_t>(u) * kCluster + r));
+    for (int r = 0; r < static_cast<int>(cluster_size()); ++r)
+      e = fmaxf(e, __ldcg(A.absolute + static_cast<int64_t>(u) * kMaxCluster + r));
     e *= 2.f * kError;
     if (sc != stored) {
       for (int i = tid; i < m; i += kThreads) sc[i] = __ldcg(stored + i);
@@ -377,9 +384,9 @@ __device__ __forceinline__ void pick_pages(const SelectArgs& A, PickShared& S, i
 }
 
 template <int kJ>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) page_select_kernel(const SelectArgs A) {
+__global__ void __launch_bounds__(kThreads, kJ == 8 ? 1 : 2) page_select_kernel(const SelectArgs A) {
   __shared__ PickShared S;
-  const int u = blockIdx.x / kCluster, b = u / A.hkv, g = u % A.hkv;
+  const int u = blockIdx.x / cluster_size(), b = u / A.hkv, g = u % A.hkv;
   const int64_t Lr = A.seqlens[b];
   const int64_t L = Lr < 0 ? 0 : (Lr > A.capacity ? A.capacity : Lr);
   const int n = static_cast<int>((L + A.page_size - 1) / A.page_size);
@@ -398,11 +405,27 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) pag
   if (first) pick_pages(A, S, u, b, g, n, lo, hi);
 }
 
+// As many CTAs per cluster as the device holds at once (two CTAs per SM): few
+// units are scored faster by many CTAs, many units better by a CTA each than
+// in turns (128 units of 1024 pages on 148 SMs: 36 us with eight, XX with two).
 template <int kJ>
 fa_status launch_width(const SelectArgs& A, const LaunchCtx& ctx) {
+  const int64_t units = static_cast<int64_t>(A.batch) * A.hkv;
+  const int64_t most = static_cast<int64_t>(device_sm_count()) * (kJ == 8 ? 1 : 2);
+  int cluster = 1;
+  while (cluster < kMaxCluster && units * cluster * 2 <= most) cluster *= 2;
   note_variant(reinterpret_cast<const void*>(page_select_kernel<kJ>));
-  page_select_kernel<kJ><<<static_cast<unsigned>(A.batch * A.hkv * kCluster), kThreads, 0, ctx.stream>>>(A);
-  return cuda_status(cudaGetLastError());
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(units * cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = ctx.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, page_select_kernel<kJ>, A));
 }
 
 size_t scores_bytes(int batch, int hkv, int max_pages) {
@@ -412,11 +435,11 @@ size_t scores_bytes(int batch, int hkv, int max_pages) {
 }  // namespace
 
 size_t page_select_workspace_bytes(int batch, int hkv, int max_pages) {
-  return scores_bytes(batch, hkv, max_pages) + static_cast<size_t>(batch) * hkv * kCluster * sizeof(float);
+  return scores_bytes(batch, hkv, max_pages) + static_cast<size_t>(batch) * hkv * kMaxCluster * sizeof(float);
 }
 
 fa_status launch_page_select(const fa_page_select_params& p, const fa_kv_pages& pages, const LaunchCtx& ctx) {
-  if (static_cast<int64_t>(p.batch) * p.hkv * kCluster >= (int64_t(1) << 31)) return FA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(p.batch) * p.hkv >= (int64_t(1) << 31)) return FA_ERR_UNSUPPORTED;
   SelectArgs A;
   A.q = static_cast<const __nv_bfloat16*>(p.q);
   A.bounds = static_cast<const __nv_bfloat16*>(p.key_bounds);
