@@ -3,11 +3,20 @@
 // read-back of cached rows (FlashRT QKV Cache RoPE, Kernels: rotation and
 // cache write of the new K fused in one kernel).
 //
-// A row of d channels is held by d / 8 lanes, eight channels per lane in two
-// chunks of four.  Rotating channel pairs (i, i + rot/2), lane i takes the
-// chunks [4i, 4i+4) and [rot/2 + 4i, +4), so both members of a pair sit in
-// one lane; rotating pairs (2i, 2i+1), and for channels past rot_dim, the two
-// chunks are adjacent.  Either way lane i's four pairs use angles 4i .. 4i+3.
+// A row of d channels is held by W lanes (d / 8 rounded up to a power of two),
+// eight channels per lane in two chunks of four.  Rotating channel pairs (i, i
+// + rot/2), lane i takes the chunks [4i, 4i+4) and [rot/2 + 4i, +4), so both
+// members of a pair sit in one lane; rotating pairs (2i, 2i+1), and for
+// channels past rot_dim, the two chunks are adjacent.  Either way lane i's
+// four pairs use angles 4i .. 4i+3.
+//
+// One launch does everything.  A group of W lanes takes one token and some of
+// its rows: the token's sequence, slot, page and angles are found once and
+// four rows' loads are in flight at a time.  Keys whose page bounds are kept
+// go another way, since all new keys of a page have to meet: a CTA per page
+// (of the first new token in it), its groups spread over KV heads and slices
+// of the page's tokens, the slices' bounds joined in shared memory.  No page
+// is touched by two CTAs, so there are no atomics and no order to depend on.
 #include "internal.h"
 #include "quant.cuh"
 
@@ -39,6 +48,10 @@ struct AppendArgs {
   int32_t* seqlens;
   int batch, total, hq, rot, interleaved, rope_rows;
   int cache_dtype;
+  // how the work is cut: rows per token (without keys that the page role
+  // takes), rows per item and items per token; page role: its CTAs and the
+  // tokens each looks at
+  int token_rows, part_rows, parts, page_blocks, window;
   PoolArgs pool;
   Watchdog wd;
 };
@@ -97,14 +110,14 @@ __device__ __forceinline__ void chunk_offsets(const AppendArgs& A, int l, bool r
 }
 
 template <typename T>
-__device__ __forceinline__ void load8(const T* row, int a, int b, float (&x)[8]) {
-  float u[4], v[4];
-  Vec4<T>::widen(Vec4<T>::load(row + a), u);
-  Vec4<T>::widen(Vec4<T>::load(row + b), v);
+__device__ __forceinline__ void widen8(const typename Vec4<T>::Raw& u, const typename Vec4<T>::Raw& v, float (&x)[8]) {
+  float y[4], z[4];
+  Vec4<T>::widen(u, y);
+  Vec4<T>::widen(v, z);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    x[e] = u[e];
-    x[4 + e] = v[e];
+    x[e] = y[e];
+    x[4 + e] = z[e];
   }
 }
 
@@ -113,21 +126,33 @@ __device__ __forceinline__ void rotate_pair(float& a, float& b, float c, float s
   a = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
   b = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
 }
-__device__ __forceinline__ void rotate8(const AppendArgs& A, int l, int64_t slot, float (&x)[8]) {
-  if (8 * l >= A.rot) return;
-  const float* row = A.rope + slot * A.rot;
-  const float4 c = *reinterpret_cast<const float4*>(row + 4 * l);
-  const float4 s = *reinterpret_cast<const float4*>(row + A.rot / 2 + 4 * l);
+// The lane's four angles at a slot; no rotation for lanes past rot_dim.
+struct Angles {
+  float4 c, s;
+  bool any;
+};
+__device__ __forceinline__ Angles angles_of(const AppendArgs& A, int l, int64_t slot) {
+  Angles r;
+  r.any = 8 * l < A.rot;
+  if (r.any) {
+    const float* row = A.rope + slot * A.rot;
+    r.c = *reinterpret_cast<const float4*>(row + 4 * l);
+    r.s = *reinterpret_cast<const float4*>(row + A.rot / 2 + 4 * l);
+  }
+  return r;
+}
+__device__ __forceinline__ void rotate8(const AppendArgs& A, const Angles& g, float (&x)[8]) {
+  if (!g.any) return;
   if (A.interleaved) {
-    rotate_pair(x[0], x[1], c.x, s.x);
-    rotate_pair(x[2], x[3], c.y, s.y);
-    rotate_pair(x[4], x[5], c.z, s.z);
-    rotate_pair(x[6], x[7], c.w, s.w);
+    rotate_pair(x[0], x[1], g.c.x, g.s.x);
+    rotate_pair(x[2], x[3], g.c.y, g.s.y);
+    rotate_pair(x[4], x[5], g.c.z, g.s.z);
+    rotate_pair(x[6], x[7], g.c.w, g.s.w);
   } else {
-    rotate_pair(x[0], x[4], c.x, s.x);
-    rotate_pair(x[1], x[5], c.y, s.y);
-    rotate_pair(x[2], x[6], c.z, s.z);
-    rotate_pair(x[3], x[7], c.w, s.w);
+    rotate_pair(x[0], x[4], g.c.x, g.s.x);
+    rotate_pair(x[1], x[5], g.c.y, g.s.y);
+    rotate_pair(x[2], x[6], g.c.z, g.s.z);
+    rotate_pair(x[3], x[7], g.c.w, g.s.w);
   }
 }
 
@@ -156,10 +181,11 @@ __device__ __forceinline__ uint32_t code4(float x, float lo, float r, float y, b
   return static_cast<uint32_t>(__float2int_rn(q)) & 15u;
 }
 
-// One row into the cache by the `width` lanes that hold it (`own`: this lane
-// holds channels).  Every lane of the group calls.
-__device__ __forceinline__ void store_row(const AppendArgs& A, bool is_v, int64_t row, int l, int width, bool own,
-                                          int a, int b, const float (&x)[8], unsigned mask) {
+// One row into the cache by the W lanes that hold it (`own`: this lane holds
+// channels).  Every lane of the group calls.
+template <int W>
+__device__ __forceinline__ void store_row(const AppendArgs& A, bool is_v, int64_t row, int l, bool own, int a, int b,
+                                          const float (&x)[8], unsigned mask) {
   void* pool = is_v ? A.v_cache : A.k_cache;
   const int d = A.pool.d;
   if (A.cache_dtype == FA_BF16) {
@@ -173,7 +199,8 @@ __device__ __forceinline__ void store_row(const AppendArgs& A, bool is_v, int64_
 #pragma unroll
       for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
     }
-    for (int off = width >> 1; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(mask, amax, off));
+#pragma unroll
+    for (int off = W >> 1; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(mask, amax, off));
     const float s = __fdiv_rn(amax, 127.0f);
     const bool fast = s >= 0x1p-60f && s <= 0x1p60f;
     const float y = fast ? __frcp_rn(s) : 0.0f;
@@ -194,7 +221,8 @@ __device__ __forceinline__ void store_row(const AppendArgs& A, bool is_v, int64_
       hi = fmaxf(hi, x[e]);
     }
   }
-  for (int off = width >> 1; off > 0; off >>= 1) {
+#pragma unroll
+  for (int off = W >> 1; off > 0; off >>= 1) {
     lo = fminf(lo, __shfl_xor_sync(mask, lo, off));
     hi = fmaxf(hi, __shfl_xor_sync(mask, hi, off));
   }
@@ -212,28 +240,203 @@ __device__ __forceinline__ void store_row(const AppendArgs& A, bool is_v, int64_
   if (l == 0) *reinterpret_cast<float2*>(scales + 2 * row) = make_float2(__fdiv_rn(r, 15.0f), lo);
 }
 
-// The lane group of this thread: `width` lanes (a power of two) per row.
+// This thread's place in its group of W lanes.
+template <int W>
 struct Group {
-  int width, l;
-  unsigned mask;
-  bool own;
+  int l = threadIdx.x & (W - 1);
+  unsigned mask = W == 32 ? 0xffffffffu : ((1u << (W & 31)) - 1u) << (threadIdx.x & 31 & ~(W - 1));
 };
-__device__ __forceinline__ Group lane_group(int d) {
-  Group g;
-  g.width = 2;
-  while (g.width * 8 < d) g.width <<= 1;
-  const int lane = threadIdx.x & 31;
-  g.l = lane & (g.width - 1);
-  g.mask = g.width == 32 ? 0xffffffffu : ((1u << g.width) - 1u) << (lane & ~(g.width - 1));
-  g.own = 8 * g.l < d;
-  return g;
+
+constexpr int kRows = 4;  // rows a group has in flight
+
+// The rows [r0, r1) of one token: its hq queries, then its V rows, then (when
+// the page role does not take them) its K rows.
+template <typename T, int W>
+__device__ __forceinline__ void append_token(const AppendArgs& A, int t, int r0, int r1) {
+  using V = Vec4<T>;
+  const Group<W> G;
+  const bool own = 8 * G.l < A.pool.d;
+  Place p;
+  bool bad;
+  if (!place_token(A, t, p, bad)) {
+    if (bad && G.l == 0) record_status(A.wd, kStatusRange);
+    return;
+  }
+  int a, b;
+  chunk_offsets(A, G.l, true, a, b);
+  const Angles ang = angles_of(A, G.l, p.slot);
+  const int hq = A.hq, hkv = A.pool.hkv;
+  for (int r = r0; r < min(r1, hq); r += kRows) {
+    typename V::Raw u[kRows], v[kRows];
+    const T* q = static_cast<const T*>(A.q) + t * A.q_ts + r * A.q_hs;
+    const int n = min(r1, hq) - r;
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      if (own && k < n) {
+        u[k] = V::load(q + k * A.q_hs + a);
+        v[k] = V::load(q + k * A.q_hs + b);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      if (own && k < n) {
+        float x[8];
+        widen8<T>(u[k], v[k], x);
+        rotate8(A, ang, x);
+        store8_bf16(A.q_out + t * A.qo_ts + (r + k) * A.qo_hs, a, b, x);
+      }
+    }
+  }
+  for (int r = max(r0, hq); r < r1; r += kRows) {
+    typename V::Raw u[kRows], v[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int g = r + k - hq;
+      if (own && r + k < r1) {
+        const bool is_v = g < hkv;
+        const T* src = is_v ? static_cast<const T*>(A.v_new) + t * A.v_ts + g * A.v_hs
+                            : static_cast<const T*>(A.k_new) + t * A.k_ts + (g - hkv) * A.k_hs;
+        u[k] = V::load(src + (is_v ? 8 * G.l : a));
+        v[k] = V::load(src + (is_v ? 8 * G.l + 4 : b));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      if (r + k < r1) {
+        const int g = r + k - hq;
+        const bool is_v = g < hkv;
+        float x[8];
+        if (own) {
+          widen8<T>(u[k], v[k], x);
+          if (!is_v) rotate8(A, ang, x);
+        }
+        store_row<W>(A, is_v, p.row0 + static_cast<int64_t>(is_v ? g : g - hkv) * A.pool.page_size, G.l, own,
+                     is_v ? 8 * G.l : a, is_v ? 8 * G.l + 4 : b, x, G.mask);
+      }
+    }
+  }
 }
 
-// Rows of every new token: Q, K (unless the bounds kernel takes them) and V.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) append_rows_kernel(const AppendArgs A) {
-  const Group G = lane_group(A.pool.d);
-  if (A.seqlens != nullptr && blockIdx.x == 0) {
+// The new keys of the pages whose first new token is one of `window` tokens
+// from t0 on, and those pages' bounds; the whole CTA together.
+template <typename T, int W>
+__device__ __forceinline__ void append_pages(const AppendArgs& A, int t0, float (&s_lo)[8 * kThreads],
+                                             float (&s_hi)[8 * kThreads]) {
+  using V = Vec4<T>;
+  constexpr int kGroups = kThreads / W;
+  const Group<W> G;
+  const bool own = 8 * G.l < A.pool.d;
+  const int lane = threadIdx.x & 31, group = threadIdx.x / W;
+  const int page = A.pool.page_size, hkv = A.pool.hkv;
+  // lane j of every warp looks at token t0 + j
+  int left = 0, off = 0;
+  Place p;
+  p.slot = p.row0 = 0;
+  bool first = false;
+  if (lane < A.window && t0 + lane < A.total) {
+    bool bad;  // reported with the token's other rows
+    first = place_token(A, t0 + lane, p, bad);
+    if (first) {
+      int b, i;
+      seq_of_token(A.cu, A.batch, t0 + lane, b, i);
+      off = static_cast<int>(p.slot % page);
+      left = min(A.cu != nullptr ? min(A.cu[b + 1], A.total) - (t0 + lane) : 1, page - off);
+      if (A.rot > 0) left = static_cast<int>(min(static_cast<int64_t>(left), A.rope_rows - p.slot));
+      first = i == 0 || off == 0;  // else an earlier token's CTA has this page
+    }
+  }
+  int ca, cb;
+  chunk_offsets(A, G.l, true, ca, cb);
+  for (unsigned todo = __ballot_sync(0xffffffffu, first); todo != 0; todo &= todo - 1) {
+    const int j0 = __ffs(todo) - 1, t = t0 + j0;
+    const int n = __shfl_sync(0xffffffffu, left, j0), at = __shfl_sync(0xffffffffu, off, j0);
+    const int64_t slot = __shfl_sync(0xffffffffu, p.slot, j0), row0 = __shfl_sync(0xffffffffu, p.row0, j0);
+    const int slices = n == 1 ? 1 : max(1, kGroups / hkv);
+    for (int g0 = 0; g0 < hkv; g0 += kGroups) {
+      const int g = g0 + (slices > 1 ? group % hkv : group), slice = slices > 1 ? group / hkv : 0;
+      float lo[8], hi[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        lo[e] = INFINITY;
+        hi[e] = -INFINITY;
+      }
+      if (g < hkv && slice < slices) {
+        for (int j = slice; j < n; j += kRows * slices) {
+          typename V::Raw u[kRows], v[kRows];
+          const T* src = static_cast<const T*>(A.k_new) + (t + j) * A.k_ts + g * A.k_hs;
+#pragma unroll
+          for (int k = 0; k < kRows; ++k) {
+            if (own && j + k * slices < n) {
+              u[k] = V::load(src + k * slices * A.k_ts + ca);
+              v[k] = V::load(src + k * slices * A.k_ts + cb);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < kRows; ++k) {
+            const int jk = j + k * slices;
+            if (jk < n) {
+              float x[8];
+              if (own) {
+                widen8<T>(u[k], v[k], x);
+                rotate8(A, angles_of(A, G.l, slot + jk), x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  lo[e] = fminf(lo[e], x[e]);
+                  hi[e] = fmaxf(hi[e], x[e]);
+                }
+              }
+              store_row<W>(A, false, row0 + jk + static_cast<int64_t>(g) * page, G.l, own, ca, cb, x, G.mask);
+            }
+          }
+        }
+      }
+      if (slices > 1) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          s_lo[e * kThreads + threadIdx.x] = lo[e];
+          s_hi[e * kThreads + threadIdx.x] = hi[e];
+        }
+        __syncthreads();
+        if (slice == 0) {
+          for (int o = 1; o < slices; ++o) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              lo[e] = fminf(lo[e], s_lo[e * kThreads + threadIdx.x + o * hkv * W]);
+              hi[e] = fmaxf(hi[e], s_hi[e * kThreads + threadIdx.x + o * hkv * W]);
+            }
+          }
+        }
+      }
+      if (g < hkv && slice == 0 && own) {
+        const int64_t plane = row0 / page + g;  // page * hkv + g
+        __nv_bfloat16* dst = A.bounds + plane * 2 * A.pool.d;
+        if (at > 0) {
+          float x[8];
+          widen8<__nv_bfloat16>(*reinterpret_cast<const uint2*>(dst + ca), *reinterpret_cast<const uint2*>(dst + cb), x);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) lo[e] = fminf(lo[e], x[e]);
+          widen8<__nv_bfloat16>(*reinterpret_cast<const uint2*>(dst + A.pool.d + ca),
+                                *reinterpret_cast<const uint2*>(dst + A.pool.d + cb), x);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) hi[e] = fmaxf(hi[e], x[e]);
+        }
+        store8_bf16(dst, ca, cb, lo);
+        store8_bf16(dst + A.pool.d, ca, cb, hi);
+      }
+    }
+  }
+}
+
+template <typename T, int W>
+__global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs A) {
+  __shared__ float s_lo[8 * kThreads], s_hi[8 * kThreads];
+  if (static_cast<int>(blockIdx.x) < A.page_blocks) {
+    append_pages<T, W>(A, static_cast<int>(blockIdx.x) * A.window, s_lo, s_hi);
+    return;
+  }
+  const int64_t block = static_cast<int64_t>(blockIdx.x) - A.page_blocks;
+  if (A.seqlens != nullptr && block == 0) {
     for (int b = threadIdx.x; b < A.batch; b += kThreads) {
       const int64_t c0 = A.cu != nullptr ? A.cu[b] : b, c1 = A.cu != nullptr ? A.cu[b + 1] : b + 1;
       const int64_t end = static_cast<int64_t>(A.cur_pos[b]) + (c1 - c0);
@@ -244,100 +447,11 @@ __global__ void __launch_bounds__(kThreads) append_rows_kernel(const AppendArgs 
       }
     }
   }
-  const int per_token = A.hq + (A.bounds != nullptr ? 1 : 2) * A.pool.hkv;
-  const int64_t items = static_cast<int64_t>(A.total) * per_token;
-  const int64_t groups = static_cast<int64_t>(gridDim.x) * (kThreads / G.width);
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kThreads / G.width) + threadIdx.x / G.width; it < items;
-       it += groups) {
-    const int t = static_cast<int>(it / per_token);
-    int h = static_cast<int>(it % per_token);
-    Place p;
-    bool bad;
-    if (!place_token(A, t, p, bad)) {
-      if (bad && G.l == 0) record_status(A.wd, kStatusRange);
-      continue;
-    }
-    float x[8];
-    int a, b;
-    if (h < A.hq) {
-      chunk_offsets(A, G.l, true, a, b);
-      if (G.own) {
-        load8(static_cast<const T*>(A.q) + t * A.q_ts + h * A.q_hs, a, b, x);
-        rotate8(A, G.l, p.slot, x);
-        store8_bf16(A.q_out + t * A.qo_ts + h * A.qo_hs, a, b, x);
-      }
-      continue;
-    }
-    h -= A.hq;
-    const bool is_v = h < A.pool.hkv;
-    if (!is_v) h -= A.pool.hkv;
-    chunk_offsets(A, G.l, !is_v, a, b);
-    if (G.own) {
-      load8(is_v ? static_cast<const T*>(A.v_new) + t * A.v_ts + h * A.v_hs
-                 : static_cast<const T*>(A.k_new) + t * A.k_ts + h * A.k_hs, a, b, x);
-      if (!is_v) rotate8(A, G.l, p.slot, x);
-    }
-    store_row(A, is_v, p.row0 + static_cast<int64_t>(h) * A.pool.page_size, G.l, G.width, G.own, a, b, x, G.mask);
-  }
-}
-
-// Keys with bounds: the CTA of a page's first new token writes all of the
-// page's new keys and folds them into the page's bounds, one lane group per
-// KV head, so no two groups touch one page's bounds.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) append_keys_kernel(const AppendArgs A) {
-  const Group G = lane_group(A.pool.d);
-  const int t0 = blockIdx.x;
-  Place p;
-  bool bad;
-  if (!place_token(A, t0, p, bad)) return;  // reported by the rows kernel
-  int b, i;
-  seq_of_token(A.cu, A.batch, t0, b, i);
-  const int off = static_cast<int>(p.slot % A.pool.page_size);
-  if (i > 0 && off > 0) return;  // an earlier token's CTA has this page
-  const int left = A.cu != nullptr ? min(A.cu[b + 1], A.total) - t0 : 1;
-  const int n = min(left, A.pool.page_size - off);
-  int ca, cb;
-  chunk_offsets(A, G.l, true, ca, cb);
-  for (int g = threadIdx.x / G.width; g < A.pool.hkv; g += kThreads / G.width) {
-    float lo[8], hi[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      lo[e] = INFINITY;
-      hi[e] = -INFINITY;
-    }
-    for (int j = 0; j < n; ++j) {
-      float x[8];
-      if (A.rot > 0 && p.slot + j >= A.rope_rows) break;
-      if (G.own) {
-        load8(static_cast<const T*>(A.k_new) + (t0 + j) * A.k_ts + g * A.k_hs, ca, cb, x);
-        rotate8(A, G.l, p.slot + j, x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          lo[e] = fminf(lo[e], x[e]);
-          hi[e] = fmaxf(hi[e], x[e]);
-        }
-      }
-      store_row(A, false, p.row0 + j + static_cast<int64_t>(g) * A.pool.page_size, G.l, G.width, G.own, ca, cb, x,
-                G.mask);
-    }
-    if (G.own) {
-      const int64_t plane = p.row0 / A.pool.page_size + g;  // page * hkv + g
-      __nv_bfloat16* dst = A.bounds + plane * 2 * A.pool.d;
-      if (off > 0) {
-        float olo[8], ohi[8];
-        load8<__nv_bfloat16>(dst, ca, cb, olo);
-        load8<__nv_bfloat16>(dst + A.pool.d, ca, cb, ohi);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          lo[e] = fminf(lo[e], olo[e]);
-          hi[e] = fmaxf(hi[e], ohi[e]);
-        }
-      }
-      store8_bf16(dst, ca, cb, lo);
-      store8_bf16(dst + A.pool.d, ca, cb, hi);
-    }
-  }
+  const int64_t item = block * (kThreads / W) + threadIdx.x / W;
+  const int64_t t = item / A.parts;
+  if (t >= A.total) return;
+  const int r0 = static_cast<int>(item - t * A.parts) * A.part_rows;
+  append_token<T, W>(A, static_cast<int>(t), r0, min(r0 + A.part_rows, A.token_rows));
 }
 
 // ---------------------------------------------------------------- read back
@@ -351,37 +465,41 @@ struct ReadArgs {
   const int32_t* cu;
   const int32_t* start;
   int batch, total, cache_dtype, out_f32;
+  int part_rows, parts;  // rows per item, items per token
   PoolArgs pool;
   Watchdog wd;
 };
 
-__global__ void __launch_bounds__(kThreads) read_rows_kernel(const ReadArgs A) {
-  const Group G = lane_group(A.pool.d);
+// A group of W lanes takes one token and `part_rows` of its 2 hkv rows.
+template <int W>
+__global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs A) {
+  const Group<W> G;
   const int d = A.pool.d, hkv = A.pool.hkv;
-  const int64_t items = static_cast<int64_t>(A.total) * 2 * hkv;
-  const int64_t groups = static_cast<int64_t>(gridDim.x) * (kThreads / G.width);
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kThreads / G.width) + threadIdx.x / G.width; it < items;
-       it += groups) {
-    const int t = static_cast<int>(it % A.total);  // neighbours read neighbouring rows
-    const int h = static_cast<int>(it / A.total);
-    const bool is_v = h >= hkv;
-    const int g = is_v ? h - hkv : h;
-    int b, i;
-    if (!seq_of_token(A.cu, A.batch, t, b, i)) continue;
-    int64_t row;
-    if (!page_row(A.pool, b, static_cast<int64_t>(A.start != nullptr ? A.start[b] : 0) + i, row)) {
-      if (G.l == 0) record_status(A.wd, kStatusRange);
-      continue;
-    }
-    if (!G.own) continue;
-    row += static_cast<int64_t>(g) * A.pool.page_size;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / W) + threadIdx.x / W;
+  const int part = static_cast<int>(item / A.total), t = static_cast<int>(item - static_cast<int64_t>(part) * A.total);
+  if (part >= A.parts) return;  // neighbouring groups read and write neighbouring rows
+  int b, i;
+  int64_t row0;
+  if (!seq_of_token(A.cu, A.batch, t, b, i)) return;
+  if (!page_row(A.pool, b, static_cast<int64_t>(A.start != nullptr ? A.start[b] : 0) + i, row0)) {
+    if (G.l == 0) record_status(A.wd, kStatusRange);
+    return;
+  }
+  if (8 * G.l >= d) return;
+  const int r1 = min((part + 1) * A.part_rows, 2 * hkv);
+#pragma unroll 4
+  for (int r = part * A.part_rows; r < r1; ++r) {
+    const bool is_v = r >= hkv;
+    const int g = is_v ? r - hkv : r;
+    const int64_t row = row0 + static_cast<int64_t>(g) * A.pool.page_size;
     const void* pool = is_v ? A.v_cache : A.k_cache;
     const float* scales = is_v ? A.v_scales : A.k_scales;
     float x[8];
     if (A.cache_dtype == FA_BF16) {
-      load8<__nv_bfloat16>(static_cast<const __nv_bfloat16*>(pool) + row * d, 8 * G.l, 8 * G.l + 4, x);
+      const uint4 w = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(pool) + row * d + 8 * G.l));
+      widen8<__nv_bfloat16>(make_uint2(w.x, w.y), make_uint2(w.z, w.w), x);
     } else if (A.cache_dtype == FA_I8) {
-      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const int8_t*>(pool) + row * d + 8 * G.l);
+      const uint2 w = __ldcs(reinterpret_cast<const uint2*>(static_cast<const int8_t*>(pool) + row * d + 8 * G.l));
       const float s = scales[row];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -389,7 +507,8 @@ __global__ void __launch_bounds__(kThreads) read_rows_kernel(const ReadArgs A) {
         x[e] = __fmul_rn(static_cast<float>(static_cast<int8_t>(u >> (8 * (e & 3)))), s);
       }
     } else {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(pool) + row * (d / 2) + 4 * G.l);
+      const uint32_t w =
+          __ldcs(reinterpret_cast<const unsigned int*>(static_cast<const uint8_t*>(pool) + row * (d / 2) + 4 * G.l));
       const float2 s = *reinterpret_cast<const float2*>(scales + 2 * row);
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = __fadd_rn(__fmul_rn(static_cast<float>((w >> (4 * e)) & 15u), s.x), s.y);
@@ -397,12 +516,12 @@ __global__ void __launch_bounds__(kThreads) read_rows_kernel(const ReadArgs A) {
     const int64_t at = (static_cast<int64_t>(g) * A.total + t) * d + 8 * G.l;
     if (A.out_f32) {
       float* dst = static_cast<float*>(is_v ? A.v_out : A.k_out) + at;
-      *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
-      *reinterpret_cast<float4*>(dst + 4) = make_float4(x[4], x[5], x[6], x[7]);
+      __stcs(reinterpret_cast<float4*>(dst), make_float4(x[0], x[1], x[2], x[3]));
+      __stcs(reinterpret_cast<float4*>(dst + 4), make_float4(x[4], x[5], x[6], x[7]));
     } else {
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? A.v_out : A.k_out) + at;
-      *reinterpret_cast<uint4*>(dst) =
-          make_uint4(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]), bf16x2(x[4], x[5]), bf16x2(x[6], x[7]));
+      __stcs(reinterpret_cast<uint4*>(dst),
+             make_uint4(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]), bf16x2(x[4], x[5]), bf16x2(x[6], x[7])));
     }
   }
 }
@@ -419,24 +538,49 @@ PoolArgs pool_args(const fa_kv_pages& pg, int hkv, int d) {
   return P;
 }
 
-unsigned blocks_for(int64_t items, int d) {
-  int width = 2;
-  while (width * 8 < d) width <<= 1;
-  const int64_t per = kThreads / width;
-  const int64_t n = (items + per - 1) / per;
-  const int64_t most = static_cast<int64_t>(device_sm_count()) * 8;
-  return static_cast<unsigned>(n < 1 ? 1 : (n < most ? n : most));
+// Rows per item: four, and twice that while the items fill the device several
+// times over (the lookups of a token are then spread over more rows).
+int rows_per_item(int64_t total, int rows, int groups) {
+  const int64_t enough = static_cast<int64_t>(device_sm_count()) * 8 * groups;
+  int per = kRows;
+  while (per < rows && total * ((rows + per - 1) / per) > enough) per *= 2;
+  return per;
 }
 
+template <typename T, int W>
+fa_status launch_append_typed(AppendArgs& A, const LaunchCtx& ctx) {
+  constexpr int kGroups = kThreads / W;
+  A.token_rows = A.hq + (A.bounds != nullptr ? 1 : 2) * A.pool.hkv;
+  A.part_rows = rows_per_item(A.total, A.token_rows, kGroups);
+  A.parts = (A.token_rows + A.part_rows - 1) / A.part_rows;
+  int64_t blocks = (static_cast<int64_t>(A.total) * A.parts + kGroups - 1) / kGroups;
+  if (blocks < 1) blocks = 1;  // cache_seqlens alone
+  A.window = A.total <= 4 * device_sm_count() ? 1 : 8;
+  A.page_blocks = A.bounds != nullptr ? (A.total + A.window - 1) / A.window : 0;
+  blocks += A.page_blocks;
+  if (blocks >= (int64_t(1) << 31)) return FA_ERR_UNSUPPORTED;
+  note_variant(reinterpret_cast<const void*>(append_kernel<T, W>));
+  append_kernel<T, W><<<static_cast<unsigned>(blocks), kThreads, 0, ctx.stream>>>(A);
+  return cuda_status(cudaGetLastError());
+}
 template <typename T>
-fa_status launch_append_typed(const AppendArgs& A, const LaunchCtx& ctx) {
-  const int64_t items = static_cast<int64_t>(A.total) * (A.hq + (A.bounds != nullptr ? 1 : 2) * A.pool.hkv);
-  note_variant(reinterpret_cast<const void*>(append_rows_kernel<T>));
-  append_rows_kernel<T><<<blocks_for(items, A.pool.d), kThreads, 0, ctx.stream>>>(A);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  if (A.bounds == nullptr || A.total == 0) return FA_OK;
-  note_variant(reinterpret_cast<const void*>(append_keys_kernel<T>));
-  append_keys_kernel<T><<<static_cast<unsigned>(A.total), kThreads, 0, ctx.stream>>>(A);
+fa_status launch_append(AppendArgs& A, const LaunchCtx& ctx) {
+  if (A.pool.d <= 16) return launch_append_typed<T, 2>(A, ctx);
+  if (A.pool.d <= 32) return launch_append_typed<T, 4>(A, ctx);
+  if (A.pool.d <= 64) return launch_append_typed<T, 8>(A, ctx);
+  if (A.pool.d <= 128) return launch_append_typed<T, 16>(A, ctx);
+  return launch_append_typed<T, 32>(A, ctx);
+}
+
+template <int W>
+fa_status launch_read(ReadArgs& A, const LaunchCtx& ctx) {
+  constexpr int kGroups = kThreads / W;
+  A.part_rows = rows_per_item(A.total, 2 * A.pool.hkv, kGroups);
+  A.parts = (2 * A.pool.hkv + A.part_rows - 1) / A.part_rows;
+  const int64_t blocks = (static_cast<int64_t>(A.total) * A.parts + kGroups - 1) / kGroups;
+  if (blocks >= (int64_t(1) << 31)) return FA_ERR_UNSUPPORTED;
+  note_variant(reinterpret_cast<const void*>(read_kernel<W>));
+  read_kernel<W><<<static_cast<unsigned>(blocks), kThreads, 0, ctx.stream>>>(A);
   return cuda_status(cudaGetLastError());
 }
 
@@ -475,8 +619,8 @@ fa_status launch_kv_append_rope(const fa_kv_append_rope_params& p, const fa_kv_p
   A.cache_dtype = p.cache_dtype;
   A.pool = pool_args(pages, p.hkv, p.head_dim);
   A.wd = ctx.wd;
-  if (p.x_dtype == FA_BF16) return launch_append_typed<__nv_bfloat16>(A, ctx);
-  return launch_append_typed<float>(A, ctx);
+  if (p.x_dtype == FA_BF16) return launch_append<__nv_bfloat16>(A, ctx);
+  return launch_append<float>(A, ctx);
 }
 
 fa_status launch_kv_read(const fa_kv_read_params& p, const fa_kv_pages& pages, const LaunchCtx& ctx) {
@@ -496,9 +640,11 @@ fa_status launch_kv_read(const fa_kv_read_params& p, const fa_kv_pages& pages, c
   A.out_f32 = p.out_dtype == FA_F32 ? 1 : 0;
   A.pool = pool_args(pages, p.hkv, p.head_dim);
   A.wd = ctx.wd;
-  note_variant(reinterpret_cast<const void*>(read_rows_kernel));
-  read_rows_kernel<<<blocks_for(static_cast<int64_t>(p.total) * 2 * p.hkv, p.head_dim), kThreads, 0, ctx.stream>>>(A);
-  return cuda_status(cudaGetLastError());
+  if (p.head_dim <= 16) return launch_read<2>(A, ctx);
+  if (p.head_dim <= 32) return launch_read<4>(A, ctx);
+  if (p.head_dim <= 64) return launch_read<8>(A, ctx);
+  if (p.head_dim <= 128) return launch_read<16>(A, ctx);
+  return launch_read<32>(A, ctx);
 }
 
 }  // namespace fa

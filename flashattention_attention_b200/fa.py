@@ -626,15 +626,16 @@ def _append_params(k_new, v_new, k_cache, v_cache, cur_pos, hkv, k_scales, v_sca
 _CACHE_DT = {torch.bfloat16: FA_BF16, torch.int8: FA_I8, torch.uint8: FA_I4}
 
 
-def _on_device(dev: torch.device, stream, what: str, fn, *args) -> None:
-    """Call fn(*args, stream) with `dev` current: on `stream`, or on dev's current stream."""
+def _on_device(dev: int, stream, what: str, fn, *args) -> None:
+    """Call fn(*args, stream) with CUDA device `dev` current: on `stream`, or on dev's current stream."""
     if stream is None:
-        raw = torch.cuda.current_stream(dev).cuda_stream
+        # what torch.cuda.current_stream(dev).cuda_stream is, at a twentieth of its cost
+        raw = torch._C._cuda_getCurrentRawStream(dev)
     else:
-        if stream.device != dev:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+        if stream.device.index != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
         raw = stream.cuda_stream
-    if torch.cuda.current_device() == dev.index:
+    if torch.cuda.current_device() == dev:
         status = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -643,39 +644,43 @@ def _on_device(dev: torch.device, stream, what: str, fn, *args) -> None:
         raise FAError(status, what)
 
 
-def _new(shape, dtype, dev: torch.device, stream) -> torch.Tensor:
-    """A tensor for a call on `stream`: allocated on that stream, so that memory
-    freed when the call returns is only reused in its order."""
+def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
+    """A tensor on like's device for a call on `stream`: allocated on that
+    stream, so that memory freed when the call returns is only reused in its order."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _operand(t, name: str, dev: torch.device, dtype, shape) -> int:
-    """The address of a contiguous tensor on dev with this dtype and shape (0 for None)."""
-    if t is None:
-        return 0
-    if t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor on {dev}")
-    if t.dtype != dtype:
+def _operand(t, name: str, dev: int, dtype, shape) -> int:
+    """The address of a contiguous tensor on CUDA device dev with this dtype and shape."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on cuda:{dev}")
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != shape:
-        _shape(t, shape, name)
-    return t.data_ptr()
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
 
 
-def _pool_operands(k_pages, v_pages, k_scales, v_scales, block_table, batch: int, hkv: int, d: int, dev):
+def _optional(t, name: str, dev: int, dtype, shape) -> int:
+    return 0 if t is None else _operand(t, name, dev, dtype, shape)
+
+
+def _pool_operands(k_pages, v_pages, k_scales, v_scales, block_table, batch: int, hkv: int, d: int, dev: int):
     """(cache dtype, KvPages, pool and scale addresses) of page pools; ValueError where they do not fit together."""
-    kind = _CACHE_DT.get(k_pages.dtype)
+    dtype = k_pages.dtype
+    kind = _CACHE_DT.get(dtype)
     if kind is None:
-        raise ValueError(f"a page pool is bfloat16, int8 or uint8 (4-bit codes), not {k_pages.dtype}")
-    if len(k_pages.shape) != 4:
-        raise ValueError(f"k_pages has shape {tuple(k_pages.shape)}, expected 4 dimensions")
+        raise ValueError(f"a page pool is bfloat16, int8 or uint8 (4-bit codes), not {dtype}")
+    if len(k_pages.shape) != 4 or len(block_table.shape) != 2:
+        raise ValueError(f"a page pool has 4 dimensions and a block table 2; got {tuple(k_pages.shape)} and "
+                         f"{tuple(block_table.shape)}")
     num_pages, _, page_size, _ = k_pages.shape
     pool = (num_pages, hkv, page_size, d // 2 if kind == FA_I4 else d)
-    kp = _operand(k_pages, "k_pages", dev, k_pages.dtype, pool)
-    vp = _operand(v_pages, "v_pages", dev, k_pages.dtype, pool)
+    kp = _operand(k_pages, "k_pages", dev, dtype, pool)
+    vp = _operand(v_pages, "v_pages", dev, dtype, pool)
     if kind == FA_BF16:
         if k_scales is not None or v_scales is not None:
             raise ValueError("a bfloat16 cache has no scales")
@@ -686,8 +691,6 @@ def _pool_operands(k_pages, v_pages, k_scales, v_scales, block_table, batch: int
         rows = (num_pages, hkv, page_size, 2) if kind == FA_I4 else (num_pages, hkv, page_size)
         ks = _operand(k_scales, "k_scales", dev, torch.float32, rows)
         vs = _operand(v_scales, "v_scales", dev, torch.float32, rows)
-    if len(block_table.shape) != 2:
-        raise ValueError(f"block_table has shape {tuple(block_table.shape)}, expected 2 dimensions")
     max_pages = block_table.shape[1]
     table = _operand(block_table, "block_table", dev, torch.int32, (batch, max_pages))
     return kind, KvPages(table, max_pages, page_size, num_pages), kp, vp, ks, vs
@@ -701,25 +704,22 @@ def _int(x, name: str, lo: int = 0) -> int:
     return x
 
 
-def _cuda_device(t, name: str) -> torch.device:
-    if not t.is_cuda:
+def _cuda_device(t, name: str) -> int:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+    return dev
 
 
-def _rows_operand(t, name: str, dev: torch.device, dtype, shape):
+def _rows_operand(t, name: str, dev: int, dtype, shape):
     """(address, token stride, head stride) of rows [tokens, heads, d] whose last dimension is contiguous."""
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != shape:
-        _shape(t, shape, name)
-    st = t.stride()
-    if st[2] != 1 and shape[2] > 1:
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {shape} on cuda:{dev}; got {t.dtype} {tuple(t.shape)} on {t.device}")
+    tokens, heads, channels = t.stride()
+    if channels != 1 and shape[2] > 1:
         raise ValueError(f"{name}: the channels of a row must be contiguous")
     # a dimension of one row has no stride of its own
-    return t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0
+    return t.data_ptr(), tokens if shape[0] > 1 else 0, heads if shape[1] > 1 else 0
 
 
 def rope_table(rows: int, rot_dim: int, base: float = 10000.0) -> torch.Tensor:
@@ -763,10 +763,10 @@ def kv_append_rope_paged(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torc
     kn, kts, khs = _rows_operand(k_new, "k_new", dev, xt, (total, hkv, d))
     vn, vts, vhs = _rows_operand(v_new, "v_new", dev, xt, (total, hkv, d))
     kind, pg, kp, vp, ks, vs = _pool_operands(k_pages, v_pages, k_scales, v_scales, block_table, batch, hkv, d, dev)
-    bounds = _operand(key_bounds, "key_bounds", dev, torch.bfloat16, (k_pages.shape[0], hkv, 2, d))
+    bounds = _optional(key_bounds, "key_bounds", dev, torch.bfloat16, (pg.num_pages, hkv, 2, d))
     pos = _operand(cur_pos, "cur_pos", dev, torch.int32, (batch,))
-    cu = _operand(cu_seqlens, "cu_seqlens", dev, torch.int32, (batch + 1,))
-    lens = _operand(cache_seqlens, "cache_seqlens", dev, torch.int32, (batch,))
+    cu = _optional(cu_seqlens, "cu_seqlens", dev, torch.int32, (batch + 1,))
+    lens = _optional(cache_seqlens, "cache_seqlens", dev, torch.int32, (batch,))
     table, rows, rot = 0, 0, 0
     if rope_table is not None:
         if len(rope_table.shape) != 2:
@@ -784,7 +784,7 @@ def kv_append_rope_paged(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torc
         qp, qts, qhs = _rows_operand(q, "q", dev, xt, (total, hq, d))
         shape = (total * hq, d) if cu_seqlens is None else (hq, total, d)
         if q_out is None:
-            q_out = _new(shape, torch.bfloat16, dev, stream)
+            q_out = _new(q, shape, torch.bfloat16, stream)
         qo = _operand(q_out, "q_out", dev, torch.bfloat16, shape)
         ots, ohs = (hq * d, d) if cu_seqlens is None else (d, total * d)
     p = KvAppendRopeParams(kn, vn, qp, qo, kts, khs, vts, vhs, qts, qhs, ots, ohs, table, kp, vp, ks, vs, bounds, cu, pos,
@@ -811,13 +811,13 @@ def kv_read_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, cu_seqlens: torc
         raise ValueError(f"out_dtype must be bfloat16 or float32, not {out_dtype}")
     shape = (hkv, _int(total, "total"), d)
     if k_out is None:
-        k_out = _new(shape, out_dtype, dev, stream)
+        k_out = _new(k_pages, shape, out_dtype, stream)
     if v_out is None:
-        v_out = _new(shape, out_dtype, dev, stream)
+        v_out = _new(k_pages, shape, out_dtype, stream)
     p = KvReadParams(kp, vp, ks, vs, _operand(k_out, "k_out", dev, out_dtype, shape),
                      _operand(v_out, "v_out", dev, out_dtype, shape),
                      _operand(cu_seqlens, "cu_seqlens", dev, torch.int32, (batch + 1,)),
-                     _operand(start, "start", dev, torch.int32, (batch,)), kind,
+                     _optional(start, "start", dev, torch.int32, (batch,)), kind,
                      FA_BF16 if out_dtype == torch.bfloat16 else FA_F32, batch, shape[1], hkv, d)
     _on_device(dev, stream, "fa_kv_read_paged", lib.fa_kv_read_paged, p, pg)
     return k_out, v_out
@@ -829,10 +829,10 @@ def _decode_queries(q, cache_seqlens, hq: int, hkv: int, dev):
         raise ValueError(f"hq = {hq} must be a positive multiple of hkv = {hkv}")
     if len(cache_seqlens.shape) != 1:
         raise ValueError(f"cache_seqlens has shape {tuple(cache_seqlens.shape)}, expected 1 dimension")
-    batch, d = cache_seqlens.shape[0], q.shape[-1]
-    shape = tuple(q.shape)
+    shape = q.shape
+    batch, d = cache_seqlens.shape[0], shape[-1]
     if shape != (batch * hq, d) and shape != (batch * hq, 1, d):
-        raise ValueError(f"q has shape {shape}, expected batch*hq = {batch * hq} rows")
+        raise ValueError(f"q has shape {tuple(shape)}, expected batch*hq = {batch * hq} rows")
     return (batch, d, _operand(q, "q", dev, torch.bfloat16, shape),
             _operand(cache_seqlens, "cache_seqlens", dev, torch.int32, (batch,)))
 
@@ -857,10 +857,10 @@ def page_select(q: torch.Tensor, key_bounds: torch.Tensor, cache_seqlens: torch.
     top_k = _int(top_k, "top_k", 1)
     shape = (batch, hkv, top_k)
     if out is None:
-        out = _new(shape, torch.int32, dev, stream)
+        out = _new(q, shape, torch.int32, stream)
     if workspace is None:
         nbytes = lib.fa_page_select_workspace_size(batch, hkv, max_pages)
-        workspace = _new((max(nbytes, 16),), torch.uint8, dev, stream)
+        workspace = _new(q, (max(nbytes, 16),), torch.uint8, stream)
     p = PageSelectParams(qp, bounds, lens, _operand(out, "out", dev, torch.int32, shape), batch, hq, hkv, d, top_k,
                          _int(n_first, "n_first"), _int(n_recent, "n_recent"), _workspace(workspace, dev),
                          workspace.numel() * workspace.element_size())
@@ -868,9 +868,9 @@ def page_select(q: torch.Tensor, key_bounds: torch.Tensor, cache_seqlens: torch.
     return out
 
 
-def _workspace(t, dev: torch.device) -> int:
-    if t.device != dev or not t.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+def _workspace(t, dev: int) -> int:
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
     return t.data_ptr()
 
 
@@ -893,11 +893,11 @@ def _decode_pages(q, k_pages, v_pages, cache_seqlens, block_table, selected, hq,
     kind, pg, kp, vp, ks, vs = _pool_operands(k_pages, v_pages, k_scales, v_scales, block_table, batch, hkv, d, dev)
     capacity = pg.max_pages * pg.page_size
     if out is None:
-        out = _new(q.shape, torch.bfloat16, dev, stream)
+        out = _new(q, q.shape, torch.bfloat16, stream)
     if workspace is None:
         nbytes = lib.fa_decode_workspace_size(batch, hq, capacity, d)
-        workspace = _new((max(nbytes, 16),), torch.uint8, dev, stream)
-    p = DecodeParams(qp, kp, vp, ks, vs, lens, _operand(out, "out", dev, torch.bfloat16, tuple(q.shape)), kind, batch, hq,
+        workspace = _new(q, (max(nbytes, 16),), torch.uint8, stream)
+    p = DecodeParams(qp, kp, vp, ks, vs, lens, _operand(out, "out", dev, torch.bfloat16, q.shape), kind, batch, hq,
                      hkv, d, capacity, _int(max_seqlen, "max_seqlen"), _int(max(0, window), "window"),
                      1.0 / math.sqrt(d) if scale is None else float(scale), 0)
     p.workspace, p.workspace_bytes = _workspace(workspace, dev), workspace.numel() * workspace.element_size()

@@ -28,6 +28,9 @@ class Fake:
     def data_ptr(self):
         return self.addr
 
+    def get_device(self):
+        return self.device.index if self.is_cuda else -1
+
     def is_contiguous(self):
         return self._contiguous
 
