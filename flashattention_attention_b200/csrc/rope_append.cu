@@ -109,23 +109,18 @@ __device__ __forceinline__ void chunk_offsets(const AppendArgs& A, int l, bool r
   }
 }
 
+// A lane's eight channels: x[0], x[1] of chunk a, x[2], x[3] of chunk b.
 template <typename T>
-__device__ __forceinline__ void widen8(const typename Vec4<T>::Raw& u, const typename Vec4<T>::Raw& v, float (&x)[8]) {
+__device__ __forceinline__ void widen8(const typename Vec4<T>::Raw& u, const typename Vec4<T>::Raw& v, float2 (&x)[4]) {
   float y[4], z[4];
   Vec4<T>::widen(u, y);
   Vec4<T>::widen(v, z);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    x[e] = y[e];
-    x[4 + e] = z[e];
-  }
+  x[0] = make_float2(y[0], y[1]);
+  x[1] = make_float2(y[2], y[3]);
+  x[2] = make_float2(z[0], z[1]);
+  x[3] = make_float2(z[2], z[3]);
 }
 
-__device__ __forceinline__ void rotate_pair(float& a, float& b, float c, float s) {
-  const float x = a, y = b;
-  a = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
-  b = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
-}
 // The lane's four angles at a slot; no rotation for lanes past rot_dim.
 struct Angles {
   float4 c, s;
@@ -134,6 +129,7 @@ struct Angles {
 __device__ __forceinline__ Angles angles_of(const AppendArgs& A, int l, int64_t slot) {
   Angles r;
   r.any = 8 * l < A.rot;
+  r.c = r.s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (r.any) {
     const float* row = A.rope + slot * A.rot;
     r.c = *reinterpret_cast<const float4*>(row + 4 * l);
@@ -141,18 +137,34 @@ __device__ __forceinline__ Angles angles_of(const AppendArgs& A, int l, int64_t 
   }
   return r;
 }
-__device__ __forceinline__ void rotate8(const AppendArgs& A, const Angles& g, float (&x)[8]) {
+// (a, b) <- (a c - b s, b c + a s), every product and sum rounded.  In scalars:
+// the compiler contracts a packed product and a packed sum into one packed FMA,
+// although each asks for its rounding (20 of 64 rows' int8 scales were off).
+__device__ __forceinline__ void rotate_pair(float& a, float& b, float c, float s) {
+  const float x = a;
+  a = __fsub_rn(__fmul_rn(x, c), __fmul_rn(b, s));
+  b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(x, s));
+}
+__device__ __forceinline__ void rotate_pairs(float2& a, float2& b, float2 c, float2 s) {
+  rotate_pair(a.x, b.x, c.x, s.x);
+  rotate_pair(a.y, b.y, c.y, s.y);
+}
+__device__ __forceinline__ void rotate8(const AppendArgs& A, const Angles& g, float2 (&x)[4]) {
   if (!g.any) return;
+  const float2 c0 = make_float2(g.c.x, g.c.y), c1 = make_float2(g.c.z, g.c.w);
+  const float2 s0 = make_float2(g.s.x, g.s.y), s1 = make_float2(g.s.z, g.s.w);
   if (A.interleaved) {
-    rotate_pair(x[0], x[1], g.c.x, g.s.x);
-    rotate_pair(x[2], x[3], g.c.y, g.s.y);
-    rotate_pair(x[4], x[5], g.c.z, g.s.z);
-    rotate_pair(x[6], x[7], g.c.w, g.s.w);
+    float2 a0 = make_float2(x[0].x, x[1].x), b0 = make_float2(x[0].y, x[1].y);
+    float2 a1 = make_float2(x[2].x, x[3].x), b1 = make_float2(x[2].y, x[3].y);
+    rotate_pairs(a0, b0, c0, s0);
+    rotate_pairs(a1, b1, c1, s1);
+    x[0] = make_float2(a0.x, b0.x);
+    x[1] = make_float2(a0.y, b0.y);
+    x[2] = make_float2(a1.x, b1.x);
+    x[3] = make_float2(a1.y, b1.y);
   } else {
-    rotate_pair(x[0], x[4], g.c.x, g.s.x);
-    rotate_pair(x[1], x[5], g.c.y, g.s.y);
-    rotate_pair(x[2], x[6], g.c.z, g.s.z);
-    rotate_pair(x[3], x[7], g.c.w, g.s.w);
+    rotate_pairs(x[0], x[2], c0, s0);
+    rotate_pairs(x[1], x[3], c1, s1);
   }
 }
 
@@ -160,84 +172,126 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
 }
-__device__ __forceinline__ void store8_bf16(__nv_bfloat16* row, int a, int b, const float (&x)[8]) {
-  *reinterpret_cast<uint2*>(row + a) = make_uint2(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]));
-  *reinterpret_cast<uint2*>(row + b) = make_uint2(bf16x2(x[4], x[5]), bf16x2(x[6], x[7]));
+__device__ __forceinline__ uint2 pack4(float2 lo, float2 hi) { return make_uint2(bf16x2(lo.x, lo.y), bf16x2(hi.x, hi.y)); }
+__device__ __forceinline__ void store8_bf16(__nv_bfloat16* row, int a, int b, const float2 (&x)[4]) {
+  *reinterpret_cast<uint2*>(row + a) = pack4(x[0], x[1]);
+  *reinterpret_cast<uint2*>(row + b) = pack4(x[2], x[3]);
 }
 
-// Code of one channel of a 4-bit row: round_half_even(15 (x - lo) / r); the
-// quotient is the correctly rounded one (Markstein's step as in quant.cu where
-// r and 1 / r are normal, the IEEE division elsewhere), so the exact halves
-// that rows of bf16 values are full of stay exact.
-__device__ __forceinline__ uint32_t code4(float x, float lo, float r, float y, bool fast) {
-  const float u = __fmul_rn(__fsub_rn(x, lo), 15.0f);
-  float q;
-  if (fast) {
-    const float q0 = __fmul_rn(u, y);
-    q = __fmaf_rn(__fmaf_rn(-q0, r, u), y, q0);
-  } else {
-    q = r > 0.0f ? __fdiv_rn(u, r) : 0.0f;
-  }
-  return static_cast<uint32_t>(__float2int_rn(q)) & 15u;
+// The quantisers below need correctly rounded quotients (codes and scales are
+// defined by them, and rows of bf16 values are full of exact halves).  With y
+// the rounded reciprocal of b, Markstein's step RN(q0 + RN(a - q0 b) y), q0 =
+// RN(a y), is that quotient as long as nothing leaves the normal range (see
+// quant.cu; checked over all mantissas for the divisors 15 and 127).  Rows
+// whose range or scale is outside [2^-60, 2^60] take the IEEE division, in a
+// function of its own so that its code stays out of the loops.
+__device__ __forceinline__ float divide_by(float a, float b, float y) {
+  const float q0 = __fmul_rn(a, y);
+  return __fmaf_rn(__fmaf_rn(-q0, b, a), y, q0);
 }
+__device__ __forceinline__ bool ordinary(float s) { return s >= 0x1p-60f && s <= 0x1p60f; }
+
+// Four 4-bit codes, 4 bits each: round_half_even(15 (x - lo) / r).
+__device__ __forceinline__ uint32_t codes4_fast(float2 x0, float2 x1, float lo, float r, float y) {
+  const float2 nlo = make_float2(-lo, -lo), nr = make_float2(-r, -r), y2 = make_float2(y, y);
+  const float2 fifteen = make_float2(15.0f, 15.0f), shift = make_float2(12582912.0f, 12582912.0f);  // 1.5 * 2^23
+  uint32_t k[4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float2 u = mul2(add2(h ? x1 : x0, nlo), fifteen);
+    const float2 q0 = mul2(u, y2);
+    const float2 z = add2(fma2(fma2(q0, nr, u), y2, q0), shift);
+    k[2 * h] = __float_as_uint(z.x);
+    k[2 * h + 1] = __float_as_uint(z.y);
+  }
+  // the low 16 bits of the shift's pattern are 0, so those of the sum are the four codes
+  return (k[0] + (k[1] << 4) + (k[2] << 8) + (k[3] << 12)) & 0xffffu;
+}
+__device__ __noinline__ uint32_t codes4_any(float2 x0, float2 x1, float lo, float r) {
+  const float x[4] = {x0.x, x0.y, x1.x, x1.y};
+  uint32_t w = 0;
+  for (int e = 0; e < 4; ++e) {
+    const float q = r > 0.0f ? __fdiv_rn(__fmul_rn(__fsub_rn(x[e], lo), 15.0f), r) : 0.0f;
+    w |= (static_cast<uint32_t>(__float2int_rn(q)) & 15u) << (4 * e);
+  }
+  return w;
+}
+__device__ __noinline__ uint32_t codes8_any(float2 x0, float2 x1, float s) {
+  const float x[4] = {x0.x, x0.y, x1.x, x1.y};
+  return quantise4_div(x, s);
+}
+__device__ __noinline__ float divide_any(float a, float b) { return __fdiv_rn(a, b); }
 
 // One row into the cache by the W lanes that hold it (`own`: this lane holds
 // channels).  Every lane of the group calls.
-template <int W>
+template <int W, int kCache>
 __device__ __forceinline__ void store_row(const AppendArgs& A, bool is_v, int64_t row, int l, bool own, int a, int b,
-                                          const float (&x)[8], unsigned mask) {
+                                          const float2 (&x)[4], unsigned mask) {
   void* pool = is_v ? A.v_cache : A.k_cache;
   const int d = A.pool.d;
-  if (A.cache_dtype == FA_BF16) {
+  if constexpr (kCache == FA_BF16) {
     if (own) store8_bf16(static_cast<__nv_bfloat16*>(pool) + row * d, a, b, x);
-    return;
-  }
-  float* scales = is_v ? A.v_scales : A.k_scales;
-  if (A.cache_dtype == FA_I8) {
+  } else if constexpr (kCache == FA_I8) {
     float amax = 0.0f;
     if (own) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
+      for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(x[e].x), fabsf(x[e].y)));
     }
 #pragma unroll
     for (int off = W >> 1; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(mask, amax, off));
-    const float s = __fdiv_rn(amax, 127.0f);
-    const bool fast = s >= 0x1p-60f && s <= 0x1p60f;
-    const float y = fast ? __frcp_rn(s) : 0.0f;
+    constexpr float k127 = 1.0f / 127.0f;
+    const float s = ordinary(amax) ? divide_by(amax, 127.0f, k127) : divide_any(amax, 127.0f);
     if (own) {
       int8_t* dst = static_cast<int8_t*>(pool) + row * d;
-      const float u[4] = {x[0], x[1], x[2], x[3]}, v[4] = {x[4], x[5], x[6], x[7]};
-      *reinterpret_cast<uint32_t*>(dst + a) = fast ? quantise4_fast(u, s, y) : quantise4_div(u, s);
-      *reinterpret_cast<uint32_t*>(dst + b) = fast ? quantise4_fast(v, s, y) : quantise4_div(v, s);
+      uint32_t u, v;
+      if (ordinary(s)) {
+        const float y = __frcp_rn(s);
+        const float p[4] = {x[0].x, x[0].y, x[1].x, x[1].y}, q[4] = {x[2].x, x[2].y, x[3].x, x[3].y};
+        u = quantise4_fast(p, s, y);
+        v = quantise4_fast(q, s, y);
+      } else {
+        u = codes8_any(x[0], x[1], s);
+        v = codes8_any(x[2], x[3], s);
+      }
+      *reinterpret_cast<uint32_t*>(dst + a) = u;
+      *reinterpret_cast<uint32_t*>(dst + b) = v;
+      if (l == 0) (is_v ? A.v_scales : A.k_scales)[row] = s;
     }
-    if (l == 0) scales[row] = s;
-    return;
-  }
-  float lo = INFINITY, hi = -INFINITY;
-  if (own) {
+  } else {
+    float lo = INFINITY, hi = -INFINITY;
+    if (own) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      lo = fminf(lo, x[e]);
-      hi = fmaxf(hi, x[e]);
+      for (int e = 0; e < 4; ++e) {
+        lo = min3f(lo, x[e].x, x[e].y);
+        hi = max3f(hi, x[e].x, x[e].y);
+      }
+    }
+#pragma unroll
+    for (int off = W >> 1; off > 0; off >>= 1) {
+      lo = fminf(lo, __shfl_xor_sync(mask, lo, off));
+      hi = fmaxf(hi, __shfl_xor_sync(mask, hi, off));
+    }
+    const float r = __fsub_rn(hi, lo);
+    if (own) {
+      uint8_t* dst = static_cast<uint8_t*>(pool) + row * (d / 2);
+      uint32_t u, v;
+      float step;
+      if (ordinary(r)) {
+        const float y = __frcp_rn(r);
+        constexpr float k15 = 1.0f / 15.0f;
+        step = divide_by(r, 15.0f, k15);
+        u = codes4_fast(x[0], x[1], lo, r, y);
+        v = codes4_fast(x[2], x[3], lo, r, y);
+      } else {
+        step = divide_any(r, 15.0f);
+        u = codes4_any(x[0], x[1], lo, r);
+        v = codes4_any(x[2], x[3], lo, r);
+      }
+      *reinterpret_cast<uint16_t*>(dst + a / 2) = static_cast<uint16_t>(u);
+      *reinterpret_cast<uint16_t*>(dst + b / 2) = static_cast<uint16_t>(v);
+      if (l == 0) *reinterpret_cast<float2*>((is_v ? A.v_scales : A.k_scales) + 2 * row) = make_float2(step, lo);
     }
   }
-#pragma unroll
-  for (int off = W >> 1; off > 0; off >>= 1) {
-    lo = fminf(lo, __shfl_xor_sync(mask, lo, off));
-    hi = fmaxf(hi, __shfl_xor_sync(mask, hi, off));
-  }
-  const float r = __fsub_rn(hi, lo);
-  const bool fast = r >= 0x1p-60f && r <= 0x1p60f;
-  const float y = fast ? __frcp_rn(r) : 0.0f;
-  if (own) {
-    uint8_t* dst = static_cast<uint8_t*>(pool) + row * (d / 2);
-    uint32_t w[2] = {0, 0};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e >> 2] |= code4(x[e], lo, r, y, fast) << (4 * (e & 3));
-    *reinterpret_cast<uint16_t*>(dst + a / 2) = static_cast<uint16_t>(w[0]);
-    *reinterpret_cast<uint16_t*>(dst + b / 2) = static_cast<uint16_t>(w[1]);
-  }
-  if (l == 0) *reinterpret_cast<float2*>(scales + 2 * row) = make_float2(__fdiv_rn(r, 15.0f), lo);
 }
 
 // This thread's place in its group of W lanes.
@@ -247,11 +301,11 @@ struct Group {
   unsigned mask = W == 32 ? 0xffffffffu : ((1u << (W & 31)) - 1u) << (threadIdx.x & 31 & ~(W - 1));
 };
 
-constexpr int kRows = 4;  // rows a group has in flight
+constexpr int kRows = 4;  // query rows a group has in flight (of K and V rows two: their arithmetic is longer)
 
 // The rows [r0, r1) of one token: its hq queries, then its V rows, then (when
 // the page role does not take them) its K rows.
-template <typename T, int W>
+template <typename T, int W, int kCache>
 __device__ __forceinline__ void append_token(const AppendArgs& A, int t, int r0, int r1) {
   using V = Vec4<T>;
   const Group<W> G;
@@ -266,62 +320,53 @@ __device__ __forceinline__ void append_token(const AppendArgs& A, int t, int r0,
   chunk_offsets(A, G.l, true, a, b);
   const Angles ang = angles_of(A, G.l, p.slot);
   const int hq = A.hq, hkv = A.pool.hkv;
-  for (int r = r0; r < min(r1, hq); r += kRows) {
+  const int q1 = min(r1, hq);
+  const T* q = static_cast<const T*>(A.q) + t * A.q_ts + r0 * A.q_hs;
+  __nv_bfloat16* qo = A.q_out + t * A.qo_ts + r0 * A.qo_hs;
+#pragma unroll 1
+  for (int r = r0; r < q1; r += kRows, q += kRows * A.q_hs, qo += kRows * A.qo_hs) {
     typename V::Raw u[kRows], v[kRows];
-    const T* q = static_cast<const T*>(A.q) + t * A.q_ts + r * A.q_hs;
-    const int n = min(r1, hq) - r;
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
-      if (own && k < n) {
+      if (own && r + k < q1) {
         u[k] = V::load(q + k * A.q_hs + a);
         v[k] = V::load(q + k * A.q_hs + b);
       }
     }
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
-      if (own && k < n) {
-        float x[8];
+      if (own && r + k < q1) {
+        float2 x[4];
         widen8<T>(u[k], v[k], x);
         rotate8(A, ang, x);
-        store8_bf16(A.q_out + t * A.qo_ts + (r + k) * A.qo_hs, a, b, x);
+        store8_bf16(qo + k * A.qo_hs, a, b, x);
       }
     }
   }
-  for (int r = max(r0, hq); r < r1; r += kRows) {
-    typename V::Raw u[kRows], v[kRows];
-#pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      const int g = r + k - hq;
-      if (own && r + k < r1) {
-        const bool is_v = g < hkv;
-        const T* src = is_v ? static_cast<const T*>(A.v_new) + t * A.v_ts + g * A.v_hs
-                            : static_cast<const T*>(A.k_new) + t * A.k_ts + (g - hkv) * A.k_hs;
-        u[k] = V::load(src + (is_v ? 8 * G.l : a));
-        v[k] = V::load(src + (is_v ? 8 * G.l + 4 : b));
-      }
+#pragma unroll 2
+  for (int r = max(r0, hq) - hq; r < r1 - hq; ++r) {
+    const bool is_v = r < hkv;
+    const int g = is_v ? r : r - hkv;
+    const int ra = is_v ? 8 * G.l : a, rb = is_v ? 8 * G.l + 4 : b;
+    float2 x[4];
+    if (own) {
+      const T* src = is_v ? static_cast<const T*>(A.v_new) + t * A.v_ts + g * A.v_hs
+                          : static_cast<const T*>(A.k_new) + t * A.k_ts + g * A.k_hs;
+      widen8<T>(V::load(src + ra), V::load(src + rb), x);
+      if (!is_v) rotate8(A, ang, x);
     }
-#pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      if (r + k < r1) {
-        const int g = r + k - hq;
-        const bool is_v = g < hkv;
-        float x[8];
-        if (own) {
-          widen8<T>(u[k], v[k], x);
-          if (!is_v) rotate8(A, ang, x);
-        }
-        store_row<W>(A, is_v, p.row0 + static_cast<int64_t>(is_v ? g : g - hkv) * A.pool.page_size, G.l, own,
-                     is_v ? 8 * G.l : a, is_v ? 8 * G.l + 4 : b, x, G.mask);
-      }
-    }
+    store_row<W, kCache>(A, is_v, p.row0 + static_cast<int64_t>(g) * A.pool.page_size, G.l, own, ra, rb, x, G.mask);
   }
 }
 
+__device__ __forceinline__ float2 min_of(float2 a, float2 b) { return make_float2(fminf(a.x, b.x), fminf(a.y, b.y)); }
+__device__ __forceinline__ float2 max_of(float2 a, float2 b) { return make_float2(fmaxf(a.x, b.x), fmaxf(a.y, b.y)); }
+
 // The new keys of the pages whose first new token is one of `window` tokens
 // from t0 on, and those pages' bounds; the whole CTA together.
-template <typename T, int W>
-__device__ __forceinline__ void append_pages(const AppendArgs& A, int t0, float (&s_lo)[8 * kThreads],
-                                             float (&s_hi)[8 * kThreads]) {
+template <typename T, int W, int kCache>
+__device__ __forceinline__ void append_pages(const AppendArgs& A, int t0, float2 (&s_lo)[4][kThreads],
+                                             float2 (&s_hi)[4][kThreads]) {
   using V = Vec4<T>;
   constexpr int kGroups = kThreads / W;
   const Group<W> G;
@@ -347,63 +392,53 @@ __device__ __forceinline__ void append_pages(const AppendArgs& A, int t0, float 
   }
   int ca, cb;
   chunk_offsets(A, G.l, true, ca, cb);
+#pragma unroll 1
   for (unsigned todo = __ballot_sync(0xffffffffu, first); todo != 0; todo &= todo - 1) {
     const int j0 = __ffs(todo) - 1, t = t0 + j0;
     const int n = __shfl_sync(0xffffffffu, left, j0), at = __shfl_sync(0xffffffffu, off, j0);
     const int64_t slot = __shfl_sync(0xffffffffu, p.slot, j0), row0 = __shfl_sync(0xffffffffu, p.row0, j0);
     const int slices = n == 1 ? 1 : max(1, kGroups / hkv);
+#pragma unroll 1
     for (int g0 = 0; g0 < hkv; g0 += kGroups) {
       const int g = g0 + (slices > 1 ? group % hkv : group), slice = slices > 1 ? group / hkv : 0;
-      float lo[8], hi[8];
+      float2 lo[4], hi[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        lo[e] = INFINITY;
-        hi[e] = -INFINITY;
+      for (int e = 0; e < 4; ++e) {
+        lo[e] = make_float2(INFINITY, INFINITY);
+        hi[e] = make_float2(-INFINITY, -INFINITY);
       }
       if (g < hkv && slice < slices) {
-        for (int j = slice; j < n; j += kRows * slices) {
-          typename V::Raw u[kRows], v[kRows];
-          const T* src = static_cast<const T*>(A.k_new) + (t + j) * A.k_ts + g * A.k_hs;
+        const T* src = static_cast<const T*>(A.k_new) + static_cast<int64_t>(t) * A.k_ts + g * A.k_hs;
+#pragma unroll 2
+        for (int j = slice; j < n; j += slices) {
+          float2 x[4];
+          if (own) {
+            widen8<T>(V::load(src + j * A.k_ts + ca), V::load(src + j * A.k_ts + cb), x);
+            rotate8(A, angles_of(A, G.l, slot + j), x);
 #pragma unroll
-          for (int k = 0; k < kRows; ++k) {
-            if (own && j + k * slices < n) {
-              u[k] = V::load(src + k * slices * A.k_ts + ca);
-              v[k] = V::load(src + k * slices * A.k_ts + cb);
+            for (int e = 0; e < 4; ++e) {
+              lo[e] = min_of(lo[e], x[e]);
+              hi[e] = max_of(hi[e], x[e]);
             }
           }
-#pragma unroll
-          for (int k = 0; k < kRows; ++k) {
-            const int jk = j + k * slices;
-            if (jk < n) {
-              float x[8];
-              if (own) {
-                widen8<T>(u[k], v[k], x);
-                rotate8(A, angles_of(A, G.l, slot + jk), x);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  lo[e] = fminf(lo[e], x[e]);
-                  hi[e] = fmaxf(hi[e], x[e]);
-                }
-              }
-              store_row<W>(A, false, row0 + jk + static_cast<int64_t>(g) * page, G.l, own, ca, cb, x, G.mask);
-            }
-          }
+          store_row<W, kCache>(A, false, row0 + j + static_cast<int64_t>(g) * page, G.l, own, ca, cb, x, G.mask);
         }
       }
       if (slices > 1) {
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          s_lo[e * kThreads + threadIdx.x] = lo[e];
-          s_hi[e * kThreads + threadIdx.x] = hi[e];
+        for (int e = 0; e < 4; ++e) {
+          s_lo[e][threadIdx.x] = lo[e];
+          s_hi[e][threadIdx.x] = hi[e];
         }
         __syncthreads();
         if (slice == 0) {
+#pragma unroll 1
           for (int o = 1; o < slices; ++o) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              lo[e] = fminf(lo[e], s_lo[e * kThreads + threadIdx.x + o * hkv * W]);
-              hi[e] = fmaxf(hi[e], s_hi[e * kThreads + threadIdx.x + o * hkv * W]);
+            for (int e = 0; e < 4; ++e) {
+              lo[e] = min_of(lo[e], s_lo[e][threadIdx.x + o * hkv * W]);
+              hi[e] = max_of(hi[e], s_hi[e][threadIdx.x + o * hkv * W]);
             }
           }
         }
@@ -412,14 +447,14 @@ __device__ __forceinline__ void append_pages(const AppendArgs& A, int t0, float 
         const int64_t plane = row0 / page + g;  // page * hkv + g
         __nv_bfloat16* dst = A.bounds + plane * 2 * A.pool.d;
         if (at > 0) {
-          float x[8];
+          float2 x[4];
           widen8<__nv_bfloat16>(*reinterpret_cast<const uint2*>(dst + ca), *reinterpret_cast<const uint2*>(dst + cb), x);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) lo[e] = fminf(lo[e], x[e]);
+          for (int e = 0; e < 4; ++e) lo[e] = min_of(lo[e], x[e]);
           widen8<__nv_bfloat16>(*reinterpret_cast<const uint2*>(dst + A.pool.d + ca),
                                 *reinterpret_cast<const uint2*>(dst + A.pool.d + cb), x);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) hi[e] = fmaxf(hi[e], x[e]);
+          for (int e = 0; e < 4; ++e) hi[e] = max_of(hi[e], x[e]);
         }
         store8_bf16(dst, ca, cb, lo);
         store8_bf16(dst + A.pool.d, ca, cb, hi);
@@ -428,11 +463,11 @@ __device__ __forceinline__ void append_pages(const AppendArgs& A, int t0, float 
   }
 }
 
-template <typename T, int W>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs A) {
-  __shared__ float s_lo[8 * kThreads], s_hi[8 * kThreads];
+template <typename T, int W, int kCache>
+__global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendArgs A) {
+  __shared__ float2 s_lo[4][kThreads], s_hi[4][kThreads];
   if (static_cast<int>(blockIdx.x) < A.page_blocks) {
-    append_pages<T, W>(A, static_cast<int>(blockIdx.x) * A.window, s_lo, s_hi);
+    append_pages<T, W, kCache>(A, static_cast<int>(blockIdx.x) * A.window, s_lo, s_hi);
     return;
   }
   const int64_t block = static_cast<int64_t>(blockIdx.x) - A.page_blocks;
@@ -451,7 +486,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs A) {
   const int64_t t = item / A.parts;
   if (t >= A.total) return;
   const int r0 = static_cast<int>(item - t * A.parts) * A.part_rows;
-  append_token<T, W>(A, static_cast<int>(t), r0, min(r0 + A.part_rows, A.token_rows));
+  append_token<T, W, kCache>(A, static_cast<int>(t), r0, min(r0 + A.part_rows, A.token_rows));
 }
 
 // ---------------------------------------------------------------- read back
@@ -471,7 +506,7 @@ struct ReadArgs {
 };
 
 // A group of W lanes takes one token and `part_rows` of its 2 hkv rows.
-template <int W>
+template <int W, int kCache>
 __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs A) {
   const Group<W> G;
   const int d = A.pool.d, hkv = A.pool.hkv;
@@ -494,34 +529,42 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs A) {
     const int64_t row = row0 + static_cast<int64_t>(g) * A.pool.page_size;
     const void* pool = is_v ? A.v_cache : A.k_cache;
     const float* scales = is_v ? A.v_scales : A.k_scales;
-    float x[8];
-    if (A.cache_dtype == FA_BF16) {
+    float2 x[4];
+    if constexpr (kCache == FA_BF16) {
       const uint4 w = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(pool) + row * d + 8 * G.l));
       widen8<__nv_bfloat16>(make_uint2(w.x, w.y), make_uint2(w.z, w.w), x);
-    } else if (A.cache_dtype == FA_I8) {
+    } else if constexpr (kCache == FA_I8) {
       const uint2 w = __ldcs(reinterpret_cast<const uint2*>(static_cast<const int8_t*>(pool) + row * d + 8 * G.l));
       const float s = scales[row];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t u = e < 4 ? w.x : w.y;
-        x[e] = __fmul_rn(static_cast<float>(static_cast<int8_t>(u >> (8 * (e & 3)))), s);
+      for (int e = 0; e < 4; ++e) {
+        const int u = static_cast<int>(e < 2 ? w.x : w.y) >> (16 * (e & 1));
+        x[e] = mul2(make_float2(static_cast<float>(static_cast<int8_t>(u)), static_cast<float>(static_cast<int8_t>(u >> 8))),
+                    make_float2(s, s));
       }
     } else {
       const uint32_t w =
           __ldcs(reinterpret_cast<const unsigned int*>(static_cast<const uint8_t*>(pool) + row * (d / 2) + 4 * G.l));
       const float2 s = *reinterpret_cast<const float2*>(scales + 2 * row);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = __fadd_rn(__fmul_rn(static_cast<float>((w >> (4 * e)) & 15u), s.x), s.y);
+      for (int e = 0; e < 4; ++e) {
+        // code + 2^23, exact, less 2^23
+        const float2 c = make_float2(__uint_as_float(((w >> (8 * e)) & 15u) | 0x4b000000u),
+                                     __uint_as_float(((w >> (8 * e + 4)) & 15u) | 0x4b000000u));
+        const float2 code = add2(c, make_float2(-8388608.0f, -8388608.0f));
+        // in scalars: a packed product and sum would become one operation
+        x[e] = make_float2(__fadd_rn(__fmul_rn(code.x, s.x), s.y), __fadd_rn(__fmul_rn(code.y, s.x), s.y));
+      }
     }
     const int64_t at = (static_cast<int64_t>(g) * A.total + t) * d + 8 * G.l;
     if (A.out_f32) {
       float* dst = static_cast<float*>(is_v ? A.v_out : A.k_out) + at;
-      __stcs(reinterpret_cast<float4*>(dst), make_float4(x[0], x[1], x[2], x[3]));
-      __stcs(reinterpret_cast<float4*>(dst + 4), make_float4(x[4], x[5], x[6], x[7]));
+      __stcs(reinterpret_cast<float4*>(dst), make_float4(x[0].x, x[0].y, x[1].x, x[1].y));
+      __stcs(reinterpret_cast<float4*>(dst + 4), make_float4(x[2].x, x[2].y, x[3].x, x[3].y));
     } else {
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? A.v_out : A.k_out) + at;
-      __stcs(reinterpret_cast<uint4*>(dst),
-             make_uint4(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]), bf16x2(x[4], x[5]), bf16x2(x[6], x[7])));
+      const uint2 u = pack4(x[0], x[1]), v = pack4(x[2], x[3]);
+      __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_v ? A.v_out : A.k_out) + at),
+             make_uint4(u.x, u.y, v.x, v.y));
     }
   }
 }
@@ -547,7 +590,7 @@ int rows_per_item(int64_t total, int rows, int groups) {
   return per;
 }
 
-template <typename T, int W>
+template <typename T, int W, int kCache>
 fa_status launch_append_typed(AppendArgs& A, const LaunchCtx& ctx) {
   constexpr int kGroups = kThreads / W;
   A.token_rows = A.hq + (A.bounds != nullptr ? 1 : 2) * A.pool.hkv;
@@ -559,29 +602,41 @@ fa_status launch_append_typed(AppendArgs& A, const LaunchCtx& ctx) {
   A.page_blocks = A.bounds != nullptr ? (A.total + A.window - 1) / A.window : 0;
   blocks += A.page_blocks;
   if (blocks >= (int64_t(1) << 31)) return FA_ERR_UNSUPPORTED;
-  note_variant(reinterpret_cast<const void*>(append_kernel<T, W>));
-  append_kernel<T, W><<<static_cast<unsigned>(blocks), kThreads, 0, ctx.stream>>>(A);
+  note_variant(reinterpret_cast<const void*>(append_kernel<T, W, kCache>));
+  append_kernel<T, W, kCache><<<static_cast<unsigned>(blocks), kThreads, 0, ctx.stream>>>(A);
   return cuda_status(cudaGetLastError());
+}
+template <typename T, int W>
+fa_status launch_append_width(AppendArgs& A, const LaunchCtx& ctx) {
+  if (A.cache_dtype == FA_BF16) return launch_append_typed<T, W, FA_BF16>(A, ctx);
+  if (A.cache_dtype == FA_I8) return launch_append_typed<T, W, FA_I8>(A, ctx);
+  return launch_append_typed<T, W, FA_I4>(A, ctx);
 }
 template <typename T>
 fa_status launch_append(AppendArgs& A, const LaunchCtx& ctx) {
-  if (A.pool.d <= 16) return launch_append_typed<T, 2>(A, ctx);
-  if (A.pool.d <= 32) return launch_append_typed<T, 4>(A, ctx);
-  if (A.pool.d <= 64) return launch_append_typed<T, 8>(A, ctx);
-  if (A.pool.d <= 128) return launch_append_typed<T, 16>(A, ctx);
-  return launch_append_typed<T, 32>(A, ctx);
+  if (A.pool.d <= 16) return launch_append_width<T, 2>(A, ctx);
+  if (A.pool.d <= 32) return launch_append_width<T, 4>(A, ctx);
+  if (A.pool.d <= 64) return launch_append_width<T, 8>(A, ctx);
+  if (A.pool.d <= 128) return launch_append_width<T, 16>(A, ctx);
+  return launch_append_width<T, 32>(A, ctx);
 }
 
-template <int W>
-fa_status launch_read(ReadArgs& A, const LaunchCtx& ctx) {
+template <int W, int kCache>
+fa_status launch_read_typed(ReadArgs& A, const LaunchCtx& ctx) {
   constexpr int kGroups = kThreads / W;
   A.part_rows = rows_per_item(A.total, 2 * A.pool.hkv, kGroups);
   A.parts = (2 * A.pool.hkv + A.part_rows - 1) / A.part_rows;
   const int64_t blocks = (static_cast<int64_t>(A.total) * A.parts + kGroups - 1) / kGroups;
   if (blocks >= (int64_t(1) << 31)) return FA_ERR_UNSUPPORTED;
-  note_variant(reinterpret_cast<const void*>(read_kernel<W>));
-  read_kernel<W><<<static_cast<unsigned>(blocks), kThreads, 0, ctx.stream>>>(A);
+  note_variant(reinterpret_cast<const void*>(read_kernel<W, kCache>));
+  read_kernel<W, kCache><<<static_cast<unsigned>(blocks), kThreads, 0, ctx.stream>>>(A);
   return cuda_status(cudaGetLastError());
+}
+template <int W>
+fa_status launch_read(ReadArgs& A, const LaunchCtx& ctx) {
+  if (A.cache_dtype == FA_BF16) return launch_read_typed<W, FA_BF16>(A, ctx);
+  if (A.cache_dtype == FA_I8) return launch_read_typed<W, FA_I8>(A, ctx);
+  return launch_read_typed<W, FA_I4>(A, ctx);
 }
 
 }  // namespace

@@ -252,6 +252,13 @@ def test_read_back(kind, out_dtype):
                 # code * step + offset: two fp32 roundings of terms no larger than 16 steps; then out_dtype's
                 tol = 2.0 ** -24 * 4 * (np.abs(ref) + 16) + (2.0 ** -8 * np.abs(ref) if out_dtype == torch.bfloat16 else 0)
                 assert (np.abs(y - ref) <= tol).all()
+                if kind == "int4" and out_dtype == torch.float32:  # each of the two rounded, no fused operation
+                    keys = np.arange(start[b], start[b] + n[b])
+                    p, o = c.table[b].numpy()[keys // 24], keys % 24
+                    pool, sc = (c.kp, c.ks) if got is k else (c.vp, c.vs)
+                    sc = sc[p, g, o].numpy()
+                    want32 = plain.unpack4(pool[p, g, o].numpy()).astype(np.float32) * sc[:, :1] + sc[:, 1:]
+                    assert np.array_equal(got[g, at:at + n[b]].cpu().numpy(), want32)
         at += n[b]
     assert (k[:, at:] == 9).all() and (v[:, at:] == 9).all()
     # from the start, and past what the table covers
