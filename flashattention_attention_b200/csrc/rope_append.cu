@@ -17,6 +17,8 @@
 // (of the first new token in it), its groups spread over KV heads and slices
 // of the page's tokens, the slices' bounds joined in shared memory.  No page
 // is touched by two CTAs, so there are no atomics and no order to depend on.
+#include <type_traits>
+
 #include "internal.h"
 #include "quant.cuh"
 
@@ -49,9 +51,8 @@ struct AppendArgs {
   int batch, total, hq, rot, interleaved, rope_rows;
   int cache_dtype;
   // how the work is cut: rows per token (without keys that the page role
-  // takes), rows per item and items per token; page role: its CTAs and the
-  // tokens each looks at
-  int token_rows, part_rows, parts, page_blocks, window;
+  // takes), rows per part; page role: the tokens a CTA looks at
+  int token_rows, part_rows, window;
   PoolArgs pool;
   Watchdog wd;
 };
@@ -222,15 +223,31 @@ __device__ __noinline__ uint32_t codes8_any(float2 x0, float2 x1, float s) {
 }
 __device__ __noinline__ float divide_any(float a, float b) { return __fdiv_rn(a, b); }
 
+// Where rows go: the current one's codes or values and its scales, and the way
+// to the next KV head's (or the next slot's).
+template <int kCache>
+struct Sink {
+  uint8_t* dst;
+  float* scale;
+  static constexpr int kScales = kCache == FA_I4 ? 2 : kCache == FA_I8 ? 1 : 0;
+  __device__ __forceinline__ static int row_bytes(int d) {
+    return kCache == FA_BF16 ? 2 * d : kCache == FA_I8 ? d : d / 2;
+  }
+  __device__ __forceinline__ Sink(void* pool, float* scales, int64_t row, int d)
+      : dst(static_cast<uint8_t*>(pool) + row * row_bytes(d)), scale(scales + row * kScales) {}
+  __device__ __forceinline__ void advance(int rows, int d) {
+    dst += static_cast<int64_t>(rows) * row_bytes(d);
+    scale += static_cast<int64_t>(rows) * kScales;
+  }
+};
+
 // One row into the cache by the W lanes that hold it (`own`: this lane holds
 // channels).  Every lane of the group calls.
 template <int W, int kCache>
-__device__ __forceinline__ void store_row(const AppendArgs& A, bool is_v, int64_t row, int l, bool own, int a, int b,
-                                          const float2 (&x)[4], unsigned mask) {
-  void* pool = is_v ? A.v_cache : A.k_cache;
-  const int d = A.pool.d;
+__device__ __forceinline__ void store_row(const Sink<kCache>& to, int l, bool own, int a, int b, const float2 (&x)[4],
+                                          unsigned mask) {
   if constexpr (kCache == FA_BF16) {
-    if (own) store8_bf16(static_cast<__nv_bfloat16*>(pool) + row * d, a, b, x);
+    if (own) store8_bf16(reinterpret_cast<__nv_bfloat16*>(to.dst), a, b, x);
   } else if constexpr (kCache == FA_I8) {
     float amax = 0.0f;
     if (own) {
@@ -242,7 +259,6 @@ __device__ __forceinline__ void store_row(const AppendArgs& A, bool is_v, int64_
     constexpr float k127 = 1.0f / 127.0f;
     const float s = ordinary(amax) ? divide_by(amax, 127.0f, k127) : divide_any(amax, 127.0f);
     if (own) {
-      int8_t* dst = static_cast<int8_t*>(pool) + row * d;
       uint32_t u, v;
       if (ordinary(s)) {
         const float y = __frcp_rn(s);
@@ -253,9 +269,9 @@ __device__ __forceinline__ void store_row(const AppendArgs& A, bool is_v, int64_
         u = codes8_any(x[0], x[1], s);
         v = codes8_any(x[2], x[3], s);
       }
-      *reinterpret_cast<uint32_t*>(dst + a) = u;
-      *reinterpret_cast<uint32_t*>(dst + b) = v;
-      if (l == 0) (is_v ? A.v_scales : A.k_scales)[row] = s;
+      *reinterpret_cast<uint32_t*>(to.dst + a) = u;
+      *reinterpret_cast<uint32_t*>(to.dst + b) = v;
+      if (l == 0) *to.scale = s;
     }
   } else {
     float lo = INFINITY, hi = -INFINITY;
@@ -273,7 +289,6 @@ __device__ __forceinline__ void store_row(const AppendArgs& A, bool is_v, int64_
     }
     const float r = __fsub_rn(hi, lo);
     if (own) {
-      uint8_t* dst = static_cast<uint8_t*>(pool) + row * (d / 2);
       uint32_t u, v;
       float step;
       if (ordinary(r)) {
@@ -287,9 +302,9 @@ __device__ __forceinline__ void store_row(const AppendArgs& A, bool is_v, int64_
         u = codes4_any(x[0], x[1], lo, r);
         v = codes4_any(x[2], x[3], lo, r);
       }
-      *reinterpret_cast<uint16_t*>(dst + a / 2) = static_cast<uint16_t>(u);
-      *reinterpret_cast<uint16_t*>(dst + b / 2) = static_cast<uint16_t>(v);
-      if (l == 0) *reinterpret_cast<float2*>((is_v ? A.v_scales : A.k_scales) + 2 * row) = make_float2(step, lo);
+      *reinterpret_cast<uint16_t*>(to.dst + a / 2) = static_cast<uint16_t>(u);
+      *reinterpret_cast<uint16_t*>(to.dst + b / 2) = static_cast<uint16_t>(v);
+      if (l == 0) *reinterpret_cast<float2*>(to.scale) = make_float2(step, lo);
     }
   }
 }
@@ -343,20 +358,25 @@ __device__ __forceinline__ void append_token(const AppendArgs& A, int t, int r0,
       }
     }
   }
+  // heads [g0, g1) of V or K
+  auto cached = [&](auto rotated, const void* rows, int64_t ts, int64_t hs, void* pool, float* scales, int g0, int g1) {
+    constexpr bool kRotated = decltype(rotated)::value;
+    const int ra = kRotated ? a : 8 * G.l, rb = kRotated ? b : 8 * G.l + 4;
+    const T* src = static_cast<const T*>(rows) + t * ts + g0 * hs;
+    Sink<kCache> to(pool, scales, p.row0 + static_cast<int64_t>(g0) * A.pool.page_size, A.pool.d);
 #pragma unroll 2
-  for (int r = max(r0, hq) - hq; r < r1 - hq; ++r) {
-    const bool is_v = r < hkv;
-    const int g = is_v ? r : r - hkv;
-    const int ra = is_v ? 8 * G.l : a, rb = is_v ? 8 * G.l + 4 : b;
-    float2 x[4];
-    if (own) {
-      const T* src = is_v ? static_cast<const T*>(A.v_new) + t * A.v_ts + g * A.v_hs
-                          : static_cast<const T*>(A.k_new) + t * A.k_ts + g * A.k_hs;
-      widen8<T>(V::load(src + ra), V::load(src + rb), x);
-      if (!is_v) rotate8(A, ang, x);
+    for (int g = g0; g < g1; ++g, src += hs) {
+      float2 x[4];
+      if (own) {
+        widen8<T>(V::load(src + ra), V::load(src + rb), x);
+        if constexpr (kRotated) rotate8(A, ang, x);
+      }
+      store_row<W, kCache>(to, G.l, own, ra, rb, x, G.mask);
+      to.advance(A.pool.page_size, A.pool.d);
     }
-    store_row<W, kCache>(A, is_v, p.row0 + static_cast<int64_t>(g) * A.pool.page_size, G.l, own, ra, rb, x, G.mask);
-  }
+  };
+  cached(std::false_type{}, A.v_new, A.v_ts, A.v_hs, A.v_cache, A.v_scales, max(r0 - hq, 0), min(r1 - hq, hkv));
+  cached(std::true_type{}, A.k_new, A.k_ts, A.k_hs, A.k_cache, A.k_scales, max(r0 - hq - hkv, 0), r1 - hq - hkv);
 }
 
 __device__ __forceinline__ float2 min_of(float2 a, float2 b) { return make_float2(fminf(a.x, b.x), fminf(a.y, b.y)); }
@@ -408,12 +428,13 @@ __device__ __forceinline__ void append_pages(const AppendArgs& A, int t0, float2
         hi[e] = make_float2(-INFINITY, -INFINITY);
       }
       if (g < hkv && slice < slices) {
-        const T* src = static_cast<const T*>(A.k_new) + static_cast<int64_t>(t) * A.k_ts + g * A.k_hs;
+        const T* src = static_cast<const T*>(A.k_new) + static_cast<int64_t>(t + slice) * A.k_ts + g * A.k_hs;
+        Sink<kCache> to(A.k_cache, A.k_scales, row0 + slice + static_cast<int64_t>(g) * page, A.pool.d);
 #pragma unroll 2
-        for (int j = slice; j < n; j += slices) {
+        for (int j = slice; j < n; j += slices, src += slices * A.k_ts) {
           float2 x[4];
           if (own) {
-            widen8<T>(V::load(src + j * A.k_ts + ca), V::load(src + j * A.k_ts + cb), x);
+            widen8<T>(V::load(src + ca), V::load(src + cb), x);
             rotate8(A, angles_of(A, G.l, slot + j), x);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -421,7 +442,8 @@ __device__ __forceinline__ void append_pages(const AppendArgs& A, int t0, float2
               hi[e] = max_of(hi[e], x[e]);
             }
           }
-          store_row<W, kCache>(A, false, row0 + j + static_cast<int64_t>(g) * page, G.l, own, ca, cb, x, G.mask);
+          store_row<W, kCache>(to, G.l, own, ca, cb, x, G.mask);
+          to.advance(slices, A.pool.d);
         }
       }
       if (slices > 1) {
@@ -466,12 +488,17 @@ __device__ __forceinline__ void append_pages(const AppendArgs& A, int t0, float2
 template <typename T, int W, int kCache>
 __global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendArgs A) {
   __shared__ float2 s_lo[4][kThreads], s_hi[4][kThreads];
-  if (static_cast<int>(blockIdx.x) < A.page_blocks) {
-    append_pages<T, W, kCache>(A, static_cast<int>(blockIdx.x) * A.window, s_lo, s_hi);
-    return;
+  // grid row 0 is the page role (where bounds are kept), the others are the parts of the tokens' rows
+  int part = static_cast<int>(blockIdx.y);
+  if (A.bounds != nullptr) {
+    if (part == 0) {
+      if (static_cast<int64_t>(blockIdx.x) * A.window < A.total)
+        append_pages<T, W, kCache>(A, static_cast<int>(blockIdx.x) * A.window, s_lo, s_hi);
+      return;
+    }
+    --part;
   }
-  const int64_t block = static_cast<int64_t>(blockIdx.x) - A.page_blocks;
-  if (A.seqlens != nullptr && block == 0) {
+  if (A.seqlens != nullptr && blockIdx.x == 0 && part == 0) {
     for (int b = threadIdx.x; b < A.batch; b += kThreads) {
       const int64_t c0 = A.cu != nullptr ? A.cu[b] : b, c1 = A.cu != nullptr ? A.cu[b + 1] : b + 1;
       const int64_t end = static_cast<int64_t>(A.cur_pos[b]) + (c1 - c0);
@@ -482,10 +509,9 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendArgs A)
       }
     }
   }
-  const int64_t item = block * (kThreads / W) + threadIdx.x / W;
-  const int64_t t = item / A.parts;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / W) + threadIdx.x / W;
   if (t >= A.total) return;
-  const int r0 = static_cast<int>(item - t * A.parts) * A.part_rows;
+  const int r0 = part * A.part_rows;
   append_token<T, W, kCache>(A, static_cast<int>(t), r0, min(r0 + A.part_rows, A.token_rows));
 }
 
@@ -500,19 +526,20 @@ struct ReadArgs {
   const int32_t* cu;
   const int32_t* start;
   int batch, total, cache_dtype, out_f32;
-  int part_rows, parts;  // rows per item, items per token
+  int part_rows;  // of a token's rows, per grid row
   PoolArgs pool;
   Watchdog wd;
 };
 
-// A group of W lanes takes one token and `part_rows` of its 2 hkv rows.
+// A group of W lanes takes one token and `part_rows` of its 2 hkv rows (one
+// part per grid row).
 template <int W, int kCache>
 __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs A) {
   const Group<W> G;
   const int d = A.pool.d, hkv = A.pool.hkv;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / W) + threadIdx.x / W;
-  const int part = static_cast<int>(item / A.total), t = static_cast<int>(item - static_cast<int64_t>(part) * A.total);
-  if (part >= A.parts) return;  // neighbouring groups read and write neighbouring rows
+  const int64_t at_token = static_cast<int64_t>(blockIdx.x) * (kThreads / W) + threadIdx.x / W;
+  if (at_token >= A.total) return;
+  const int t = static_cast<int>(at_token), part = blockIdx.y;  // neighbouring groups: neighbouring rows
   int b, i;
   int64_t row0;
   if (!seq_of_token(A.cu, A.batch, t, b, i)) return;
@@ -581,8 +608,8 @@ PoolArgs pool_args(const fa_kv_pages& pg, int hkv, int d) {
   return P;
 }
 
-// Rows per item: four, and twice that while the items fill the device several
-// times over (the lookups of a token are then spread over more rows).
+// Rows of a token per group: four, and twice that while the groups fill the
+// device several times over (the lookups of a token are then spread over more rows).
 int rows_per_item(int64_t total, int rows, int groups) {
   const int64_t enough = static_cast<int64_t>(device_sm_count()) * 8 * groups;
   int per = kRows;
@@ -595,15 +622,14 @@ fa_status launch_append_typed(AppendArgs& A, const LaunchCtx& ctx) {
   constexpr int kGroups = kThreads / W;
   A.token_rows = A.hq + (A.bounds != nullptr ? 1 : 2) * A.pool.hkv;
   A.part_rows = rows_per_item(A.total, A.token_rows, kGroups);
-  A.parts = (A.token_rows + A.part_rows - 1) / A.part_rows;
-  int64_t blocks = (static_cast<int64_t>(A.total) * A.parts + kGroups - 1) / kGroups;
-  if (blocks < 1) blocks = 1;  // cache_seqlens alone
+  const int parts = (A.token_rows + A.part_rows - 1) / A.part_rows;
   A.window = A.total <= 4 * device_sm_count() ? 1 : 8;
-  A.page_blocks = A.bounds != nullptr ? (A.total + A.window - 1) / A.window : 0;
-  blocks += A.page_blocks;
-  if (blocks >= (int64_t(1) << 31)) return FA_ERR_UNSUPPORTED;
+  int blocks = A.total / kGroups + 1;  // at least one, for cache_seqlens alone
+  const int page_blocks = A.bounds != nullptr ? A.total / A.window + 1 : 0;
+  if (blocks < page_blocks) blocks = page_blocks;
+  if (parts >= 65535) return FA_ERR_UNSUPPORTED;
   note_variant(reinterpret_cast<const void*>(append_kernel<T, W, kCache>));
-  append_kernel<T, W, kCache><<<static_cast<unsigned>(blocks), kThreads, 0, ctx.stream>>>(A);
+  append_kernel<T, W, kCache><<<dim3(blocks, parts + (A.bounds != nullptr ? 1 : 0)), kThreads, 0, ctx.stream>>>(A);
   return cuda_status(cudaGetLastError());
 }
 template <typename T, int W>
@@ -625,11 +651,10 @@ template <int W, int kCache>
 fa_status launch_read_typed(ReadArgs& A, const LaunchCtx& ctx) {
   constexpr int kGroups = kThreads / W;
   A.part_rows = rows_per_item(A.total, 2 * A.pool.hkv, kGroups);
-  A.parts = (2 * A.pool.hkv + A.part_rows - 1) / A.part_rows;
-  const int64_t blocks = (static_cast<int64_t>(A.total) * A.parts + kGroups - 1) / kGroups;
-  if (blocks >= (int64_t(1) << 31)) return FA_ERR_UNSUPPORTED;
+  const int parts = (2 * A.pool.hkv + A.part_rows - 1) / A.part_rows;
+  if (parts > 65535) return FA_ERR_UNSUPPORTED;
   note_variant(reinterpret_cast<const void*>(read_kernel<W, kCache>));
-  read_kernel<W, kCache><<<static_cast<unsigned>(blocks), kThreads, 0, ctx.stream>>>(A);
+  read_kernel<W, kCache><<<dim3((A.total - 1) / kGroups + 1, parts), kThreads, 0, ctx.stream>>>(A);
   return cuda_status(cudaGetLastError());
 }
 template <int W>
