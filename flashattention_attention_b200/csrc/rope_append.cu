@@ -3,12 +3,12 @@
 // read-back of cached rows (FlashRT QKV Cache RoPE, Kernels: rotation and
 // cache write of the new K fused in one kernel).
 //
-// A row of d channels is held by W lanes (d / 8 rounded up to a power of two),
-// eight channels per lane in two chunks of four.  Rotating channel pairs (i, i
-// + rot/2), lane i takes the chunks [4i, 4i+4) and [rot/2 + 4i, +4), so both
-// members of a pair sit in one lane; rotating pairs (2i, 2i+1), and for
-// channels past rot_dim, the two chunks are adjacent.  Either way lane i's
-// four pairs use angles 4i .. 4i+3.
+// A row of d channels is held by W lanes (d / 16 rounded up to a power of two),
+// 16 channels per lane in two chunks of eight (16-byte loads of bf16).  Rotating
+// channel pairs (i, i + rot/2), lane i takes the chunks [8i, 8i+8) and [rot/2 +
+// 8i, +8), so both members of a pair sit in one lane; rotating pairs (2i,
+// 2i+1), and for channels past rot_dim, the two chunks are adjacent.  Either way
+// lane i's eight pairs use angles 8i .. 8i+7.
 //
 // One launch does everything.  A group of W lanes takes one token and some of
 // its rows: the token's sequence, slot, page and angles are found once and
@@ -101,40 +101,66 @@ __device__ __forceinline__ bool place_token(const AppendArgs& A, int t, Place& p
 
 // Channel offsets of lane `l`'s two chunks.
 __device__ __forceinline__ void chunk_offsets(const AppendArgs& A, int l, bool rotated, int& a, int& b) {
-  if (rotated && !A.interleaved && 8 * l < A.rot) {
-    a = 4 * l;
-    b = A.rot / 2 + 4 * l;
-  } else {
+  if (rotated && !A.interleaved && 16 * l < A.rot) {
     a = 8 * l;
-    b = a + 4;
+    b = A.rot / 2 + 8 * l;
+  } else {
+    a = 16 * l;
+    b = a + 8;
   }
 }
 
-// A lane's eight channels: x[0], x[1] of chunk a, x[2], x[3] of chunk b.
+// Eight consecutive elements as they are loaded, and their exact widening.
 template <typename T>
-__device__ __forceinline__ void widen8(const typename Vec4<T>::Raw& u, const typename Vec4<T>::Raw& v, float2 (&x)[4]) {
-  float y[4], z[4];
-  Vec4<T>::widen(u, y);
-  Vec4<T>::widen(v, z);
-  x[0] = make_float2(y[0], y[1]);
-  x[1] = make_float2(y[2], y[3]);
-  x[2] = make_float2(z[0], z[1]);
-  x[3] = make_float2(z[2], z[3]);
-}
+struct Chunk;
+template <>
+struct Chunk<__nv_bfloat16> {
+  uint4 raw;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { raw = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void widen(float2* x) const {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+  }
+};
+template <>
+struct Chunk<float> {
+  float4 lo, hi;
+  __device__ __forceinline__ void load(const float* p) {
+    lo = __ldcs(reinterpret_cast<const float4*>(p));
+    hi = __ldcs(reinterpret_cast<const float4*>(p + 4));
+  }
+  __device__ __forceinline__ void widen(float2* x) const {
+    x[0] = make_float2(lo.x, lo.y);
+    x[1] = make_float2(lo.z, lo.w);
+    x[2] = make_float2(hi.x, hi.y);
+    x[3] = make_float2(hi.z, hi.w);
+  }
+};
 
-// The lane's four angles at a slot; no rotation for lanes past rot_dim.
+// A lane's 16 channels are x[0 .. 3] of chunk a and x[4 .. 7] of chunk b.
+
+// The lane's eight angles at a slot; no rotation for lanes past rot_dim.
 struct Angles {
-  float4 c, s;
+  float2 c[4], s[4];
   bool any;
 };
 __device__ __forceinline__ Angles angles_of(const AppendArgs& A, int l, int64_t slot) {
   Angles r;
-  r.any = 8 * l < A.rot;
-  r.c = r.s = make_float4(0.f, 0.f, 0.f, 0.f);
+  r.any = 16 * l < A.rot;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) r.c[e] = r.s[e] = make_float2(0.f, 0.f);
   if (r.any) {
-    const float* row = A.rope + slot * A.rot;
-    r.c = *reinterpret_cast<const float4*>(row + 4 * l);
-    r.s = *reinterpret_cast<const float4*>(row + A.rot / 2 + 4 * l);
+    const float4* c = reinterpret_cast<const float4*>(A.rope + slot * A.rot + 8 * l);
+    const float4* s = reinterpret_cast<const float4*>(A.rope + slot * A.rot + A.rot / 2 + 8 * l);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float4 u = c[e], v = s[e];
+      r.c[2 * e] = make_float2(u.x, u.y);
+      r.c[2 * e + 1] = make_float2(u.z, u.w);
+      r.s[2 * e] = make_float2(v.x, v.y);
+      r.s[2 * e + 1] = make_float2(v.z, v.w);
+    }
   }
   return r;
 }
@@ -146,26 +172,20 @@ __device__ __forceinline__ void rotate_pair(float& a, float& b, float c, float s
   a = __fsub_rn(__fmul_rn(x, c), __fmul_rn(b, s));
   b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(x, s));
 }
-__device__ __forceinline__ void rotate_pairs(float2& a, float2& b, float2 c, float2 s) {
-  rotate_pair(a.x, b.x, c.x, s.x);
-  rotate_pair(a.y, b.y, c.y, s.y);
-}
-__device__ __forceinline__ void rotate8(const AppendArgs& A, const Angles& g, float2 (&x)[4]) {
+__device__ __forceinline__ void rotate16(const AppendArgs& A, const Angles& g, float2 (&x)[8]) {
   if (!g.any) return;
-  const float2 c0 = make_float2(g.c.x, g.c.y), c1 = make_float2(g.c.z, g.c.w);
-  const float2 s0 = make_float2(g.s.x, g.s.y), s1 = make_float2(g.s.z, g.s.w);
   if (A.interleaved) {
-    float2 a0 = make_float2(x[0].x, x[1].x), b0 = make_float2(x[0].y, x[1].y);
-    float2 a1 = make_float2(x[2].x, x[3].x), b1 = make_float2(x[2].y, x[3].y);
-    rotate_pairs(a0, b0, c0, s0);
-    rotate_pairs(a1, b1, c1, s1);
-    x[0] = make_float2(a0.x, b0.x);
-    x[1] = make_float2(a0.y, b0.y);
-    x[2] = make_float2(a1.x, b1.x);
-    x[3] = make_float2(a1.y, b1.y);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      rotate_pair(x[2 * e].x, x[2 * e].y, g.c[e].x, g.s[e].x);
+      rotate_pair(x[2 * e + 1].x, x[2 * e + 1].y, g.c[e].y, g.s[e].y);
+    }
   } else {
-    rotate_pairs(x[0], x[2], c0, s0);
-    rotate_pairs(x[1], x[3], c1, s1);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      rotate_pair(x[e].x, x[4 + e].x, g.c[e].x, g.s[e].x);
+      rotate_pair(x[e].y, x[4 + e].y, g.c[e].y, g.s[e].y);
+    }
   }
 }
 
@@ -173,10 +193,12 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
 }
-__device__ __forceinline__ uint2 pack4(float2 lo, float2 hi) { return make_uint2(bf16x2(lo.x, lo.y), bf16x2(hi.x, hi.y)); }
-__device__ __forceinline__ void store8_bf16(__nv_bfloat16* row, int a, int b, const float2 (&x)[4]) {
-  *reinterpret_cast<uint2*>(row + a) = pack4(x[0], x[1]);
-  *reinterpret_cast<uint2*>(row + b) = pack4(x[2], x[3]);
+__device__ __forceinline__ uint4 pack8(const float2* x) {
+  return make_uint4(bf16x2(x[0].x, x[0].y), bf16x2(x[1].x, x[1].y), bf16x2(x[2].x, x[2].y), bf16x2(x[3].x, x[3].y));
+}
+__device__ __forceinline__ void store16_bf16(__nv_bfloat16* row, int a, int b, const float2 (&x)[8]) {
+  *reinterpret_cast<uint4*>(row + a) = pack8(x);
+  *reinterpret_cast<uint4*>(row + b) = pack8(x + 4);
 }
 
 // The quantisers below need correctly rounded quotients (codes and scales are
@@ -244,40 +266,42 @@ struct Sink {
 // One row into the cache by the W lanes that hold it (`own`: this lane holds
 // channels).  Every lane of the group calls.
 template <int W, int kCache>
-__device__ __forceinline__ void store_row(const Sink<kCache>& to, int l, bool own, int a, int b, const float2 (&x)[4],
+__device__ __forceinline__ void store_row(const Sink<kCache>& to, int l, bool own, int a, int b, const float2 (&x)[8],
                                           unsigned mask) {
   if constexpr (kCache == FA_BF16) {
-    if (own) store8_bf16(reinterpret_cast<__nv_bfloat16*>(to.dst), a, b, x);
+    if (own) store16_bf16(reinterpret_cast<__nv_bfloat16*>(to.dst), a, b, x);
   } else if constexpr (kCache == FA_I8) {
     float amax = 0.0f;
     if (own) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(x[e].x), fabsf(x[e].y)));
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(x[e].x), fabsf(x[e].y)));
     }
 #pragma unroll
     for (int off = W >> 1; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(mask, amax, off));
     constexpr float k127 = 1.0f / 127.0f;
     const float s = ordinary(amax) ? divide_by(amax, 127.0f, k127) : divide_any(amax, 127.0f);
     if (own) {
-      uint32_t u, v;
+      uint32_t w[4];
       if (ordinary(s)) {
         const float y = __frcp_rn(s);
-        const float p[4] = {x[0].x, x[0].y, x[1].x, x[1].y}, q[4] = {x[2].x, x[2].y, x[3].x, x[3].y};
-        u = quantise4_fast(p, s, y);
-        v = quantise4_fast(q, s, y);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float v[4] = {x[2 * e].x, x[2 * e].y, x[2 * e + 1].x, x[2 * e + 1].y};
+          w[e] = quantise4_fast(v, s, y);
+        }
       } else {
-        u = codes8_any(x[0], x[1], s);
-        v = codes8_any(x[2], x[3], s);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = codes8_any(x[2 * e], x[2 * e + 1], s);
       }
-      *reinterpret_cast<uint32_t*>(to.dst + a) = u;
-      *reinterpret_cast<uint32_t*>(to.dst + b) = v;
+      *reinterpret_cast<uint2*>(to.dst + a) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2*>(to.dst + b) = make_uint2(w[2], w[3]);
       if (l == 0) *to.scale = s;
     }
   } else {
     float lo = INFINITY, hi = -INFINITY;
     if (own) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < 8; ++e) {
         lo = min3f(lo, x[e].x, x[e].y);
         hi = max3f(hi, x[e].x, x[e].y);
       }
@@ -289,21 +313,21 @@ __device__ __forceinline__ void store_row(const Sink<kCache>& to, int l, bool ow
     }
     const float r = __fsub_rn(hi, lo);
     if (own) {
-      uint32_t u, v;
+      uint32_t w[4];
       float step;
       if (ordinary(r)) {
         const float y = __frcp_rn(r);
         constexpr float k15 = 1.0f / 15.0f;
         step = divide_by(r, 15.0f, k15);
-        u = codes4_fast(x[0], x[1], lo, r, y);
-        v = codes4_fast(x[2], x[3], lo, r, y);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = codes4_fast(x[2 * e], x[2 * e + 1], lo, r, y);
       } else {
         step = divide_any(r, 15.0f);
-        u = codes4_any(x[0], x[1], lo, r);
-        v = codes4_any(x[2], x[3], lo, r);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = codes4_any(x[2 * e], x[2 * e + 1], lo, r);
       }
-      *reinterpret_cast<uint16_t*>(to.dst + a / 2) = static_cast<uint16_t>(u);
-      *reinterpret_cast<uint16_t*>(to.dst + b / 2) = static_cast<uint16_t>(v);
+      *reinterpret_cast<uint32_t*>(to.dst + a / 2) = w[0] | (w[1] << 16);
+      *reinterpret_cast<uint32_t*>(to.dst + b / 2) = w[2] | (w[3] << 16);
       if (l == 0) *reinterpret_cast<float2*>(to.scale) = make_float2(step, lo);
     }
   }
@@ -316,15 +340,14 @@ struct Group {
   unsigned mask = W == 32 ? 0xffffffffu : ((1u << (W & 31)) - 1u) << (threadIdx.x & 31 & ~(W - 1));
 };
 
-constexpr int kRows = 4;  // query rows a group has in flight (of K and V rows two: their arithmetic is longer)
+constexpr int kRows = 2;  // rows a group has in flight
 
 // The rows [r0, r1) of one token: its hq queries, then its V rows, then (when
 // the page role does not take them) its K rows.
 template <typename T, int W, int kCache>
 __device__ __forceinline__ void append_token(const AppendArgs& A, int t, int r0, int r1) {
-  using V = Vec4<T>;
   const Group<W> G;
-  const bool own = 8 * G.l < A.pool.d;
+  const bool own = 16 * G.l < A.pool.d;
   Place p;
   bool bad;
   if (!place_token(A, t, p, bad)) {
@@ -340,36 +363,41 @@ __device__ __forceinline__ void append_token(const AppendArgs& A, int t, int r0,
   __nv_bfloat16* qo = A.q_out + t * A.qo_ts + r0 * A.qo_hs;
 #pragma unroll 1
   for (int r = r0; r < q1; r += kRows, q += kRows * A.q_hs, qo += kRows * A.qo_hs) {
-    typename V::Raw u[kRows], v[kRows];
+    Chunk<T> u[kRows], v[kRows];
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
       if (own && r + k < q1) {
-        u[k] = V::load(q + k * A.q_hs + a);
-        v[k] = V::load(q + k * A.q_hs + b);
+        u[k].load(q + k * A.q_hs + a);
+        v[k].load(q + k * A.q_hs + b);
       }
     }
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
       if (own && r + k < q1) {
-        float2 x[4];
-        widen8<T>(u[k], v[k], x);
-        rotate8(A, ang, x);
-        store8_bf16(qo + k * A.qo_hs, a, b, x);
+        float2 x[8];
+        u[k].widen(x);
+        v[k].widen(x + 4);
+        rotate16(A, ang, x);
+        store16_bf16(qo + k * A.qo_hs, a, b, x);
       }
     }
   }
   // heads [g0, g1) of V or K
   auto cached = [&](auto rotated, const void* rows, int64_t ts, int64_t hs, void* pool, float* scales, int g0, int g1) {
     constexpr bool kRotated = decltype(rotated)::value;
-    const int ra = kRotated ? a : 8 * G.l, rb = kRotated ? b : 8 * G.l + 4;
+    const int ra = kRotated ? a : 16 * G.l, rb = kRotated ? b : 16 * G.l + 8;
     const T* src = static_cast<const T*>(rows) + t * ts + g0 * hs;
     Sink<kCache> to(pool, scales, p.row0 + static_cast<int64_t>(g0) * A.pool.page_size, A.pool.d);
 #pragma unroll 2
     for (int g = g0; g < g1; ++g, src += hs) {
-      float2 x[4];
+      float2 x[8];
       if (own) {
-        widen8<T>(V::load(src + ra), V::load(src + rb), x);
-        if constexpr (kRotated) rotate8(A, ang, x);
+        Chunk<T> u, v;
+        u.load(src + ra);
+        v.load(src + rb);
+        u.widen(x);
+        v.widen(x + 4);
+        if constexpr (kRotated) rotate16(A, ang, x);
       }
       store_row<W, kCache>(to, G.l, own, ra, rb, x, G.mask);
       to.advance(A.pool.page_size, A.pool.d);
@@ -379,18 +407,14 @@ __device__ __forceinline__ void append_token(const AppendArgs& A, int t, int r0,
   cached(std::true_type{}, A.k_new, A.k_ts, A.k_hs, A.k_cache, A.k_scales, max(r0 - hq - hkv, 0), r1 - hq - hkv);
 }
 
-__device__ __forceinline__ float2 min_of(float2 a, float2 b) { return make_float2(fminf(a.x, b.x), fminf(a.y, b.y)); }
-__device__ __forceinline__ float2 max_of(float2 a, float2 b) { return make_float2(fmaxf(a.x, b.x), fmaxf(a.y, b.y)); }
-
 // The new keys of the pages whose first new token is one of `window` tokens
 // from t0 on, and those pages' bounds; the whole CTA together.
 template <typename T, int W, int kCache>
-__device__ __forceinline__ void append_pages(const AppendArgs& A, int t0, float2 (&s_lo)[4][kThreads],
-                                             float2 (&s_hi)[4][kThreads]) {
-  using V = Vec4<T>;
+__device__ __forceinline__ void append_pages(const AppendArgs& A, int t0, uint32_t (&s_lo)[8][kThreads],
+                                             uint32_t (&s_hi)[8][kThreads]) {
   constexpr int kGroups = kThreads / W;
   const Group<W> G;
-  const bool own = 8 * G.l < A.pool.d;
+  const bool own = 16 * G.l < A.pool.d;
   const int lane = threadIdx.x & 31, group = threadIdx.x / W;
   const int page = A.pool.page_size, hkv = A.pool.hkv;
   // lane j of every warp looks at token t0 + j
@@ -421,25 +445,31 @@ __device__ __forceinline__ void append_pages(const AppendArgs& A, int t0, float2
 #pragma unroll 1
     for (int g0 = 0; g0 < hkv; g0 += kGroups) {
       const int g = g0 + (slices > 1 ? group % hkv : group), slice = slices > 1 ? group / hkv : 0;
-      float2 lo[4], hi[4];
+      // in bf16 pairs: rounding keeps the order, so the rounded bounds are the bounds of the rounded keys
+      uint32_t lo[8], hi[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        lo[e] = make_float2(INFINITY, INFINITY);
-        hi[e] = make_float2(-INFINITY, -INFINITY);
+      for (int e = 0; e < 8; ++e) {
+        lo[e] = 0x7f807f80u;  // +inf
+        hi[e] = 0xff80ff80u;  // -inf
       }
       if (g < hkv && slice < slices) {
         const T* src = static_cast<const T*>(A.k_new) + static_cast<int64_t>(t + slice) * A.k_ts + g * A.k_hs;
         Sink<kCache> to(A.k_cache, A.k_scales, row0 + slice + static_cast<int64_t>(g) * page, A.pool.d);
 #pragma unroll 2
         for (int j = slice; j < n; j += slices, src += slices * A.k_ts) {
-          float2 x[4];
+          float2 x[8];
           if (own) {
-            widen8<T>(V::load(src + ca), V::load(src + cb), x);
-            rotate8(A, angles_of(A, G.l, slot + j), x);
+            Chunk<T> u, v;
+            u.load(src + ca);
+            v.load(src + cb);
+            u.widen(x);
+            v.widen(x + 4);
+            rotate16(A, angles_of(A, G.l, slot + j), x);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              lo[e] = min_of(lo[e], x[e]);
-              hi[e] = max_of(hi[e], x[e]);
+            for (int e = 0; e < 8; ++e) {
+              const uint32_t k = bf16x2(x[e].x, x[e].y);
+              lo[e] = bf16x2_min(lo[e], k);
+              hi[e] = bf16x2_max(hi[e], k);
             }
           }
           store_row<W, kCache>(to, G.l, own, ca, cb, x, G.mask);
@@ -449,7 +479,7 @@ __device__ __forceinline__ void append_pages(const AppendArgs& A, int t0, float2
       if (slices > 1) {
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 8; ++e) {
           s_lo[e][threadIdx.x] = lo[e];
           s_hi[e][threadIdx.x] = hi[e];
         }
@@ -458,36 +488,45 @@ __device__ __forceinline__ void append_pages(const AppendArgs& A, int t0, float2
 #pragma unroll 1
           for (int o = 1; o < slices; ++o) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              lo[e] = min_of(lo[e], s_lo[e][threadIdx.x + o * hkv * W]);
-              hi[e] = max_of(hi[e], s_hi[e][threadIdx.x + o * hkv * W]);
+            for (int e = 0; e < 8; ++e) {
+              lo[e] = bf16x2_min(lo[e], s_lo[e][threadIdx.x + o * hkv * W]);
+              hi[e] = bf16x2_max(hi[e], s_hi[e][threadIdx.x + o * hkv * W]);
             }
           }
         }
       }
       if (g < hkv && slice == 0 && own) {
         const int64_t plane = row0 / page + g;  // page * hkv + g
-        __nv_bfloat16* dst = A.bounds + plane * 2 * A.pool.d;
+        uint4* row[4];  // the low row's two chunks, the high row's
+        row[0] = reinterpret_cast<uint4*>(A.bounds + plane * 2 * A.pool.d + ca);
+        row[1] = reinterpret_cast<uint4*>(A.bounds + plane * 2 * A.pool.d + cb);
+        row[2] = reinterpret_cast<uint4*>(A.bounds + (plane * 2 + 1) * A.pool.d + ca);
+        row[3] = reinterpret_cast<uint4*>(A.bounds + (plane * 2 + 1) * A.pool.d + cb);
         if (at > 0) {
-          float2 x[4];
-          widen8<__nv_bfloat16>(*reinterpret_cast<const uint2*>(dst + ca), *reinterpret_cast<const uint2*>(dst + cb), x);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) lo[e] = min_of(lo[e], x[e]);
-          widen8<__nv_bfloat16>(*reinterpret_cast<const uint2*>(dst + A.pool.d + ca),
-                                *reinterpret_cast<const uint2*>(dst + A.pool.d + cb), x);
+          for (int c = 0; c < 2; ++c) {
+            const uint4 u = *row[c], v = *row[2 + c];
+            const uint32_t ul[4] = {u.x, u.y, u.z, u.w}, vl[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) hi[e] = max_of(hi[e], x[e]);
+            for (int e = 0; e < 4; ++e) {
+              lo[4 * c + e] = bf16x2_min(lo[4 * c + e], ul[e]);
+              hi[4 * c + e] = bf16x2_max(hi[4 * c + e], vl[e]);
+            }
+          }
         }
-        store8_bf16(dst, ca, cb, lo);
-        store8_bf16(dst + A.pool.d, ca, cb, hi);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          *row[c] = make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+          *row[2 + c] = make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
+        }
       }
     }
   }
 }
 
 template <typename T, int W, int kCache>
-__global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendArgs A) {
-  __shared__ float2 s_lo[4][kThreads], s_hi[4][kThreads];
+__global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendArgs A) {
+  __shared__ uint32_t s_lo[8][kThreads], s_hi[8][kThreads];
   // grid row 0 is the page role (where bounds are kept), the others are the parts of the tokens' rows
   int part = static_cast<int>(blockIdx.y);
   if (A.bounds != nullptr) {
@@ -531,8 +570,8 @@ struct ReadArgs {
   Watchdog wd;
 };
 
-// A group of W lanes takes one token and `part_rows` of its 2 hkv rows (one
-// part per grid row).
+// A group of W lanes (d / 8 rounded up to a power of two, eight channels a
+// lane) takes one token and `part_rows` of its 2 hkv rows (one part per grid row).
 template <int W, int kCache>
 __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs A) {
   const Group<W> G;
@@ -558,8 +597,9 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs A) {
     const float* scales = is_v ? A.v_scales : A.k_scales;
     float2 x[4];
     if constexpr (kCache == FA_BF16) {
-      const uint4 w = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(pool) + row * d + 8 * G.l));
-      widen8<__nv_bfloat16>(make_uint2(w.x, w.y), make_uint2(w.z, w.w), x);
+      Chunk<__nv_bfloat16> u;
+      u.load(static_cast<const __nv_bfloat16*>(pool) + row * d + 8 * G.l);
+      u.widen(x);
     } else if constexpr (kCache == FA_I8) {
       const uint2 w = __ldcs(reinterpret_cast<const uint2*>(static_cast<const int8_t*>(pool) + row * d + 8 * G.l));
       const float s = scales[row];
@@ -589,9 +629,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs A) {
       __stcs(reinterpret_cast<float4*>(dst), make_float4(x[0].x, x[0].y, x[1].x, x[1].y));
       __stcs(reinterpret_cast<float4*>(dst + 4), make_float4(x[2].x, x[2].y, x[3].x, x[3].y));
     } else {
-      const uint2 u = pack4(x[0], x[1]), v = pack4(x[2], x[3]);
-      __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_v ? A.v_out : A.k_out) + at),
-             make_uint4(u.x, u.y, v.x, v.y));
+      __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_v ? A.v_out : A.k_out) + at), pack8(x));
     }
   }
 }
@@ -612,7 +650,7 @@ PoolArgs pool_args(const fa_kv_pages& pg, int hkv, int d) {
 // device several times over (the lookups of a token are then spread over more rows).
 int rows_per_item(int64_t total, int rows, int groups) {
   const int64_t enough = static_cast<int64_t>(device_sm_count()) * 8 * groups;
-  int per = kRows;
+  int per = 4;
   while (per < rows && total * ((rows + per - 1) / per) > enough) per *= 2;
   return per;
 }
@@ -640,11 +678,11 @@ fa_status launch_append_width(AppendArgs& A, const LaunchCtx& ctx) {
 }
 template <typename T>
 fa_status launch_append(AppendArgs& A, const LaunchCtx& ctx) {
-  if (A.pool.d <= 16) return launch_append_width<T, 2>(A, ctx);
-  if (A.pool.d <= 32) return launch_append_width<T, 4>(A, ctx);
-  if (A.pool.d <= 64) return launch_append_width<T, 8>(A, ctx);
-  if (A.pool.d <= 128) return launch_append_width<T, 16>(A, ctx);
-  return launch_append_width<T, 32>(A, ctx);
+  if (A.pool.d <= 16) return launch_append_width<T, 1>(A, ctx);
+  if (A.pool.d <= 32) return launch_append_width<T, 2>(A, ctx);
+  if (A.pool.d <= 64) return launch_append_width<T, 4>(A, ctx);
+  if (A.pool.d <= 128) return launch_append_width<T, 8>(A, ctx);
+  return launch_append_width<T, 16>(A, ctx);
 }
 
 template <int W, int kCache>
