@@ -8,6 +8,7 @@ when it is missing -- there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional, Sequence, Tuple
@@ -622,20 +623,28 @@ def _append_params(k_new, v_new, k_cache, v_cache, cur_pos, hkv, k_scales, v_sca
 
 
 # --- rotated append, page selection and attention over page pools -----------------
+#
+# A decode step makes a few of these calls per layer, so their checks are
+# written for their cost: each call tests all of its tensors in one expression
+# and looks for the one at fault (_refuse) only when the expression fails.
 
 _CACHE_DT = {torch.bfloat16: FA_BF16, torch.int8: FA_I8, torch.uint8: FA_I4}
+_BF16, _F32, _INT32 = torch.bfloat16, torch.float32, torch.int32
+_NO_EPILOGUE = (EpiOp * FA_MAX_EPILOGUE)()
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _on_device(dev: int, stream, what: str, fn, *args) -> None:
-    """Call fn(*args, stream) with CUDA device `dev` current: on `stream`, or on dev's current stream."""
+    """Call fn(*args, stream) with CUDA device `dev` current: on `stream`, or
+    on dev's current stream (torch.cuda.current_stream(dev), without the
+    object that costs more than the rest of the call)."""
     if stream is None:
-        # what torch.cuda.current_stream(dev).cuda_stream is, at a twentieth of its cost
-        raw = torch._C._cuda_getCurrentRawStream(dev)
+        raw = _raw_stream(dev)
     else:
         if stream.device.index != dev:
             raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
         raw = stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         status = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -653,53 +662,76 @@ def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
         return like.new_empty(shape, dtype=dtype)
 
 
+@functools.lru_cache(maxsize=256)
+def _decode_workspace_bytes(dev: int, batch: int, hq: int, capacity: int, head_dim: int) -> int:
+    with torch.cuda.device(dev):  # its count of SMs enters the size
+        return max(16, lib.fa_decode_workspace_size(batch, hq, capacity, head_dim))
+
+
+@functools.lru_cache(maxsize=256)
+def _select_workspace_bytes(batch: int, hkv: int, max_pages: int) -> int:
+    return max(16, lib.fa_page_select_workspace_size(batch, hkv, max_pages))
+
+
+def _refuse(dev: int, *operands) -> None:
+    """ValueError for the first operand (tensor, name, dtype, shape) that is not a
+    contiguous tensor of that dtype and shape on CUDA device dev."""
+    for t, name, dtype, shape in operands:
+        if t is None:
+            continue
+        if t.get_device() != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous tensor on cuda:{dev}")
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+
+
 def _operand(t, name: str, dev: int, dtype, shape) -> int:
-    """The address of a contiguous tensor on CUDA device dev with this dtype and shape."""
-    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
-    if t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor on cuda:{dev}")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-
-
-def _optional(t, name: str, dev: int, dtype, shape) -> int:
-    return 0 if t is None else _operand(t, name, dev, dtype, shape)
+    """The address of a contiguous tensor on CUDA device dev with this dtype and shape (0 for None)."""
+    if t is None:
+        return 0
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
+        _refuse(dev, (t, name, dtype, shape))
+    return t.data_ptr()
 
 
 def _pool_operands(k_pages, v_pages, k_scales, v_scales, block_table, batch: int, hkv: int, d: int, dev: int):
     """(cache dtype, KvPages, pool and scale addresses) of page pools; ValueError where they do not fit together."""
-    dtype = k_pages.dtype
+    dtype, shape, table_shape = k_pages.dtype, k_pages.shape, block_table.shape
     kind = _CACHE_DT.get(dtype)
     if kind is None:
         raise ValueError(f"a page pool is bfloat16, int8 or uint8 (4-bit codes), not {dtype}")
-    if len(k_pages.shape) != 4 or len(block_table.shape) != 2:
-        raise ValueError(f"a page pool has 4 dimensions and a block table 2; got {tuple(k_pages.shape)} and "
-                         f"{tuple(block_table.shape)}")
-    num_pages, _, page_size, _ = k_pages.shape
-    pool = (num_pages, hkv, page_size, d // 2 if kind == FA_I4 else d)
-    kp = _operand(k_pages, "k_pages", dev, dtype, pool)
-    vp = _operand(v_pages, "v_pages", dev, dtype, pool)
+    if len(shape) != 4 or len(table_shape) != 2:
+        raise ValueError(f"a page pool has 4 dimensions and a block table 2; got {tuple(shape)} and {tuple(table_shape)}")
+    num_pages, heads, page_size, width = shape
+    want = d >> 1 if kind == FA_I4 else d
+    if not (heads == hkv and width == want and table_shape[0] == batch and v_pages.dtype is dtype
+            and v_pages.shape == shape and block_table.dtype is _INT32 and k_pages.get_device() == dev
+            and v_pages.get_device() == dev and block_table.get_device() == dev and k_pages.is_contiguous()
+            and v_pages.is_contiguous() and block_table.is_contiguous()):
+        pool = (num_pages, hkv, page_size, want)
+        _refuse(dev, (k_pages, "k_pages", dtype, pool), (v_pages, "v_pages", dtype, pool),
+                (block_table, "block_table", _INT32, (batch, table_shape[1])))
+    pages = KvPages(block_table.data_ptr(), table_shape[1], page_size, num_pages)
     if kind == FA_BF16:
         if k_scales is not None or v_scales is not None:
             raise ValueError("a bfloat16 cache has no scales")
-        ks = vs = 0
-    else:
-        if k_scales is None or v_scales is None:
-            raise ValueError("k_scales and v_scales are required with a quantised cache")
-        rows = (num_pages, hkv, page_size, 2) if kind == FA_I4 else (num_pages, hkv, page_size)
-        ks = _operand(k_scales, "k_scales", dev, torch.float32, rows)
-        vs = _operand(v_scales, "v_scales", dev, torch.float32, rows)
-    max_pages = block_table.shape[1]
-    table = _operand(block_table, "block_table", dev, torch.int32, (batch, max_pages))
-    return kind, KvPages(table, max_pages, page_size, num_pages), kp, vp, ks, vs
+        return kind, pages, k_pages.data_ptr(), v_pages.data_ptr(), 0, 0
+    if k_scales is None or v_scales is None:
+        raise ValueError("k_scales and v_scales are required with a quantised cache")
+    rows = (num_pages, hkv, page_size, 2) if kind == FA_I4 else (num_pages, hkv, page_size)
+    if not (k_scales.dtype is _F32 and v_scales.dtype is _F32 and k_scales.shape == rows and v_scales.shape == rows
+            and k_scales.get_device() == dev and v_scales.get_device() == dev and k_scales.is_contiguous()
+            and v_scales.is_contiguous()):
+        _refuse(dev, (k_scales, "k_scales", _F32, rows), (v_scales, "v_scales", _F32, rows))
+    return kind, pages, k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr()
 
 
 def _int(x, name: str, lo: int = 0) -> int:
     """x as an int of the C ABI's 32 bits, at least lo."""
     x = int(x)
-    if not lo <= x < 2 ** 31:
+    if not lo <= x < 2147483648:
         raise ValueError(f"{name} = {x} is out of range")
     return x
 
@@ -713,8 +745,8 @@ def _cuda_device(t, name: str) -> int:
 
 def _rows_operand(t, name: str, dev: int, dtype, shape):
     """(address, token stride, head stride) of rows [tokens, heads, d] whose last dimension is contiguous."""
-    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
-        raise ValueError(f"{name} must be {dtype} {shape} on cuda:{dev}; got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev):
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on cuda:{dev}; got {t.dtype} {tuple(t.shape)} on {t.device}")
     tokens, heads, channels = t.stride()
     if channels != 1 and shape[2] > 1:
         raise ValueError(f"{name}: the channels of a row must be contiguous")
@@ -750,46 +782,52 @@ def kv_append_rope_paged(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torc
     take: [B*hq, d] without cu_seqlens, else [hq, total, d] (`q_out` of that
     shape if given), or None without q.  As fa_kv_append_rope_paged in fa.h."""
     dev = _cuda_device(k_pages, "k_pages")
-    if len(k_new.shape) != 3 or len(cur_pos.shape) != 1:
-        raise ValueError(f"k_new must be [total, hkv, d] and cur_pos [batch]; got {tuple(k_new.shape)} and "
-                         f"{tuple(cur_pos.shape)}")
-    total, hkv, d = k_new.shape
-    batch = cur_pos.shape[0]
+    rows, pos_shape = k_new.shape, cur_pos.shape
+    if len(rows) != 3 or len(pos_shape) != 1:
+        raise ValueError(f"k_new must be [total, hkv, d] and cur_pos [batch]; got {tuple(rows)} and {tuple(pos_shape)}")
+    total, hkv, d = rows
+    batch = pos_shape[0]
     xt = k_new.dtype
-    if xt != torch.bfloat16 and xt != torch.float32:
+    if xt is not _BF16 and xt is not _F32:
         raise ValueError(f"k_new must be bfloat16 or float32, not {xt}")
     if cu_seqlens is None and total != batch:
         raise ValueError(f"without cu_seqlens there is one token per sequence: {total} tokens, {batch} sequences")
-    kn, kts, khs = _rows_operand(k_new, "k_new", dev, xt, (total, hkv, d))
-    vn, vts, vhs = _rows_operand(v_new, "v_new", dev, xt, (total, hkv, d))
+    kn, kts, khs = _rows_operand(k_new, "k_new", dev, xt, rows)
+    vn, vts, vhs = _rows_operand(v_new, "v_new", dev, xt, rows)
     kind, pg, kp, vp, ks, vs = _pool_operands(k_pages, v_pages, k_scales, v_scales, block_table, batch, hkv, d, dev)
-    bounds = _optional(key_bounds, "key_bounds", dev, torch.bfloat16, (pg.num_pages, hkv, 2, d))
-    pos = _operand(cur_pos, "cur_pos", dev, torch.int32, (batch,))
-    cu = _optional(cu_seqlens, "cu_seqlens", dev, torch.int32, (batch + 1,))
-    lens = _optional(cache_seqlens, "cache_seqlens", dev, torch.int32, (batch,))
-    table, rows, rot = 0, 0, 0
+    bounds = _operand(key_bounds, "key_bounds", dev, _BF16, (pg.num_pages, hkv, 2, d))
+    pos = _operand(cur_pos, "cur_pos", dev, _INT32, pos_shape)
+    cu = _operand(cu_seqlens, "cu_seqlens", dev, _INT32, (batch + 1,))
+    lens = _operand(cache_seqlens, "cache_seqlens", dev, _INT32, pos_shape)
+    table = table_rows = rot = 0
     if rope_table is not None:
-        if len(rope_table.shape) != 2:
-            raise ValueError(f"rope_table has shape {tuple(rope_table.shape)}, expected 2 dimensions")
-        rows, rot = rope_table.shape
-        table = _operand(rope_table, "rope_table", dev, torch.float32, (rows, rot))
+        shape = rope_table.shape
+        if len(shape) != 2:
+            raise ValueError(f"rope_table has shape {tuple(shape)}, expected 2 dimensions")
+        table_rows, rot = shape
+        table = _operand(rope_table, "rope_table", dev, _F32, shape)
     qp = qo = qts = qhs = ots = ohs = hq = 0
     if q is None:
         if q_out is not None:
             raise ValueError("q_out without q")
     else:
-        if len(q.shape) != 3:
-            raise ValueError(f"q must be [total, hq, d]; got {tuple(q.shape)}")
-        hq = q.shape[1]
-        qp, qts, qhs = _rows_operand(q, "q", dev, xt, (total, hq, d))
-        shape = (total * hq, d) if cu_seqlens is None else (hq, total, d)
+        shape = q.shape
+        if len(shape) != 3 or shape[0] != total or shape[2] != d:
+            raise ValueError(f"q must be [{total}, hq, {d}]; got {tuple(shape)}")
+        hq = shape[1]
+        qp, qts, qhs = _rows_operand(q, "q", dev, xt, shape)
+        if cu_seqlens is None:
+            out_shape, ots, ohs = (total * hq, d), hq * d, d
+        else:
+            out_shape, ots, ohs = (hq, total, d), d, total * d
         if q_out is None:
-            q_out = _new(q, shape, torch.bfloat16, stream)
-        qo = _operand(q_out, "q_out", dev, torch.bfloat16, shape)
-        ots, ohs = (hq * d, d) if cu_seqlens is None else (d, total * d)
+            q_out = _new(q, out_shape, _BF16, stream)
+            qo = q_out.data_ptr()
+        else:
+            qo = _operand(q_out, "q_out", dev, _BF16, out_shape)
     p = KvAppendRopeParams(kn, vn, qp, qo, kts, khs, vts, vhs, qts, qhs, ots, ohs, table, kp, vp, ks, vs, bounds, cu, pos,
-                           lens, FA_BF16 if xt == torch.bfloat16 else FA_F32, kind, batch, total, hq, hkv, d, rot,
-                           1 if interleaved else 0, rows)
+                           lens, FA_BF16 if xt is _BF16 else FA_F32, kind, batch, total, hq, hkv, d, rot,
+                           1 if interleaved else 0, table_rows)
     _on_device(dev, stream, "fa_kv_append_rope_paged", lib.fa_kv_append_rope_paged, p, pg)
     return q_out
 
@@ -805,9 +843,9 @@ def kv_read_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, cu_seqlens: torc
     if len(cu_seqlens.shape) != 1 or cu_seqlens.shape[0] < 1 or len(k_pages.shape) != 4:
         raise ValueError("cu_seqlens must be [batch + 1] and k_pages [num_pages, hkv, page_size, d]")
     batch, hkv = cu_seqlens.shape[0] - 1, k_pages.shape[1]
-    d = k_pages.shape[3] * (2 if k_pages.dtype == torch.uint8 else 1)
+    d = k_pages.shape[3] * (2 if k_pages.dtype is torch.uint8 else 1)
     kind, pg, kp, vp, ks, vs = _pool_operands(k_pages, v_pages, k_scales, v_scales, block_table, batch, hkv, d, dev)
-    if out_dtype != torch.bfloat16 and out_dtype != torch.float32:
+    if out_dtype is not _BF16 and out_dtype is not _F32:
         raise ValueError(f"out_dtype must be bfloat16 or float32, not {out_dtype}")
     shape = (hkv, _int(total, "total"), d)
     if k_out is None:
@@ -816,25 +854,33 @@ def kv_read_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, cu_seqlens: torc
         v_out = _new(k_pages, shape, out_dtype, stream)
     p = KvReadParams(kp, vp, ks, vs, _operand(k_out, "k_out", dev, out_dtype, shape),
                      _operand(v_out, "v_out", dev, out_dtype, shape),
-                     _operand(cu_seqlens, "cu_seqlens", dev, torch.int32, (batch + 1,)),
-                     _optional(start, "start", dev, torch.int32, (batch,)), kind,
-                     FA_BF16 if out_dtype == torch.bfloat16 else FA_F32, batch, shape[1], hkv, d)
+                     _operand(cu_seqlens, "cu_seqlens", dev, _INT32, (batch + 1,)),
+                     _operand(start, "start", dev, _INT32, (batch,)), kind,
+                     FA_BF16 if out_dtype is _BF16 else FA_F32, batch, shape[1], hkv, d)
     _on_device(dev, stream, "fa_kv_read_paged", lib.fa_kv_read_paged, p, pg)
     return k_out, v_out
 
 
-def _decode_queries(q, cache_seqlens, hq: int, hkv: int, dev):
+def _decode_queries(q, cache_seqlens, hq: int, hkv: int, dev: int):
     """(batch, d, address of q, address of cache_seqlens) of a decode step's operands."""
     if hq < 1 or hkv < 1 or hq % hkv:
         raise ValueError(f"hq = {hq} must be a positive multiple of hkv = {hkv}")
-    if len(cache_seqlens.shape) != 1:
-        raise ValueError(f"cache_seqlens has shape {tuple(cache_seqlens.shape)}, expected 1 dimension")
-    shape = q.shape
-    batch, d = cache_seqlens.shape[0], shape[-1]
+    shape, lens_shape = q.shape, cache_seqlens.shape
+    if len(lens_shape) != 1:
+        raise ValueError(f"cache_seqlens has shape {tuple(lens_shape)}, expected 1 dimension")
+    batch, d = lens_shape[0], shape[-1]
     if shape != (batch * hq, d) and shape != (batch * hq, 1, d):
         raise ValueError(f"q has shape {tuple(shape)}, expected batch*hq = {batch * hq} rows")
-    return (batch, d, _operand(q, "q", dev, torch.bfloat16, shape),
-            _operand(cache_seqlens, "cache_seqlens", dev, torch.int32, (batch,)))
+    if not (q.dtype is _BF16 and cache_seqlens.dtype is _INT32 and cache_seqlens.get_device() == dev
+            and q.is_contiguous() and cache_seqlens.is_contiguous()):
+        _refuse(dev, (q, "q", _BF16, shape), (cache_seqlens, "cache_seqlens", _INT32, lens_shape))
+    return batch, d, q.data_ptr(), cache_seqlens.data_ptr()
+
+
+def _workspace(t, dev: int) -> int:
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    return t.data_ptr()
 
 
 def page_select(q: torch.Tensor, key_bounds: torch.Tensor, cache_seqlens: torch.Tensor, block_table: torch.Tensor, *,
@@ -848,30 +894,30 @@ def page_select(q: torch.Tensor, key_bounds: torch.Tensor, cache_seqlens: torch.
     in fa.h."""
     dev = _cuda_device(q, "q")
     batch, d, qp, lens = _decode_queries(q, cache_seqlens, hq, hkv, dev)
-    if len(key_bounds.shape) != 4 or len(block_table.shape) != 2:
+    bounds_shape, table_shape = key_bounds.shape, block_table.shape
+    if len(bounds_shape) != 4 or len(table_shape) != 2:
         raise ValueError("key_bounds must be [num_pages, hkv, 2, d] and block_table [batch, max_pages]")
-    num_pages, max_pages = key_bounds.shape[0], block_table.shape[1]
-    bounds = _operand(key_bounds, "key_bounds", dev, torch.bfloat16, (num_pages, hkv, 2, d))
-    pg = KvPages(_operand(block_table, "block_table", dev, torch.int32, (batch, max_pages)), max_pages,
-                 _int(page_size, "page_size", 1), num_pages)
+    num_pages, max_pages = bounds_shape[0], table_shape[1]
+    bounds = _operand(key_bounds, "key_bounds", dev, _BF16, (num_pages, hkv, 2, d))
+    table = _operand(block_table, "block_table", dev, _INT32, (batch, max_pages))
     top_k = _int(top_k, "top_k", 1)
     shape = (batch, hkv, top_k)
     if out is None:
-        out = _new(q, shape, torch.int32, stream)
+        out = _new(q, shape, _INT32, stream)
+        selected = out.data_ptr()
+    else:
+        selected = _operand(out, "out", dev, _INT32, shape)
     if workspace is None:
-        nbytes = lib.fa_page_select_workspace_size(batch, hkv, max_pages)
-        workspace = _new(q, (max(nbytes, 16),), torch.uint8, stream)
-    p = PageSelectParams(qp, bounds, lens, _operand(out, "out", dev, torch.int32, shape), batch, hq, hkv, d, top_k,
-                         _int(n_first, "n_first"), _int(n_recent, "n_recent"), _workspace(workspace, dev),
-                         workspace.numel() * workspace.element_size())
-    _on_device(dev, stream, "fa_page_select", lib.fa_page_select, p, pg)
+        nbytes = _select_workspace_bytes(batch, hkv, max_pages)
+        workspace = _new(q, nbytes, torch.uint8, stream)
+        ws = workspace.data_ptr()
+    else:
+        nbytes, ws = workspace.numel() * workspace.element_size(), _workspace(workspace, dev)
+    p = PageSelectParams(qp, bounds, lens, selected, batch, hq, hkv, d, top_k, _int(n_first, "n_first"),
+                         _int(n_recent, "n_recent"), ws, nbytes)
+    _on_device(dev, stream, "fa_page_select", lib.fa_page_select, p,
+               KvPages(table, max_pages, _int(page_size, "page_size", 1), num_pages))
     return out
-
-
-def _workspace(t, dev: int) -> int:
-    if t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
-    return t.data_ptr()
 
 
 def attention_decode_selected(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -893,24 +939,29 @@ def _decode_pages(q, k_pages, v_pages, cache_seqlens, block_table, selected, hq,
     kind, pg, kp, vp, ks, vs = _pool_operands(k_pages, v_pages, k_scales, v_scales, block_table, batch, hkv, d, dev)
     capacity = pg.max_pages * pg.page_size
     if out is None:
-        out = _new(q, q.shape, torch.bfloat16, stream)
+        out = torch.empty_like(q) if stream is None else _new(q, q.shape, _BF16, stream)
+        op = out.data_ptr()
+    else:
+        op = _operand(out, "out", dev, _BF16, q.shape)
     if workspace is None:
-        nbytes = lib.fa_decode_workspace_size(batch, hq, capacity, d)
-        workspace = _new(q, (max(nbytes, 16),), torch.uint8, stream)
-    p = DecodeParams(qp, kp, vp, ks, vs, lens, _operand(out, "out", dev, torch.bfloat16, q.shape), kind, batch, hq,
-                     hkv, d, capacity, _int(max_seqlen, "max_seqlen"), _int(max(0, window), "window"),
-                     1.0 / math.sqrt(d) if scale is None else float(scale), 0)
-    p.workspace, p.workspace_bytes = _workspace(workspace, dev), workspace.numel() * workspace.element_size()
+        nbytes = _decode_workspace_bytes(dev, batch, hq, capacity, d)
+        workspace = _new(q, nbytes, torch.uint8, stream)
+        ws = workspace.data_ptr()
+    else:
+        nbytes, ws = workspace.numel() * workspace.element_size(), _workspace(workspace, dev)
+    p = DecodeParams(qp, kp, vp, ks, vs, lens, op, kind, batch, hq, hkv, d, capacity, _int(max_seqlen, "max_seqlen"),
+                     _int(window, "window") if window > 0 else 0, 1.0 / math.sqrt(d) if scale is None else float(scale),
+                     0, 0, _NO_EPILOGUE, ws, nbytes)
     if epilogue:
         p.n_epilogue = _fill_epilogue(p.epilogue, epilogue)
     if selected is None:
         _on_device(dev, stream, "fa_attention_decode_paged", lib.fa_attention_decode_paged, p, pg)
     else:
-        if len(selected.shape) != 3:
-            raise ValueError(f"selected must be [batch, hkv, top_k]; got {tuple(selected.shape)}")
-        top_k = selected.shape[2]
-        sel = _operand(selected, "selected", dev, torch.int32, (batch, hkv, top_k))
-        _on_device(dev, stream, "fa_attention_decode_selected", lib.fa_attention_decode_selected, p, pg, sel, top_k)
+        shape = selected.shape
+        if len(shape) != 3 or shape[0] != batch or shape[1] != hkv:
+            raise ValueError(f"selected must be [{batch}, {hkv}, top_k]; got {tuple(shape)}")
+        _on_device(dev, stream, "fa_attention_decode_selected", lib.fa_attention_decode_selected, p, pg,
+                   _operand(selected, "selected", dev, _INT32, shape), shape[2])
     return out
 
 
