@@ -146,15 +146,10 @@ struct TileInfo {
   }
 };
 
+// Tile t of segment (b, g).
 template <int kRuns, bool kSel>
-__device__ __forceinline__ TileInfo<kRuns> tile_info(const PageArgs& A, const int32_t* pre, int x) {
-  int lo = 0, hi = A.batch - 1;  // the last b with pre[b] <= x
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (pre[mid] <= x) lo = mid; else hi = mid - 1;
-  }
-  const int b = lo, Tb = A.by_hkv.div(pre[b + 1] - pre[b]), y = x - pre[b];
-  const int g = y / Tb, t = y - g * Tb, gr = A.by_split.div(g);
+__device__ __forceinline__ TileInfo<kRuns> tile_at(const PageArgs& A, int b, int g, int t) {
+  const int gr = A.by_split.div(g);
   const int L = length_of(A, b), n_pages = pages_in(A, L);
   TileInfo<kRuns> info;
   info.seg = b * A.hkv + g;
@@ -184,6 +179,17 @@ __device__ __forceinline__ TileInfo<kRuns> tile_info(const PageArgs& A, const in
   }
   return info;
 }
+// Tile x of all segments' tiles, by their prefix over the sequences.
+template <int kRuns, bool kSel>
+__device__ __forceinline__ TileInfo<kRuns> tile_info(const PageArgs& A, const int32_t* pre, int x) {
+  int lo = 0, hi = A.batch - 1;  // the last b with pre[b] <= x
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  const int Tb = A.by_hkv.div(pre[lo + 1] - pre[lo]), y = x - pre[lo], g = y / Tb;
+  return tile_at<kRuns, kSel>(A, lo, g, y - g * Tb);
+}
 
 // S row r of a 16-key half is key key_of(r) of it: for packed rows of 64 bytes
 // the K loads of rows (2i, 2i + 1) then fall on different banks, and so do half
@@ -193,7 +199,10 @@ __device__ __forceinline__ int key_of(int r) {
   return kKind == FA_I4 ? r ^ ((r >> 1) & 1) : r;
 }
 
-template <int D, int kKind, bool kSel>
+// kCluster: the CTAs of a cluster serve one segment, its tiles dealt evenly to
+// their warps, and merge their states through distributed shared memory.
+// Else: the tiles of all segments are dealt evenly to all warps.
+template <int D, int kKind, bool kSel, bool kCluster>
 __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
     decode_pages_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ CUtensorMap tm_k32, const __grid_constant__ CUtensorMap tm_v32,
@@ -211,8 +220,9 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
   uint64_t* all_bars = reinterpret_cast<uint64_t*>(smem + TL::kRing);
   int32_t* pre = reinterpret_cast<int32_t*>(all_bars + kWarps * kStages);
   __shared__ int32_t warp_sums[kWarps];
+  __shared__ float2 s_ml[kWarps][8];  // cluster: each warp's (m, l) per head
 
-  griddep_launch_dependents();
+  if constexpr (!kCluster) griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gq = lane >> 2, qq = lane & 3;
   uint64_t* bars = all_bars + warp * kStages;
@@ -220,50 +230,70 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
     for (int s = 0; s < kStages; ++s) mbar_init(&bars[s], 1);
     fence_barrier_init();
   }
-  // tile prefix over the sequences
-  {
-    const int per = (A.batch + kThreads - 1) / kThreads;
-    const int b0 = min(A.batch, static_cast<int>(threadIdx.x) * per), b1 = min(A.batch, b0 + per);
-    int own = 0;
-    for (int b = b0; b < b1; ++b) {
-      const int L = A.seqlens[b];
-      if ((L < 0 || L > A.capacity) && blockIdx.x == 0) record_status(A.wd, kStatusRange);
-      own += tiles_in<TL::kKeys, kSel>(A, length_of(A, b)) * A.hkv;
-    }
-    int incl = own;
+  // this warp's tiles: [t_first, t_first + my_tiles) of all, or of the cluster's segment
+  int w = 0, T = 0, P = 1, t_first, my_tiles, the_seg = 0, the_b = 0, the_g = 0;
+  if constexpr (kCluster) {
+    const int c = static_cast<int>(cluster_size());
+    the_seg = static_cast<int>(blockIdx.x) / c;
+    the_b = A.by_hkv.div(the_seg);
+    the_g = the_seg - the_b * A.hkv;
+    const int L = A.seqlens[the_b];
+    if ((L < 0 || L > A.capacity) && threadIdx.x == 0) record_status(A.wd, kStatusRange);
+    const int64_t Tb = tiles_in<TL::kKeys, kSel>(A, length_of(A, the_b));
+    const int workers = c * kWarps, v = static_cast<int>(cluster_ctarank()) * kWarps + warp;
+    t_first = static_cast<int>(Tb * v / workers);
+    my_tiles = static_cast<int>(Tb * (v + 1) / workers) - t_first;
+    if (lane < 8) s_ml[warp][lane] = make_float2(-INFINITY, 0.f);
+    __syncwarp();
+  } else {
+    // tile prefix over the sequences
+    {
+      const int per = (A.batch + kThreads - 1) / kThreads;
+      const int b0 = min(A.batch, static_cast<int>(threadIdx.x) * per), b1 = min(A.batch, b0 + per);
+      int own = 0;
+      for (int b = b0; b < b1; ++b) {
+        const int L = A.seqlens[b];
+        if ((L < 0 || L > A.capacity) && blockIdx.x == 0) record_status(A.wd, kStatusRange);
+        own += tiles_in<TL::kKeys, kSel>(A, length_of(A, b)) * A.hkv;
+      }
+      int incl = own;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += v;
+      for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += v;
+      }
+      if (lane == 31) warp_sums[warp] = incl;
+      __syncthreads();
+      int at = incl - own;
+      for (int v = 0; v < warp; ++v) at += warp_sums[v];
+      for (int b = b0; b < b1; ++b) {
+        pre[b] = at;
+        if (blockIdx.x == 0) A.prefix[b] = at;
+        at += tiles_in<TL::kKeys, kSel>(A, length_of(A, b)) * A.hkv;
+      }
+      if (threadIdx.x == 0) {
+        int total = 0;
+        for (int v = 0; v < kWarps; ++v) total += warp_sums[v];
+        pre[A.batch] = total;
+        if (blockIdx.x == 0) A.prefix[A.batch] = total;
+      }
+      __syncthreads();
     }
-    if (lane == 31) warp_sums[warp] = incl;
-    __syncthreads();
-    int at = incl - own;
-    for (int v = 0; v < warp; ++v) at += warp_sums[v];
-    for (int b = b0; b < b1; ++b) {
-      pre[b] = at;
-      if (blockIdx.x == 0) A.prefix[b] = at;
-      at += tiles_in<TL::kKeys, kSel>(A, length_of(A, b)) * A.hkv;
-    }
-    if (threadIdx.x == 0) {
-      int total = 0;
-      for (int v = 0; v < kWarps; ++v) total += warp_sums[v];
-      pre[A.batch] = total;
-      if (blockIdx.x == 0) A.prefix[A.batch] = total;
-    }
-    __syncthreads();
+    T = pre[A.batch];
+    P = min(A.n_workers, T);
+    w = static_cast<int>(blockIdx.x) * kWarps + warp;
+    if (w >= P) return;
+    const Split split(T, P);
+    t_first = split.begin(w);
+    my_tiles = split.begin(w + 1) - t_first;
   }
-  const int T = pre[A.batch], P = min(A.n_workers, T);
-  const int w = static_cast<int>(blockIdx.x) * kWarps + warp;
-  if (w >= P) return;
-  const Split split(T, P);
-  const int t_first = split.begin(w);
-  const int my_tiles = split.begin(w + 1) - t_first;
 
   auto stage_ptr = [&](int s) { return smem + (warp * kStages + s) * TL::kStageBytes; };
   auto info_of = [&](int block) {
-    if (block * 32 + lane < my_tiles) return tile_info<TL::kRuns, kSel>(A, pre, t_first + block * 32 + lane);
-    return TileInfo<TL::kRuns>();
+    const int x = block * 32 + lane;
+    if (x >= my_tiles) return TileInfo<TL::kRuns>();
+    if constexpr (kCluster) return tile_at<TL::kRuns, kSel>(A, the_b, the_g, t_first + x);
+    return tile_info<TL::kRuns, kSel>(A, pre, t_first + x);
   };
   TileInfo<TL::kRuns> cur = info_of(0), nxt;
   auto cur_key0 = [&](int r) {
@@ -419,7 +449,8 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
     return 4 * (gq * (D / 32) + mi / 2) + 2 * (mi % 2);
   };
   // The segment's state: the output rows where this worker saw all of it, else
-  // its record (segment + worker).
+  // its record (segment + worker; cluster: in this warp's ring, [group][D]).
+  float* held = reinterpret_cast<float*>(stage_ptr(0));
   auto finish = [&](int seg, bool whole) {
     float l0 = l_run.x, l1 = l_run.y, m0 = om.x, m1 = om.y;
 #pragma unroll
@@ -452,9 +483,15 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
         }
       }
       if (!whole) {
-        if (gq == 0)
-          *reinterpret_cast<float2*>(A.rec_ml + (rec * A.group + h) * 2) = make_float2(j ? m_run[1] : m_run[0], l);
-        float* ro = A.rec_o + (rec * A.group + h) * D;
+        const float2 ml = make_float2(j ? m_run[1] : m_run[0], l);
+        if (gq == 0) {
+          if constexpr (kCluster) {
+            s_ml[warp][h] = ml;
+          } else {
+            *reinterpret_cast<float2*>(A.rec_ml + (rec * A.group + h) * 2) = ml;
+          }
+        }
+        float* ro = kCluster ? held + h * D : A.rec_o + (rec * A.group + h) * D;
 #pragma unroll
         for (int mi = 0; mi < kMT; ++mi) {
           if constexpr (kBF) {
@@ -493,7 +530,15 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
       cur = nxt;
       nxt = info_of((i >> 5) + 1);
     }
-    if (left == 0) {
+    if (kCluster && i == 0) {
+      seg = the_seg;
+      reset();
+      load_q(the_b, the_g);
+      left = my_tiles;
+      key_end = length_of(A, the_b);
+      k_lo = first_key<kSel>(A, key_end);
+    }
+    if (!kCluster && left == 0) {
       seg = __shfl_sync(0xffffffffu, cur.seg, i & 31);
       const int b = A.by_hkv.div(seg), g = seg - b * A.hkv, Tb = A.by_hkv.div(pre[b + 1] - pre[b]);
       reset();
@@ -502,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
       left = min(Tb - done, my_tiles - i);
       whole = left == Tb;
       if (done == 0 && lane == 0) {
-        const int n = split.worker_of(pre[b] + g * Tb + Tb - 1) - w + 1;
+        const int n = Split(T, P).worker_of(pre[b] + g * Tb + Tb - 1) - w + 1;
         A.range[seg] = static_cast<uint32_t>(w) << 16 | static_cast<uint32_t>(n);
       }
       key_end = length_of(A, b);
@@ -510,7 +555,12 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
     }
     // every lane polls; whether to go on is a decision of the whole warp
     const bool ready = wait_parity(&bars[s], parity, A.wd);
-    if (!__all_sync(0xffffffffu, ready)) break;
+    if (!__all_sync(0xffffffffu, ready)) {
+      // gave up (reported): no state; the copies still on their way get one more bounded wait
+      for (int j = 1; j < min(kStages, my_tiles - i); ++j)
+        wait_parity(&bars[(s + j) % kStages], s + j < kStages ? parity : parity ^ 1, A.wd);
+      break;
+    }
 #pragma unroll 1
     for (int r = 0; r < TL::kRuns; ++r) {
       const int key0 = __shfl_sync(0xffffffffu, cur_key0(r), i & 31);
@@ -593,6 +643,9 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
       // ---- online softmax per head; positions are looked at only in tiles
       // that reach past [k_lo, key_end)
       uint32_t pb[2][2];
+      // bf16: what rounding to bf16 took from the weights, for a second product
+      // (eight bits of a weight are fewer than the result's own rounding keeps)
+      [[maybe_unused]] uint32_t pl[2][2];
       auto softmax = [&](auto masked_tag) {
         constexpr bool kMasked = decltype(masked_tag)::value;
         float2 x[2][2];                             // [mt][key half], heads 2qq and 2qq + 1
@@ -665,6 +718,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
           uint32_t packed[2];
+          [[maybe_unused]] uint32_t rest[2];
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const float2 y = add2(x[mt][hf], nref);
@@ -672,6 +726,8 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
             l_run = add2(l_run, p);
             if constexpr (kBF) {
               packed[hf] = pack_bf16x2(p.x, p.y);
+              rest[hf] = pack_bf16x2(p.x - __uint_as_float(packed[hf] << 16),
+                                     p.y - __uint_as_float(packed[hf] & 0xffff0000u));
             } else {
               if constexpr (kI4) om = fma2(p, make_float2(vo[mt][hf], vo[mt][hf]), om);
               const float u = vs[mt][hf] * to_unit;
@@ -681,6 +737,10 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
           }
           pb[mt][0] = transpose8x8(packed[0]);  // (head gq; S rows 2qq, 2qq+1)
           pb[mt][1] = transpose8x8(packed[1]);  // (head gq; S rows 8+2qq, 8+2qq+1)
+          if constexpr (kBF) {
+            pl[mt][0] = transpose8x8(rest[0]);
+            pl[mt][1] = transpose8x8(rest[1]);
+          }
         }
       };
       const bool inside = key0 >= k_lo && key0 + kTile <= key_end;
@@ -711,6 +771,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
             uint32_t a[4];
             ldsm_x4_trans(bf_addr<D>(vt, 16 * mt + 8 * (mi4 / 2) + mr, 16 * mi + 8 * (mi4 % 2)), a);
             mma16816_bf16(o[mi], a, pb[mt][0], pb[mt][1]);
+            mma16816_bf16(o[mi], a, pl[mt][0], pl[mt][1]);
           }
         }
       } else if constexpr (kI8) {
@@ -807,6 +868,47 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
       parity ^= 1;
     }
     if (--left == 0) finish(seg, whole);
+  }
+  if constexpr (kCluster) {
+    // every warp's state is in its CTA's shared memory: a thread takes two
+    // channels of a head from all of them
+    cluster_sync_all();
+    const int c = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_ctarank());
+    const uint32_t ml0 = smem_u32(&s_ml[0][0]), rec0 = smem_u32(smem);
+    for (int x = rank * kThreads + static_cast<int>(threadIdx.x); x < A.group * (D / 2); x += c * kThreads) {
+      const int h = x / (D / 2), dim = 2 * (x - h * (D / 2));
+      float m = -INFINITY;
+      for (int r = 0; r < c; ++r) {
+#pragma unroll
+        for (int v = 0; v < kWarps; ++v) m = fmaxf(m, ld_cluster_f2(mapa_shared(ml0 + (v * 8 + h) * 8, r)).x);
+      }
+      const float ref = m == -INFINITY ? 0.f : m;
+      float l = 0.f;
+      float y[2] = {0.f, 0.f};
+      for (int r = 0; r < c; ++r) {
+        float2 ml[kWarps], part[kWarps];
+#pragma unroll
+        for (int v = 0; v < kWarps; ++v) {
+          ml[v] = ld_cluster_f2(mapa_shared(ml0 + (v * 8 + h) * 8, r));
+          part[v] = ld_cluster_f2(mapa_shared(rec0 + v * kStages * TL::kStageBytes + (h * D + dim) * 4, r));
+        }
+#pragma unroll
+        for (int v = 0; v < kWarps; ++v) {
+          if (ml[v].x == -INFINITY) continue;  // no key there (and perhaps no record)
+          const float wt = ex2_approx(ml[v].x - ref);
+          l = fmaf(wt, ml[v].y, l);
+          y[0] = fmaf(wt, part[v].x, y[0]);
+          y[1] = fmaf(wt, part[v].y, y[1]);
+        }
+      }
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      y[0] *= inv;
+      y[1] *= inv;
+      apply_epilogue_vec(y, A.epi);
+      *reinterpret_cast<uint32_t*>(A.out + (static_cast<int64_t>(the_b) * A.hq + the_g * A.group + h) * D + dim) =
+          pack_bf16x2(y[0], y[1]);
+    }
+    cluster_sync_all();  // nobody leaves while its shared memory is read
   }
 }
 
@@ -936,20 +1038,79 @@ fa_status allow_smem(const void* kern, int bytes, std::atomic<bool> (&done)[64])
   return FA_OK;
 }
 
+// Tiles that a segment has at most.
+template <int D, int kKind, bool kSel>
+int64_t most_tiles(const PageArgs& A) {
+  constexpr int kKeys = Tile<D, kKind>::kKeys;
+  int64_t keys = A.capacity;
+  if (kSel) {
+    const int64_t chosen = static_cast<int64_t>(A.top_k) * A.page_size;
+    keys = chosen < keys ? chosen : keys;
+  } else if (A.window > 0 && A.window + kKeys < keys) {
+    keys = A.window + kKeys;  // the window may start inside a tile
+  }
+  return (keys + kKeys - 1) / kKeys;
+}
+
+// One cluster per segment: as many CTAs as the device holds at once and the
+// tiles are worth; 0 where spreading all tiles evenly over the device, and a
+// second kernel's merge, is faster.  Counted in tiles one after the other: a
+// cluster's warps take seg_tiles / (4 c) each, in turns where the clusters do
+// not fit at once; an even split the device's share of all tiles, and about
+// four tiles' time for the records, the second launch and its reads.  (XX)
+template <int D, int kKind>
+int cluster_of(int64_t segs, int64_t seg_tiles) {
+  const int64_t resident = static_cast<int64_t>(device_sm_count()) * Tile<D, kKind>::kCtas;
+  int64_t c = 1;
+  while (c < 8 && segs * c * 2 <= resident && c * kWarps < seg_tiles) c *= 2;
+  const int64_t turns = (segs * c + resident - 1) / resident;
+  const int64_t clustered = (seg_tiles + c * kWarps - 1) / (c * kWarps) * turns;
+  const int64_t even = (segs * seg_tiles + resident * kWarps - 1) / (resident * kWarps) + 4;
+  return clustered <= even && segs * c < (int64_t(1) << 31) ? static_cast<int>(c) : 0;
+}
+
+template <int D, int kKind, bool kSel>
+fa_status launch_clustered(const PageArgs& A, const Maps& maps, int cluster, const LaunchCtx& ctx) {
+  using TL = Tile<D, kKind>;
+  auto kern = decode_pages_kernel<D, kKind, kSel, true>;
+  static_assert(TL::kStages * TL::kStageBytes >= 8 * D * 4, "a warp's record in its ring");
+  static std::atomic<bool> allowed[64];
+  const fa_status st = allow_smem(reinterpret_cast<const void*>(kern), TL::kSmem, allowed);
+  if (st != FA_OK) return st;
+  note_variant(reinterpret_cast<const void*>(kern));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(A.batch) * A.hkv * cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = TL::kSmem;
+  cfg.stream = ctx.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kern, maps.k, maps.v, maps.k32, maps.v32, A));
+}
+
 template <int D, int kKind, bool kSel>
 fa_status launch_typed(const fa_decode_params& p, const fa_kv_pages& pg, PageArgs A, const LaunchCtx& ctx) {
   using TL = Tile<D, kKind>;
-  auto kern = decode_pages_kernel<D, kKind, kSel>;
+  auto kern = decode_pages_kernel<D, kKind, kSel, false>;
   auto merge = decode_pages_merge_kernel<D>;
-  static std::atomic<bool> allowed[64];
-  static_assert(TL::kSmem + (kMaxBatch + 1) * 4 <= 232448, "shared memory of a CTA");
-  fa_status st = allow_smem(reinterpret_cast<const void*>(kern), TL::kSmem + (kMaxBatch + 1) * 4, allowed);
-  if (st != FA_OK) return st;
   Maps maps = {};
+  fa_status st = FA_OK;
   if constexpr (kKind != FA_I4) {
     st = encode_maps<D, kKind == FA_BF16>(p, pg, &maps);
     if (st != FA_OK) return st;
   }
+  const int64_t seg_tiles = most_tiles<D, kKind, kSel>(A);
+  A.batch = p.batch;
+  if (const int cluster = cluster_of<D, kKind>(static_cast<int64_t>(p.batch) * A.hkv, seg_tiles))
+    return launch_clustered<D, kKind, kSel>(A, maps, cluster, ctx);
+  static std::atomic<bool> allowed[64];
+  static_assert(TL::kSmem + (kMaxBatch + 1) * 4 <= 232448, "shared memory of a CTA");
+  st = allow_smem(reinterpret_cast<const void*>(kern), TL::kSmem + (kMaxBatch + 1) * 4, allowed);
+  if (st != FA_OK) return st;
   // Workers: four per CTA, as many CTAs as fit, as far as the caller's
   // workspace holds their records (it is sized for eight workers per SM that
   // serve min(hq, 8) heads each).
@@ -970,9 +1131,6 @@ fa_status launch_typed(const fa_decode_params& p, const fa_kv_pages& pg, PageArg
     A.block_table = all.block_table + static_cast<int64_t>(b0) * A.max_pages;
     if (kSel) A.selected = all.selected + static_cast<int64_t>(b0) * A.hkv_real * A.top_k;
     // no more workers than there can be tiles
-    const int64_t seg_tiles = kSel ? static_cast<int64_t>(A.top_k < A.max_pages ? A.top_k : A.max_pages) *
-                                         (A.page_size / kTile)
-                                   : A.capacity / kTile;
     const int64_t most = seg_tiles * A.batch * A.hkv;
     if (most >= (int64_t(1) << 31)) return FA_ERR_UNSUPPORTED;
     A.n_workers = most < workers ? static_cast<int>((most + kWarps - 1) / kWarps * kWarps) : workers;

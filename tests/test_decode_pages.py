@@ -62,7 +62,15 @@ INT4_CASES = [
     ([2000, 300, 1025, 5], 8, 2, 128, 64, 700),
     ([2000, 90, 31], 4, 4, 256, 32, 1),          # a window of one key
     ([129] * 40, 4, 2, 64, 64, 100),
-    ([9000, 1, 4097], 4, 1, 128, 128, 0),        # one KV head over the whole device
+    ([9000, 1, 4097], 4, 1, 128, 128, 0),
+    # long enough that all tiles are dealt over the device and split segments merged by a second kernel
+    ([30011], 4, 1, 128, 96, 0),
+    ([17000, 0, 33, 23456, 1], 16, 2, 128, 128, 0),
+    ([40000, 7], 24, 1, 64, 64, 0),              # three passes of 8 heads
+    ([25001, 12000], 2, 1, 32, 64, 0),
+    ([25001, 64], 3, 1, 96, 32, 0),
+    ([20000, 9001], 8, 1, 256, 32, 0),
+    ([30000, 20000], 4, 2, 128, 64, 15000),
 ]
 
 
@@ -121,6 +129,12 @@ SELECT_CASES = [
     ([1500, 31], 8, 1, 256, 32, 9, 3, 3),
     ([777, 1024], 4, 4, 32, 32, 1, 0, 1),
     ([9999], 2, 1, 64, 32, 200, 1, 1),
+    # selections long enough to be dealt over the device
+    ([33000], 8, 1, 128, 32, 900, 2, 2),
+    ([30000, 5, 26000], 3, 1, 64, 64, 420, 0, 1),
+    ([16000, 12000], 2, 1, 256, 32, 350, 1, 1),
+    ([25000], 1, 1, 96, 96, 250, 1, 1),
+    ([33000], 4, 1, 32, 32, 1000, 1, 1),
 ]
 
 
