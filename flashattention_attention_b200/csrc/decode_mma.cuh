@@ -150,11 +150,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
-__device__ __forceinline__ void griddep_launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // The worker whose range [w*T/P, (w+1)*T/P) holds tile x.
 __device__ __forceinline__ int worker_of(long long x, long long T, long long P) {
   return static_cast<int>((x * P + P - 1) / T);

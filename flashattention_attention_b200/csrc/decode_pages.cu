@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
   __shared__ int32_t warp_sums[kWarps];
   __shared__ float2 s_ml[kWarps][8];  // cluster: each warp's (m, l) per head
 
-  if constexpr (!kCluster) griddep_launch_dependents();
+  griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gq = lane >> 2, qq = lane & 3;
   uint64_t* bars = all_bars + warp * kStages;
@@ -230,6 +230,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
     for (int s = 0; s < kStages; ++s) mbar_init(&bars[s], 1);
     fence_barrier_init();
   }
+  griddep_wait();
   // this warp's tiles: [t_first, t_first + my_tiles) of all, or of the cluster's segment
   int w = 0, T = 0, P = 1, t_first, my_tiles, the_seg = 0, the_b = 0, the_g = 0;
   if constexpr (kCluster) {
@@ -926,6 +927,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_pages_merge_kernel(const
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int seg = A.by_group.div(blockIdx.x), h = blockIdx.x - seg * A.group;
   const int b = A.by_hkv.div(seg), g = seg - b * A.hkv;
+  griddep_launch_dependents();
   griddep_wait();
   const int p0 = __ldcg(A.prefix + b), p1 = __ldcg(A.prefix + b + 1);
   const uint32_t range = __ldcg(A.range + seg);
@@ -1077,19 +1079,8 @@ fa_status launch_clustered(const PageArgs& A, const Maps& maps, int cluster, con
   static std::atomic<bool> allowed[64];
   const fa_status st = allow_smem(reinterpret_cast<const void*>(kern), TL::kSmem, allowed);
   if (st != FA_OK) return st;
-  note_variant(reinterpret_cast<const void*>(kern));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(A.batch) * A.hkv * cluster));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = TL::kSmem;
-  cfg.stream = ctx.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, kern, maps.k, maps.v, maps.k32, maps.v32, A));
+  return launch_dependent(kern, dim3(static_cast<unsigned>(static_cast<int64_t>(A.batch) * A.hkv * cluster)), kThreads,
+                          TL::kSmem, cluster, ctx.stream, maps.k, maps.v, maps.k32, maps.v32, A);
 }
 
 template <int D, int kKind, bool kSel>
@@ -1136,21 +1127,11 @@ fa_status launch_typed(const fa_decode_params& p, const fa_kv_pages& pg, PageArg
     A.n_workers = most < workers ? static_cast<int>((most + kWarps - 1) / kWarps * kWarps) : workers;
     A.rec_o = reinterpret_cast<float*>(ws + plan);
     A.rec_ml = A.rec_o + (static_cast<size_t>(A.batch) * A.hkv + A.n_workers) * A.group * D;
-    note_variant(reinterpret_cast<const void*>(kern));
-    kern<<<A.n_workers / kWarps, kThreads, TL::kSmem + (A.batch + 1) * 4, ctx.stream>>>(maps.k, maps.v, maps.k32,
-                                                                                        maps.v32, A);
-    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-    note_variant(reinterpret_cast<const void*>(merge));
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(A.batch * A.hkv * A.group));
-    cfg.blockDim = dim3(kMergeThreads);
-    cfg.stream = ctx.stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, merge, A) != cudaSuccess) return FA_ERR_CUDA;
+    st = launch_dependent(kern, dim3(A.n_workers / kWarps), kThreads, TL::kSmem + (A.batch + 1) * 4, 0, ctx.stream, maps.k,
+                          maps.v, maps.k32, maps.v32, A);
+    if (st != FA_OK) return st;
+    st = launch_dependent(merge, dim3(static_cast<unsigned>(A.batch * A.hkv * A.group)), kMergeThreads, 0, 0, ctx.stream, A);
+    if (st != FA_OK) return st;
   }
   return FA_OK;
 }

@@ -14,6 +14,31 @@ struct LaunchCtx {
   Watchdog wd;
 };
 
+// Launch with programmatic stream serialisation: the kernel may start while the
+// one before it in the stream still runs (if that one allows it,
+// griddep_launch_dependents), so it calls griddep_wait() in every block before
+// it touches global memory.  cluster > 1: that many blocks per cluster.
+void note_variant(const void* kernel_fn);
+template <typename... P, typename... A>
+fa_status launch_dependent(void (*kern)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream,
+                           const A&... args) {
+  note_variant(reinterpret_cast<const void*>(kern));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
 Epilogue make_epilogue(const fa_epi_op* ops, int n);
 
 // Records that a kernel instantiation was launched (distinct-variant count).

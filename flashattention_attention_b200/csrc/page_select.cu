@@ -11,7 +11,7 @@
 //      query heads on N, bf16 operands, fp32 sums) together with
 //      A = |q| . max(|lo|, |hi|), which bounds the terms' absolute sum;
 //   2. CTA 0 finds a narrow range [t0, t1] that holds the k-th largest score.
-//      With e = kError max A every score is within e of the exact one, so pages
+//      With e = error_share max A every score is within e of the exact one, so pages
 //      above t1 + 2e are in, pages below t0 - 2e are out, and the few between
 //      are summed again in fp64 (products of two bf16 numbers are exact) and
 //      rounded to fp32 once;
@@ -29,18 +29,30 @@ constexpr int kThreads = 256;
 constexpr int kSelWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 2048;
-// Of A: an fp32 sum on the tensor cores over at most 32 k-steps (d = 256, hi
-// and lo) whose 17 addends may each lose 2^-22 of the largest partial sum
-// (which is at most A): 32 * 17 * 2^-22 < 2^-12.
-constexpr float kError = 1.f / 4096.f;
+// The error of a score, as a share of A: an fp32 sum on the tensor cores whose
+// k-steps (d / 16 of hi and of lo) have 17 addends, each of which may lose
+// 2^-22 of the largest partial sum (at most A).
+__device__ __forceinline__ float error_share(int d) { return static_cast<float>(d / 8 * 17) * 0x1p-22f; }
+
+constexpr int kHeld = 4096;    // scores CTA 0 holds in shared memory (more go through L2)
+constexpr int kBetween = 256;  // pages next to the border that are ranked directly
+
+struct PickShared {
+  int hist[kBins];
+  float scores[kHeld];
+  float part[kMaxCluster][3];  // of each CTA's pages: largest A, least and greatest score
+  int between[kBetween];
+  uint32_t exact[kBetween];
+  int warp_sum[kSelWarps];
+  int bin, above, inside, n_between;
+};
 
 struct SelectArgs {
   const __nv_bfloat16* q;
   const __nv_bfloat16* bounds;
   const int32_t* seqlens;
   int32_t* selected;
-  float* scores;    // [batch*hkv][max_pages]
-  float* absolute;  // [batch*hkv][kMaxCluster]: largest A of each CTA
+  float* scores;  // [batch*hkv][max_pages], where there are more than kHeld
   int batch, hq, hkv, group, d, top_k, n_first, n_recent;
   const int32_t* block_table;
   int max_pages, page_size, num_pages;
@@ -54,27 +66,33 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Page ids of a row of the block table; one outside the pool is reported and read as page 0.
-__device__ __forceinline__ int page_id(const SelectArgs& A, int b, int p) {
-  const int pg = A.block_table[static_cast<int64_t>(b) * A.max_pages + p];
+// A page id outside the pool is reported and read as page 0.
+__device__ __forceinline__ int checked(const SelectArgs& A, int pg) {
   if (pg >= 0 && pg < A.num_pages) return pg;
   record_status(A.wd, kStatusRange);
   return 0;
 }
+__device__ __forceinline__ int page_id(const SelectArgs& A, int b, int p) {
+  return checked(A, A.block_table[static_cast<int64_t>(b) * A.max_pages + p]);
+}
 
-// Scores of pages first + 16 i .. for one unit; kJ = ceil(d / 32): lane quarter
-// qq holds channels [8 qq + 32 j, +8) of rows gq and gq + 8.
+// Scores of pages [lo_page, hi_page) of one unit into CTA 0's shared memory (or
+// to L2); kJ = ceil(d / 32): lane quarter qq holds channels [8 qq + 32 j, +8)
+// of rows gq and gq + 8.
 template <int kJ>
-__device__ __forceinline__ void score_pages(const SelectArgs& A, int u, int b, int g, int lo_page, int hi_page) {
+__device__ __forceinline__ void score_pages(const SelectArgs& A, PickShared& S, int u, int b, int g, int lo_page,
+                                            int hi_page, const int (&first_pg)[2]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, qq = lane & 3;
   const int rank = static_cast<int>(cluster_ctarank());
   const int stride = 16 * static_cast<int>(cluster_size()) * kSelWarps;
-  float most = 0.f;
+  const bool held = hi_page - lo_page <= kHeld;
+  const uint32_t remote = mapa_shared(smem_u32(S.scores), 0);
+  float most = 0.f, least = INFINITY, greatest = -INFINITY;
   const __nv_bfloat16* q_unit = A.q + (static_cast<int64_t>(b) * A.hq + static_cast<int64_t>(g) * A.group) * A.d;
   int p0 = lo_page + 16 * (rank * kSelWarps + warp);
   int pg[2];  // the lane's two pages, looked up one round ahead
 #pragma unroll
-  for (int i = 0; i < 2; ++i) pg[i] = p0 + gq + 8 * i < hi_page ? page_id(A, b, p0 + gq + 8 * i) : -1;
+  for (int i = 0; i < 2; ++i) pg[i] = p0 + gq + 8 * i < hi_page ? checked(A, first_pg[i]) : -1;
   for (; p0 < hi_page; p0 += stride) {
     const uint4* row[2];
 #pragma unroll
@@ -137,51 +155,68 @@ __device__ __forceinline__ void score_pages(const SelectArgs& A, int u, int b, i
       best[i] = fmaxf(best[i], __shfl_xor_sync(0xffffffffu, best[i], 1));
       best[i] = fmaxf(best[i], __shfl_xor_sync(0xffffffffu, best[i], 2));
       const int p = p0 + gq + 8 * i;
-      if (qq == 0 && p < hi_page) A.scores[static_cast<int64_t>(u) * A.max_pages + p] = best[i];
+      if (p >= hi_page) continue;
+      least = fminf(least, best[i]);
+      greatest = fmaxf(greatest, best[i]);
+      if (qq != 0) continue;
+      if (held) {
+        st_cluster_f32(remote + 4 * (p - lo_page), best[i]);
+      } else {
+        A.scores[static_cast<int64_t>(u) * A.max_pages + p] = best[i];
+      }
     }
   }
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
-  __shared__ float s_most[kSelWarps];
-  if (lane == 0) s_most[warp] = most;
+  for (int off = 16; off > 0; off >>= 1) {
+    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+    least = fminf(least, __shfl_xor_sync(0xffffffffu, least, off));
+    greatest = fmaxf(greatest, __shfl_xor_sync(0xffffffffu, greatest, off));
+  }
+  __shared__ float s_part[kSelWarps][3];
+  if (lane == 0) {
+    s_part[warp][0] = most;
+    s_part[warp][1] = least;
+    s_part[warp][2] = greatest;
+  }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kSelWarps; ++w) most = fmaxf(most, s_most[w]);
-    A.absolute[static_cast<int64_t>(u) * kMaxCluster + rank] = most;
+  if (threadIdx.x < 3) {
+    const int x = threadIdx.x;
+    float v = s_part[0][x];
+    for (int w = 1; w < kSelWarps; ++w) v = x == 1 ? fminf(v, s_part[w][x]) : fmaxf(v, s_part[w][x]);
+    st_cluster_f32(mapa_shared(smem_u32(&S.part[rank][x]), 0), v);
   }
 }
 
-// The exact score of page p by one warp: fp64 sums of exact products, rounded once.
+// The exact score of page p by one warp: fp64 sums of exact products, rounded
+// once; four heads' sums at a time.
 __device__ float exact_score(const SelectArgs& A, int b, int g, int p) {
   const int lane = threadIdx.x & 31;
   const __nv_bfloat16* row = A.bounds + (static_cast<int64_t>(page_id(A, b, p)) * A.hkv + g) * 2 * A.d;
+  const __nv_bfloat16* q = A.q + (static_cast<int64_t>(b) * A.hq + static_cast<int64_t>(g) * A.group) * A.d;
   float best = -INFINITY;
-  for (int h = 0; h < A.group; ++h) {
-    const __nv_bfloat16* q = A.q + (static_cast<int64_t>(b) * A.hq + static_cast<int64_t>(g) * A.group + h) * A.d;
-    double sum = 0.0;
+#pragma unroll 1
+  for (int h = 0; h < A.group; h += 4, q += 4 * A.d) {
+    double sum[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 2
     for (int c = lane; c < A.d; c += 32) {
-      const float qv = __bfloat162float(q[c]);
-      sum += fmaxf(qv * __bfloat162float(row[c]), qv * __bfloat162float(row[A.d + c]));
+      const float lo = __bfloat162float(row[c]), hi = __bfloat162float(row[A.d + c]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float qv = h + k < A.group ? __bfloat162float(q[k * A.d + c]) : 0.f;
+        sum[k] += fmaxf(qv * lo, qv * hi);
+      }
     }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    best = fmaxf(best, static_cast<float>(sum));
+    for (int off = 16; off > 0; off >>= 1) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], off);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (h + k < A.group) best = fmaxf(best, static_cast<float>(sum[k]));
   }
   return best;
 }
-
-constexpr int kHeld = 4096;    // scores CTA 0 holds in shared memory (more stay in L2)
-constexpr int kBetween = 256;  // pages next to the border that are ranked directly
-
-struct PickShared {
-  int hist[kBins];
-  float scores[kHeld];
-  int between[kBetween];
-  uint32_t exact[kBetween];
-  int warp_sum[kSelWarps];
-  uint32_t warp_lo[kSelWarps], warp_hi[kSelWarps];
-  int bin, above, inside, n_between;
-};
 
 // Exclusive sum over the block's threads, and the total.
 __device__ __forceinline__ int block_scan(PickShared& S, int v, int& total) {
@@ -205,34 +240,15 @@ __device__ __forceinline__ int block_scan(PickShared& S, int v, int& total) {
   return before + incl - v;
 }
 
-// A range [lo, hi] of keys that holds the need-th largest (1-based) of m keys
-// key(i), and how many keys are above it: rounds of a histogram over the range
-// found so far, 2048 bins each, the whole block together, until at most
-// `few` keys are left in it or it is one key wide (at most three rounds).
+// Narrows [lo, hi], which holds all m keys key(i), to a range that holds the
+// need-th largest (1-based) of them, with the number of keys above it: rounds
+// of a histogram over the range found so far, 2048 bins each, the whole block
+// together, until at most `few` keys are left in it or it is one key wide (at
+// most three rounds).  S.hist is zero and the block in step on entry.
 template <typename K>
 __device__ __forceinline__ void kth_range(PickShared& S, int m, int need, int few, K key, uint32_t& lo, uint32_t& hi,
                                           int& above) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  lo = 0xffffffffu;
-  hi = 0;
-  for (int i = tid; i < m; i += kThreads) {
-    const uint32_t k = key(i);
-    lo = min(lo, k);
-    hi = max(hi, k);
-  }
-  lo = __reduce_min_sync(0xffffffffu, lo);
-  hi = __reduce_max_sync(0xffffffffu, hi);
-  if (lane == 0) {
-    S.warp_lo[warp] = lo;
-    S.warp_hi[warp] = hi;
-  }
-  for (int i = tid; i < kBins; i += kThreads) S.hist[i] = 0;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kSelWarps; ++w) {
-    lo = min(lo, S.warp_lo[w]);
-    hi = max(hi, S.warp_hi[w]);
-  }
+  const int tid = threadIdx.x;
   above = 0;
   while (true) {
     const int bits = 32 - __clz(hi - lo);
@@ -283,18 +299,16 @@ __device__ __forceinline__ void pick_pages(const SelectArgs& A, PickShared& S, i
   uint32_t kth = 0xffffffffu;  // pages above this key are taken, and the first `ties` equal to it
   int ties = 0;
   if (need > 0) {
-    float e = 0.f;
-    for (int r = 0; r < static_cast<int>(cluster_size()); ++r)
-      e = fmaxf(e, __ldcg(A.absolute + static_cast<int64_t>(u) * kMaxCluster + r));
-    e *= 2.f * kError;
-    if (sc != stored) {
-      for (int i = tid; i < m; i += kThreads) sc[i] = __ldcg(stored + i);
+    float e = 0.f, least = INFINITY, greatest = -INFINITY;
+    for (int r = 0; r < static_cast<int>(cluster_size()); ++r) {
+      e = fmaxf(e, S.part[r][0]);
+      least = fminf(least, S.part[r][1]);
+      greatest = fmaxf(greatest, S.part[r][2]);
     }
-    if (tid == 0) S.n_between = 0;
-    __syncthreads();
-    uint32_t k0, k1;
+    e *= 2.f * error_share(A.d);
+    uint32_t k0 = order_key(least), k1 = order_key(greatest);
     int above;
-    kth_range(S, m, need, 8, [&](int i) { return order_key(sc[i]); }, k0, k1, above);
+    kth_range(S, m, need, 4, [&](int i) { return order_key(sc[i]); }, k0, k1, above);
     // in: +inf, out: -inf, between: to be summed exactly
     const float in_from = key_float(k1) + e, out_to = key_float(k0) - e;
     int in = 0;
@@ -313,7 +327,9 @@ __device__ __forceinline__ void pick_pages(const SelectArgs& A, PickShared& S, i
     int taken;
     block_scan(S, in, taken);
     const int n_between = S.n_between;
-    if (n_between <= kBetween) {
+    if (n_between == need - taken && out_to > -INFINITY) {  // no choice to make: what is not out is in
+      kth = order_key(-INFINITY);
+    } else if (n_between <= kBetween) {
       for (int c = warp; c < n_between; c += kSelWarps) {
         const float x = exact_score(A, b, g, lo + S.between[c]);
         if (lane == 0) S.exact[c] = order_key(x);
@@ -337,7 +353,10 @@ __device__ __forceinline__ void pick_pages(const SelectArgs& A, PickShared& S, i
           if (lane == 0) sc[i] = x;
         }
       }
+      for (int i = tid; i < kBins; i += kThreads) S.hist[i] = 0;
       __syncthreads();
+      k0 = order_key(-INFINITY);
+      k1 = order_key(INFINITY);
       kth_range(S, m, need, 0, [&](int i) { return order_key(sc[i]); }, k0, k1, above);
       kth = k0;
       ties = need - above;
@@ -375,23 +394,39 @@ __device__ __forceinline__ void pick_pages(const SelectArgs& A, PickShared& S, i
 template <int kJ>
 __global__ void __launch_bounds__(kThreads, kJ == 8 ? 1 : 2) page_select_kernel(const SelectArgs A) {
   __shared__ PickShared S;
+  griddep_launch_dependents();
+  cluster_arrive_relaxed();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool first = cluster_ctarank() == 0;
   const int u = blockIdx.x / cluster_size(), b = u / A.hkv, g = u % A.hkv;
+  if (first) {
+    for (int i = threadIdx.x; i < kBins; i += kThreads) S.hist[i] = 0;
+    if (threadIdx.x == 0) S.n_between = 0;
+  }
+  griddep_wait();
+  // the first round's pages, looked up together with the length
+  int pg[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int p = A.n_first + 16 * (static_cast<int>(cluster_ctarank()) * kSelWarps + warp) + (lane >> 2) + 8 * i;
+    pg[i] = p < A.max_pages ? A.block_table[static_cast<int64_t>(b) * A.max_pages + p] : 0;
+  }
   const int64_t Lr = A.seqlens[b];
   const int64_t L = Lr < 0 ? 0 : (Lr > A.capacity ? A.capacity : Lr);
   const int n = static_cast<int>((L + A.page_size - 1) / A.page_size);
-  const bool first = cluster_ctarank() == 0;
   if (L != Lr && first && threadIdx.x == 0) record_status(A.wd, kStatusRange);
-  if (n <= A.top_k) {  // the same for the whole cluster
-    if (first) {
-      int32_t* out = A.selected + static_cast<int64_t>(u) * A.top_k;
-      for (int i = threadIdx.x; i < A.top_k; i += kThreads) out[i] = i < n ? i : -1;
-    }
-    return;
-  }
-  const int lo = A.n_first, hi = n - A.n_recent;  // lo + n_recent <= top_k < n
-  score_pages<kJ>(A, u, b, g, lo, hi);
+  const int lo = A.n_first, hi = n - A.n_recent;
+  cluster_wait();  // every block of the cluster has started: CTA 0's shared memory may be written
+  const bool choose = n > A.top_k;  // the same for the whole cluster; then lo < hi
+  if (choose) score_pages<kJ>(A, S, u, b, g, lo, hi, pg);
   cluster_sync_all();  // the cluster's scores are visible to CTA 0
-  if (first) pick_pages(A, S, u, b, g, n, lo, hi);
+  if (!first) return;
+  if (choose) {
+    pick_pages(A, S, u, b, g, n, lo, hi);
+  } else {
+    int32_t* out = A.selected + static_cast<int64_t>(u) * A.top_k;
+    for (int i = threadIdx.x; i < A.top_k; i += kThreads) out[i] = i < n ? i : -1;
+  }
 }
 
 // As many CTAs per cluster as the device holds at once (two CTAs per SM): few
@@ -403,18 +438,8 @@ fa_status launch_width(const SelectArgs& A, const LaunchCtx& ctx) {
   const int64_t most = static_cast<int64_t>(device_sm_count()) * (kJ == 8 ? 1 : 2);
   int cluster = 1;
   while (cluster < kMaxCluster && units * cluster * 2 <= most) cluster *= 2;
-  note_variant(reinterpret_cast<const void*>(page_select_kernel<kJ>));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(units * cluster));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = ctx.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, page_select_kernel<kJ>, A));
+  return launch_dependent(page_select_kernel<kJ>, dim3(static_cast<unsigned>(units * cluster)), kThreads, 0, cluster,
+                          ctx.stream, A);
 }
 
 size_t scores_bytes(int batch, int hkv, int max_pages) {
@@ -424,7 +449,7 @@ size_t scores_bytes(int batch, int hkv, int max_pages) {
 }  // namespace
 
 size_t page_select_workspace_bytes(int batch, int hkv, int max_pages) {
-  return scores_bytes(batch, hkv, max_pages) + static_cast<size_t>(batch) * hkv * kMaxCluster * sizeof(float);
+  return scores_bytes(batch, hkv, max_pages);
 }
 
 fa_status launch_page_select(const fa_page_select_params& p, const fa_kv_pages& pages, const LaunchCtx& ctx) {
@@ -435,8 +460,6 @@ fa_status launch_page_select(const fa_page_select_params& p, const fa_kv_pages& 
   A.seqlens = p.cache_seqlens;
   A.selected = p.selected;
   A.scores = static_cast<float*>(p.workspace);
-  A.absolute = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) +
-                                        scores_bytes(p.batch, p.hkv, pages.max_pages));
   A.batch = p.batch;
   A.hq = p.hq;
   A.hkv = p.hkv;

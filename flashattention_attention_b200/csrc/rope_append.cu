@@ -527,6 +527,8 @@ __device__ __forceinline__ void append_pages(const AppendArgs& A, int t0, uint32
 template <typename T, int W, int kCache>
 __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendArgs A) {
   __shared__ uint32_t s_lo[8][kThreads], s_hi[8][kThreads];
+  griddep_launch_dependents();
+  griddep_wait();
   // grid row 0 is the page role (where bounds are kept), the others are the parts of the tokens' rows
   int part = static_cast<int>(blockIdx.y);
   if (A.bounds != nullptr) {
@@ -574,6 +576,8 @@ struct ReadArgs {
 // lane) takes one token and `part_rows` of its 2 hkv rows (one part per grid row).
 template <int W, int kCache>
 __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs A) {
+  griddep_launch_dependents();
+  griddep_wait();
   const Group<W> G;
   const int d = A.pool.d, hkv = A.pool.hkv;
   const int64_t at_token = static_cast<int64_t>(blockIdx.x) * (kThreads / W) + threadIdx.x / W;
@@ -666,9 +670,8 @@ fa_status launch_append_typed(AppendArgs& A, const LaunchCtx& ctx) {
   const int page_blocks = A.bounds != nullptr ? A.total / A.window + 1 : 0;
   if (blocks < page_blocks) blocks = page_blocks;
   if (parts >= 65535) return FA_ERR_UNSUPPORTED;
-  note_variant(reinterpret_cast<const void*>(append_kernel<T, W, kCache>));
-  append_kernel<T, W, kCache><<<dim3(blocks, parts + (A.bounds != nullptr ? 1 : 0)), kThreads, 0, ctx.stream>>>(A);
-  return cuda_status(cudaGetLastError());
+  return launch_dependent(append_kernel<T, W, kCache>, dim3(blocks, parts + (A.bounds != nullptr ? 1 : 0)), kThreads, 0, 0,
+                          ctx.stream, A);
 }
 template <typename T, int W>
 fa_status launch_append_width(AppendArgs& A, const LaunchCtx& ctx) {
@@ -691,9 +694,7 @@ fa_status launch_read_typed(ReadArgs& A, const LaunchCtx& ctx) {
   A.part_rows = rows_per_item(A.total, 2 * A.pool.hkv, kGroups);
   const int parts = (2 * A.pool.hkv + A.part_rows - 1) / A.part_rows;
   if (parts > 65535) return FA_ERR_UNSUPPORTED;
-  note_variant(reinterpret_cast<const void*>(read_kernel<W, kCache>));
-  read_kernel<W, kCache><<<dim3((A.total - 1) / kGroups + 1, parts), kThreads, 0, ctx.stream>>>(A);
-  return cuda_status(cudaGetLastError());
+  return launch_dependent(read_kernel<W, kCache>, dim3((A.total - 1) / kGroups + 1, parts), kThreads, 0, 0, ctx.stream, A);
 }
 template <int W>
 fa_status launch_read(ReadArgs& A, const LaunchCtx& ctx) {
