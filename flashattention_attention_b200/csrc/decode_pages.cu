@@ -1064,7 +1064,7 @@ template <int D, int kKind>
 int cluster_of(int64_t segs, int64_t seg_tiles) {
   const int64_t resident = static_cast<int64_t>(device_sm_count()) * Tile<D, kKind>::kCtas;
   int64_t c = 1;
-  while (c < 8 && segs * c * 2 <= resident && c * kWarps < seg_tiles) c *= 2;
+  while (c < 8 && segs * (c + 1) <= resident && c * kWarps < seg_tiles) ++c;
   const int64_t turns = (segs * c + resident - 1) / resident;
   const int64_t clustered = (seg_tiles + c * kWarps - 1) / (c * kWarps) * turns;
   const int64_t even = (segs * seg_tiles + resident * kWarps - 1) / (resident * kWarps) + 4;
@@ -1095,7 +1095,6 @@ fa_status launch_typed(const fa_decode_params& p, const fa_kv_pages& pg, PageArg
     if (st != FA_OK) return st;
   }
   const int64_t seg_tiles = most_tiles<D, kKind, kSel>(A);
-  A.batch = p.batch;
   if (const int cluster = cluster_of<D, kKind>(static_cast<int64_t>(p.batch) * A.hkv, seg_tiles))
     return launch_clustered<D, kKind, kSel>(A, maps, cluster, ctx);
   static std::atomic<bool> allowed[64];
@@ -1136,18 +1135,30 @@ fa_status launch_typed(const fa_decode_params& p, const fa_kv_pages& pg, PageArg
   return FA_OK;
 }
 
-template <int D>
-fa_status launch_dim(const fa_decode_params& p, const fa_kv_pages& pg, const PageArgs& A, const LaunchCtx& ctx) {
-  if (A.selected == nullptr) return launch_typed<D, FA_I4, false>(p, pg, A, ctx);
-  if (p.kv_dtype == FA_I4) return launch_typed<D, FA_I4, true>(p, pg, A, ctx);
-  if (p.kv_dtype == FA_I8) return launch_typed<D, FA_I8, true>(p, pg, A, ctx);
-  return launch_typed<D, FA_BF16, true>(p, pg, A, ctx);
+// Calls f(dimension, kind, selected?) with the call's head size, cache type and
+// form as types; FA_ERR_UNSUPPORTED for a head size without kernels.
+template <int D, typename F>
+fa_status dispatch_kind(int kind, bool selected, const F& f) {
+  using Dim = std::integral_constant<int, D>;
+  using I4 = std::integral_constant<int, FA_I4>;
+  if (!selected) return f(Dim{}, I4{}, std::false_type{});
+  if (kind == FA_I4) return f(Dim{}, I4{}, std::true_type{});
+  if (kind == FA_I8) return f(Dim{}, std::integral_constant<int, FA_I8>{}, std::true_type{});
+  return f(Dim{}, std::integral_constant<int, FA_BF16>{}, std::true_type{});
+}
+template <typename F>
+fa_status dispatch(const fa_decode_params& p, bool selected, const F& f) {
+  switch (p.head_dim) {
+    case 32: return dispatch_kind<32>(p.kv_dtype, selected, f);
+    case 64: return dispatch_kind<64>(p.kv_dtype, selected, f);
+    case 96: return dispatch_kind<96>(p.kv_dtype, selected, f);
+    case 128: return dispatch_kind<128>(p.kv_dtype, selected, f);
+    case 256: return dispatch_kind<256>(p.kv_dtype, selected, f);
+  }
+  return FA_ERR_UNSUPPORTED;
 }
 
-}  // namespace
-
-fa_status launch_decode_pages(const fa_decode_params& p, const fa_kv_pages& pages, const int32_t* selected, int top_k,
-                              const LaunchCtx& ctx) {
+PageArgs page_args(const fa_decode_params& p, const fa_kv_pages& pages, const int32_t* selected, int top_k) {
   PageArgs A = {};
   A.q = static_cast<const __nv_bfloat16*>(p.q);
   A.k_cache = static_cast<const uint8_t*>(p.k_cache);
@@ -1179,15 +1190,28 @@ fa_status launch_decode_pages(const fa_decode_params& p, const fa_kv_pages& page
   A.by_group = FastDiv::of(A.group);
   A.scale_log2 = p.softmax_scale * kLog2e;
   A.epi = make_epilogue(p.epilogue, p.n_epilogue);
+  A.batch = p.batch;
+  return A;
+}
+
+}  // namespace
+
+bool decode_pages_needs_workspace(const fa_decode_params& p, const fa_kv_pages& pages, int top_k) {
+  const PageArgs A = page_args(p, pages, nullptr, top_k);
+  int cluster = 0;
+  dispatch(p, top_k > 0, [&](auto d, auto kind, auto sel) {
+    cluster = cluster_of<d, kind>(static_cast<int64_t>(p.batch) * A.hkv, most_tiles<d, kind, sel>(A));
+    return FA_OK;
+  });
+  return cluster == 0;
+}
+
+fa_status launch_decode_pages(const fa_decode_params& p, const fa_kv_pages& pages, const int32_t* selected, int top_k,
+                              const LaunchCtx& ctx) {
+  PageArgs A = page_args(p, pages, selected, top_k);
   A.wd = ctx.wd;
-  switch (p.head_dim) {
-    case 32: return launch_dim<32>(p, pages, A, ctx);
-    case 64: return launch_dim<64>(p, pages, A, ctx);
-    case 96: return launch_dim<96>(p, pages, A, ctx);
-    case 128: return launch_dim<128>(p, pages, A, ctx);
-    case 256: return launch_dim<256>(p, pages, A, ctx);
-  }
-  return FA_ERR_UNSUPPORTED;
+  return dispatch(p, selected != nullptr,
+                  [&](auto d, auto kind, auto sel) { return launch_typed<d, kind, sel>(p, pages, A, ctx); });
 }
 
 }  // namespace fa

@@ -383,7 +383,7 @@ fa_status fa_attention_decode(const fa_decode_params* p, fa_stream_t stream) {
 namespace {
 // Host checks shared by the paged decodes; *launch is false when the call has
 // nothing to do.
-fa_status decode_paged_args(const fa_decode_params* p, const fa_kv_pages* pages, bool* launch) {
+fa_status decode_paged_args(const fa_decode_params* p, const fa_kv_pages* pages, int32_t top_k, bool* launch) {
   *launch = false;
   fa_status st = decode_args(p, true);
   if (st != FA_OK) return st;
@@ -396,16 +396,27 @@ fa_status decode_paged_args(const fa_decode_params* p, const fa_kv_pages* pages,
     return FA_ERR_UNSUPPORTED;
   if (p->batch == 0) return FA_OK;
   if (pages->block_table == nullptr || !aligned16(pages->block_table)) return FA_ERR_INVALID;
-  const size_t need = fa_decode_workspace_size(p->batch, p->hq, p->capacity, p->head_dim);
-  if (p->workspace == nullptr || p->workspace_bytes < need || !aligned16(p->workspace)) return FA_ERR_WORKSPACE;
+  if (p->kv_dtype != FA_I4 && top_k == 0) {
+    const size_t need = fa_decode_workspace_size(p->batch, p->hq, p->capacity, p->head_dim);
+    if (p->workspace == nullptr || p->workspace_bytes < need || !aligned16(p->workspace)) return FA_ERR_WORKSPACE;
+  } else if (const size_t need = fa_decode_pages_workspace_size(p, pages, top_k)) {
+    if (p->workspace == nullptr || p->workspace_bytes < need || !aligned16(p->workspace)) return FA_ERR_WORKSPACE;
+  }
   *launch = true;
   return FA_OK;
 }
 }  // namespace
 
+size_t fa_decode_pages_workspace_size(const fa_decode_params* p, const fa_kv_pages* pages, int32_t top_k) {
+  if (p == nullptr || pages == nullptr || p->batch <= 0 || p->hkv <= 0 || p->hq <= 0 || p->hq % p->hkv != 0) return 0;
+  if (top_k < 0 || pages->page_size < 32 || pages->page_size % 32 != 0 || p->capacity <= 0) return 0;
+  if (!decode_pages_needs_workspace(*p, *pages, top_k)) return 0;
+  return fa_decode_workspace_size(p->batch, p->hq, p->capacity, p->head_dim);
+}
+
 fa_status fa_attention_decode_paged(const fa_decode_params* p, const fa_kv_pages* pages, fa_stream_t stream) {
   bool launch = false;
-  fa_status st = decode_paged_args(p, pages, &launch);
+  fa_status st = decode_paged_args(p, pages, 0, &launch);
   if (st != FA_OK || !launch) return st;
   LaunchCtx ctx;
   st = make_ctx(stream, &ctx);
@@ -419,7 +430,7 @@ fa_status fa_attention_decode_selected(const fa_decode_params* p, const fa_kv_pa
   if (p != nullptr && p->window != 0) return FA_ERR_INVALID;
   if (top_k < 1 || top_k > kMaxTopPages) return FA_ERR_INVALID;
   bool launch = false;
-  fa_status st = decode_paged_args(p, pages, &launch);
+  fa_status st = decode_paged_args(p, pages, top_k, &launch);
   if (st != FA_OK || !launch) return st;
   if (selected == nullptr || !aligned16(selected)) return FA_ERR_INVALID;
   LaunchCtx ctx;
@@ -611,7 +622,8 @@ fa_status fa_page_select(const fa_page_select_params* p, const fa_kv_pages* page
   for (const void* q : ptrs)
     if (q == nullptr || !aligned16(q)) return FA_ERR_INVALID;
   const size_t need = fa_page_select_workspace_size(p->batch, p->hkv, pages->max_pages);
-  if (p->workspace == nullptr || p->workspace_bytes < need || !aligned16(p->workspace)) return FA_ERR_WORKSPACE;
+  if (need > 0 && (p->workspace == nullptr || p->workspace_bytes < need || !aligned16(p->workspace)))
+    return FA_ERR_WORKSPACE;
   LaunchCtx ctx;
   st = make_ctx(stream, &ctx);
   if (st != FA_OK) return st;

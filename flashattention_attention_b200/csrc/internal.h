@@ -71,7 +71,9 @@ fa_status launch_kv_append_rope(const fa_kv_append_rope_params& p, const fa_kv_p
 fa_status launch_kv_read(const fa_kv_read_params& p, const fa_kv_pages& pages, const LaunchCtx& ctx);
 size_t page_select_workspace_bytes(int batch, int hkv, int max_pages);
 fa_status launch_page_select(const fa_page_select_params& p, const fa_kv_pages& pages, const LaunchCtx& ctx);
-// FA_I4 pools, or (selected given) the chosen pages of any pool
+// FA_I4 pools, or (top_k > 0) the chosen pages of any pool: whether the call
+// needs its workspace, and the launch
+bool decode_pages_needs_workspace(const fa_decode_params& p, const fa_kv_pages& pages, int top_k);
 fa_status launch_decode_pages(const fa_decode_params& p, const fa_kv_pages& pages, const int32_t* selected, int top_k,
                               const LaunchCtx& ctx);
 fa_status launch_decode(const fa_decode_params& p, const fa_kv_pages* pages, int split_keys, const LaunchCtx& ctx);

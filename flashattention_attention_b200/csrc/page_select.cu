@@ -437,19 +437,16 @@ fa_status launch_width(const SelectArgs& A, const LaunchCtx& ctx) {
   const int64_t units = static_cast<int64_t>(A.batch) * A.hkv;
   const int64_t most = static_cast<int64_t>(device_sm_count()) * (kJ == 8 ? 1 : 2);
   int cluster = 1;
-  while (cluster < kMaxCluster && units * cluster * 2 <= most) cluster *= 2;
+  while (cluster < kMaxCluster && units * (cluster + 1) <= most) ++cluster;
   return launch_dependent(page_select_kernel<kJ>, dim3(static_cast<unsigned>(units * cluster)), kThreads, 0, cluster,
                           ctx.stream, A);
-}
-
-size_t scores_bytes(int batch, int hkv, int max_pages) {
-  return (static_cast<size_t>(batch) * hkv * max_pages * sizeof(float) + 15) / 16 * 16;
 }
 
 }  // namespace
 
 size_t page_select_workspace_bytes(int batch, int hkv, int max_pages) {
-  return scores_bytes(batch, hkv, max_pages);
+  if (max_pages <= kHeld) return 0;
+  return (static_cast<size_t>(batch) * hkv * max_pages * sizeof(float) + 15) / 16 * 16;
 }
 
 fa_status launch_page_select(const fa_page_select_params& p, const fa_kv_pages& pages, const LaunchCtx& ctx) {

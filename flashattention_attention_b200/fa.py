@@ -8,7 +8,6 @@ when it is missing -- there is no fallback path.
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
 from typing import Optional, Sequence, Tuple
@@ -136,6 +135,8 @@ lib.fa_page_select_workspace_size.restype = ctypes.c_size_t
 lib.fa_page_select_workspace_size.argtypes = [_I32] * 3
 lib.fa_page_select.restype = ctypes.c_int
 lib.fa_page_select.argtypes = [ctypes.POINTER(PageSelectParams), ctypes.POINTER(KvPages), _P]
+lib.fa_decode_pages_workspace_size.restype = ctypes.c_size_t
+lib.fa_decode_pages_workspace_size.argtypes = [ctypes.POINTER(DecodeParams), ctypes.POINTER(KvPages), _I32]
 lib.fa_attention_decode_selected.restype = ctypes.c_int
 lib.fa_attention_decode_selected.argtypes = [ctypes.POINTER(DecodeParams), ctypes.POINTER(KvPages), _P, _I32, _P]
 lib.fa_compress_kv.restype = ctypes.c_int
@@ -662,17 +663,6 @@ def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
         return like.new_empty(shape, dtype=dtype)
 
 
-@functools.lru_cache(maxsize=256)
-def _decode_workspace_bytes(dev: int, batch: int, hq: int, capacity: int, head_dim: int) -> int:
-    with torch.cuda.device(dev):  # its count of SMs enters the size
-        return max(16, lib.fa_decode_workspace_size(batch, hq, capacity, head_dim))
-
-
-@functools.lru_cache(maxsize=256)
-def _select_workspace_bytes(batch: int, hkv: int, max_pages: int) -> int:
-    return max(16, lib.fa_page_select_workspace_size(batch, hkv, max_pages))
-
-
 def _refuse(dev: int, *operands) -> None:
     """ValueError for the first operand (tensor, name, dtype, shape) that is not a
     contiguous tensor of that dtype and shape on CUDA device dev."""
@@ -907,10 +897,12 @@ def page_select(q: torch.Tensor, key_bounds: torch.Tensor, cache_seqlens: torch.
         selected = out.data_ptr()
     else:
         selected = _operand(out, "out", dev, _INT32, shape)
+    nbytes = ws = 0
     if workspace is None:
-        nbytes = _select_workspace_bytes(batch, hkv, max_pages)
-        workspace = _new(q, nbytes, torch.uint8, stream)
-        ws = workspace.data_ptr()
+        if max_pages > 4096:  # smaller tables need none
+            nbytes = lib.fa_page_select_workspace_size(batch, hkv, max_pages)
+            workspace = _new(q, nbytes, torch.uint8, stream)
+            ws = workspace.data_ptr()
     else:
         nbytes, ws = workspace.numel() * workspace.element_size(), _workspace(workspace, dev)
     p = PageSelectParams(qp, bounds, lens, selected, batch, hq, hkv, d, top_k, _int(n_first, "n_first"),
@@ -943,11 +935,8 @@ def _decode_pages(q, k_pages, v_pages, cache_seqlens, block_table, selected, hq,
         op = out.data_ptr()
     else:
         op = _operand(out, "out", dev, _BF16, q.shape)
-    if workspace is None:
-        nbytes = _decode_workspace_bytes(dev, batch, hq, capacity, d)
-        workspace = _new(q, nbytes, torch.uint8, stream)
-        ws = workspace.data_ptr()
-    else:
+    nbytes = ws = 0
+    if workspace is not None:
         nbytes, ws = workspace.numel() * workspace.element_size(), _workspace(workspace, dev)
     p = DecodeParams(qp, kp, vp, ks, vs, lens, op, kind, batch, hq, hkv, d, capacity, _int(max_seqlen, "max_seqlen"),
                      _int(window, "window") if window > 0 else 0, 1.0 / math.sqrt(d) if scale is None else float(scale),
@@ -955,13 +944,24 @@ def _decode_pages(q, k_pages, v_pages, cache_seqlens, block_table, selected, hq,
     if epilogue:
         p.n_epilogue = _fill_epilogue(p.epilogue, epilogue)
     if selected is None:
-        _on_device(dev, stream, "fa_attention_decode_paged", lib.fa_attention_decode_paged, p, pg)
+        top_k, what, call = 0, "fa_attention_decode_paged", (lib.fa_attention_decode_paged, p, pg)
     else:
         shape = selected.shape
         if len(shape) != 3 or shape[0] != batch or shape[1] != hkv:
             raise ValueError(f"selected must be [{batch}, {hkv}, top_k]; got {tuple(shape)}")
-        _on_device(dev, stream, "fa_attention_decode_selected", lib.fa_attention_decode_selected, p, pg,
-                   _operand(selected, "selected", dev, _INT32, shape), shape[2])
+        top_k, what = shape[2], "fa_attention_decode_selected"
+        call = (lib.fa_attention_decode_selected, p, pg, _operand(selected, "selected", dev, _INT32, shape), top_k)
+    if workspace is None:
+        # only problems too long for one kernel need a workspace (the count of SMs decides)
+        if _current_device() == dev:
+            nbytes = lib.fa_decode_pages_workspace_size(p, pg, top_k)
+        else:
+            with torch.cuda.device(dev):
+                nbytes = lib.fa_decode_pages_workspace_size(p, pg, top_k)
+        if nbytes:
+            workspace = _new(q, nbytes, torch.uint8, stream)
+            p.workspace, p.workspace_bytes = workspace.data_ptr(), nbytes
+    _on_device(dev, stream, what, *call)
     return out
 
 

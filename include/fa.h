@@ -228,8 +228,8 @@ FA_API fa_status fa_attention_decode(const fa_decode_params *p, fa_stream_t stre
  * v_scales [num_pages, hkv, page_size, 2], the rows fa_kv_append_rope_paged
  * writes.  Key j has the value  code * step_j + offset_j  per channel; the
  * codes enter the tensor cores exactly, steps and offsets are applied to the
- * scores and the probabilities in fp32.  split_keys is not used (the work is
- * split evenly over the device).
+ * scores and the probabilities in fp32.  split_keys is not used, and the
+ * workspace need be no larger than fa_decode_pages_workspace_size() says.
  */
 typedef struct {
     const int32_t *block_table;
@@ -519,7 +519,8 @@ FA_API fa_status fa_kv_read_paged(const fa_kv_read_params *p, const fa_kv_pages 
  *   selected  device int32 [batch, hkv, top_k] out: the chosen logical page
  *             numbers, ascending, then -1 where n_b < top_k
  *   workspace device, >= fa_page_select_workspace_size() bytes, 16-byte
- *             aligned, contents need no initialisation
+ *             aligned, contents need no initialisation; that size is 0 (and
+ *             the workspace may be NULL) for tables of up to 4096 pages
  * Bounds or queries that are not finite give an unspecified choice (of pages
  * of the sequence).  A page id outside the pool is scored as page 0 and
  * reported as FA_ERR_INVALID.  head_dim a multiple of 16 up to 256; any hq /
@@ -548,9 +549,16 @@ FA_API fa_status fa_page_select(const fa_page_select_params *p, const fa_kv_page
  *             counts; one outside [0, ceil(L_b / page_size)), such as -1,
  *             stands for no key; a page named twice counts twice
  * A query head without any key gets the epilogue of 0.  p->window must be 0;
- * p->split_keys and p->max_seqlen are not used; workspace as
- * fa_attention_decode_paged's.
+ * p->split_keys and p->max_seqlen are not used.  workspace: at least
+ * fa_decode_pages_workspace_size() bytes.
+ *
+ * fa_decode_pages_workspace_size -- bytes of workspace that this call (top_k >
+ * 0) or fa_attention_decode_paged over FA_I4 pools (top_k = 0) needs with
+ * these sizes (pointers are not looked at): 0 where the problem is short enough
+ * for one kernel without a workspace, which may then be NULL, else
+ * fa_decode_workspace_size()'s.
  */
+FA_API size_t fa_decode_pages_workspace_size(const fa_decode_params *p, const fa_kv_pages *pages, int32_t top_k);
 FA_API fa_status fa_attention_decode_selected(const fa_decode_params *p, const fa_kv_pages *pages,
                                               const int32_t *selected, int32_t top_k, fa_stream_t stream);
 

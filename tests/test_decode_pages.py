@@ -285,9 +285,9 @@ def test_bad_lengths_and_pages_are_reported(kind):
 
 def test_int4_same_result_run_after_run_and_with_any_workspace():
     fa = _fa()
-    c = plain.Cache(150, "int4", [3000, 77, 1500], 2, 128, 64).cuda()
+    c = plain.Cache(150, "int4", [30000, 77, 15000], 1, 128, 64).cuda()
     q = _queries(150, 3, 8, 128).cuda()
-    kw = dict(hq=8, hkv=2, k_scales=c.ks_, v_scales=c.vs_)
+    kw = dict(hq=8, hkv=1, k_scales=c.ks_, v_scales=c.vs_)
     need = fa.decode_workspace_size(3, 8, c.width * 64, 128)
     ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
     a = fa.attention_decode_paged(q, c.kp_, c.vp_, c.lens_, c.table_, workspace=ws, **kw)

@@ -117,16 +117,18 @@ def test_page_select_refusals(fa):
                 dict(key_bounds=0x20008), dict(cache_seqlens=None), dict(selected=0x40004), dict(head_dim=100)):
         assert call(**bad) == fa.FA_ERR_INVALID, bad
     for bad in (dict(workspace=None), dict(workspace=0x50008), dict(workspace_bytes=16)):
-        assert call(**bad) == fa.FA_ERR_WORKSPACE, bad
+        assert call(pages(fa, max_pages=5000), **bad) == fa.FA_ERR_WORKSPACE, bad
     assert call(pages(fa, max_pages=65537, page_size=1)) == fa.FA_ERR_UNSUPPORTED
     assert call(head_dim=320) == fa.FA_ERR_UNSUPPORTED
     assert call(batch=0, q=None) == fa.FA_OK
     assert fa.lib.fa_page_select_workspace_size(0, 1, 1) == 0
-    assert fa.lib.fa_page_select_workspace_size(4, 8, 1000) >= 4 * 4 * 8 * 1000
+    assert fa.lib.fa_page_select_workspace_size(4, 8, 4096) == 0  # scores in shared memory
+    assert fa.lib.fa_page_select_workspace_size(4, 8, 5000) >= 4 * 4 * 8 * 5000
 
 
 def test_decode_refusals(fa):
-    need = fa.decode_workspace_size(2, 8, 128, 128)
+    long = 100000 * 32  # a capacity whose work is spread over the device, with a workspace
+    need = fa.decode_workspace_size(2, 8, long, 128)
 
     def params(**kw):
         p = fa.DecodeParams()
@@ -153,10 +155,18 @@ def test_decode_refusals(fa):
                     dict(kv_dtype=fa.FA_F32), dict(softmax_scale=float("nan")), dict(n_epilogue=9), dict(out=None)):
             assert call(**bad) == fa.FA_ERR_INVALID, bad
         assert call(head_dim=160) == fa.FA_ERR_UNSUPPORTED
-        assert call(workspace_bytes=need - 1) == fa.FA_ERR_WORKSPACE
+        far = dict(pg=pages(fa, max_pages=100000), capacity=long)
+        if call is selected:
+            far["top_k"] = 4096
+        for bad in (dict(workspace_bytes=need - 1), dict(workspace=None), dict(workspace=0x80008)):
+            assert call(**far, **bad) == fa.FA_ERR_WORKSPACE, bad
         assert call(pg=pages(fa, page_size=48), capacity=192) == fa.FA_ERR_INVALID
         assert call(pg=pages(fa, num_pages=1 << 25)) == fa.FA_ERR_UNSUPPORTED
         assert call(batch=0) == fa.FA_OK
+    size = lambda top_k, **kw: fa.lib.fa_decode_pages_workspace_size(
+        ctypes.byref(params(**kw)), ctypes.byref(pages(fa, max_pages=kw.get("capacity", 128) // 32)), top_k)
+    assert size(0) == 0 and size(3) == 0 and size(3, capacity=long) == 0 and size(0, batch=0) == 0
+    assert size(0, capacity=long) == need and size(4096, capacity=long) == need
     assert selected(window=4) == fa.FA_ERR_INVALID
     assert selected(top_k=0) == fa.FA_ERR_INVALID and selected(top_k=4097) == fa.FA_ERR_INVALID
     assert selected(sel=None) == fa.FA_ERR_INVALID and selected(sel=0xa0004) == fa.FA_ERR_INVALID
