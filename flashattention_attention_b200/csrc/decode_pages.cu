@@ -1064,7 +1064,7 @@ template <int D, int kKind>
 int cluster_of(int64_t segs, int64_t seg_tiles) {
   const int64_t resident = static_cast<int64_t>(device_sm_count()) * Tile<D, kKind>::kCtas;
   int64_t c = 1;
-  while (c < 8 && segs * (c + 1) <= resident && c * kWarps < seg_tiles) ++c;
+  while (c < 8 && segs * c * 2 <= resident && c * kWarps < seg_tiles) c *= 2;
   const int64_t turns = (segs * c + resident - 1) / resident;
   const int64_t clustered = (seg_tiles + c * kWarps - 1) / (c * kWarps) * turns;
   const int64_t even = (segs * seg_tiles + resident * kWarps - 1) / (resident * kWarps) + 4;

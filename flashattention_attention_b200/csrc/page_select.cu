@@ -437,7 +437,7 @@ fa_status launch_width(const SelectArgs& A, const LaunchCtx& ctx) {
   const int64_t units = static_cast<int64_t>(A.batch) * A.hkv;
   const int64_t most = static_cast<int64_t>(device_sm_count()) * (kJ == 8 ? 1 : 2);
   int cluster = 1;
-  while (cluster < kMaxCluster && units * (cluster + 1) <= most) ++cluster;
+  while (cluster < kMaxCluster && units * cluster * 2 <= most) cluster *= 2;
   return launch_dependent(page_select_kernel<kJ>, dim3(static_cast<unsigned>(units * cluster)), kThreads, 0, cluster,
                           ctx.stream, A);
 }
