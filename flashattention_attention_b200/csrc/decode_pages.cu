@@ -523,6 +523,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
 
   int seg = 0, left = 0, key_end = 0, k_lo = 0;  // left: tiles until this worker leaves the segment
   bool whole = false;
+  [[maybe_unused]] int tile_key = 0;  // every page: first key of the tile
   int s = 0;
   uint32_t parity = 0;
 #pragma unroll 1
@@ -538,6 +539,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
       left = my_tiles;
       key_end = length_of(A, the_b);
       k_lo = first_key<kSel>(A, key_end);
+      tile_key = __shfl_sync(0xffffffffu, cur.key0[0], 0);
     }
     if (!kCluster && left == 0) {
       seg = __shfl_sync(0xffffffffu, cur.seg, i & 31);
@@ -553,6 +555,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
       }
       key_end = length_of(A, b);
       k_lo = first_key<kSel>(A, key_end);
+      tile_key = __shfl_sync(0xffffffffu, cur.key0[0], i & 31);
     }
     // every lane polls; whether to go on is a decision of the whole warp
     const bool ready = wait_parity(&bars[s], parity, A.wd);
@@ -564,8 +567,8 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
     }
 #pragma unroll 1
     for (int r = 0; r < TL::kRuns; ++r) {
-      const int key0 = __shfl_sync(0xffffffffu, cur_key0(r), i & 31);
-      if (key0 == kNoKey) continue;
+      const int key0 = kSel ? __shfl_sync(0xffffffffu, cur_key0(r), i & 31) : tile_key + r * kTile;
+      if (kSel ? key0 == kNoKey : key0 >= key_end) continue;
       const uint32_t kt = smem_u32(stage_ptr(s)) + r * (TL::kBytes / TL::kRuns);
       const uint32_t vt = kt + TL::kBytes;
       const uint32_t ksc = smem_u32(stage_ptr(s)) + TL::kScaleOff + r * (TL::kScaleBytes / TL::kRuns);
@@ -868,6 +871,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
       s = 0;
       parity ^= 1;
     }
+    tile_key += TL::kKeys;
     if (--left == 0) finish(seg, whole);
   }
   if constexpr (kCluster) {
