@@ -6,19 +6,24 @@
 //
 // Which of two near pages is better must not depend on rounding, so the sum is
 // defined far more exactly than fp32; but only pages next to the k-th best need
-// that.  A cluster of one to eight CTAs serves one (sequence, KV head):
+// that:
 //   1. every warp scores 16 pages at a time on mma.sync m16n8k16 (pages on M,
 //      query heads on N, bf16 operands, fp32 sums) together with
 //      A = |q| . max(|lo|, |hi|), which bounds the terms' absolute sum;
-//   2. CTA 0 finds a narrow range [t0, t1] that holds the k-th largest score.
-//      With e = error_share max A every score is within e of the exact one, so pages
-//      above t1 + 2e are in, pages below t0 - 2e are out, and the few between
-//      are summed again in fp64 (products of two bf16 numbers are exact) and
-//      rounded to fp32 once;
+//   2. one block per (sequence, KV head) finds a narrow range [t0, t1] that
+//      holds the k-th largest score.  With e = error_share max A every score is
+//      within e of the exact one, so pages above t1 + 2e are in, pages below
+//      t0 - 2e are out, and the few between are summed again in fp64 (products
+//      of two bf16 numbers are exact) and rounded to fp32 once;
 //   3. the rest of the k is taken from those, the lower page first where
 //      rounded sums are equal, and the pages are written in order.
-// One pass over the bounds, 4 d bytes a page; the selection works on 4 bytes a
-// page out of L2.
+// Where the tables are short for the number of (sequence, KV head) pairs, a
+// cluster per pair does all of it in one launch, the scores going straight into
+// the choosing block's shared memory.  Else the pages of all pairs are dealt
+// evenly to the device's warps and a second kernel chooses, since a pair's own
+// cluster would go over its pages in rounds that each wait for memory (128
+// pairs of up to 1021 pages: 22.6 us in clusters of two, XX us dealt evenly).
+// One pass over the bounds, 4 d bytes a page; the choice works on 4 bytes a page.
 #include "decode_mma.cuh"
 #include "internal.h"
 
@@ -34,13 +39,13 @@ constexpr int kBins = 2048;
 // 2^-22 of the largest partial sum (at most A).
 __device__ __forceinline__ float error_share(int d) { return static_cast<float>(d / 8 * 17) * 0x1p-22f; }
 
-constexpr int kHeld = 4096;    // scores CTA 0 holds in shared memory (more go through L2)
+constexpr int kHeld = 4096;    // scores a block holds in shared memory (more stay in L2)
 constexpr int kBetween = 256;  // pages next to the border that are ranked directly
 
 struct PickShared {
-  int hist[kBins];
+  alignas(16) int hist[kBins];
   float scores[kHeld];
-  float part[kMaxCluster][3];  // of each CTA's pages: largest A, least and greatest score
+  float part[kMaxCluster][3];  // of each block's (or warp's) pages: largest A, least and greatest score
   int between[kBetween];
   uint32_t exact[kBetween];
   int warp_sum[kSelWarps];
@@ -52,7 +57,10 @@ struct SelectArgs {
   const __nv_bfloat16* bounds;
   const int32_t* seqlens;
   int32_t* selected;
-  float* scores;  // [batch*hkv][max_pages], where there are more than kHeld
+  // dealt evenly: the scores [batch*hkv][max_pages], and per 16 pages their
+  // largest A, least and greatest score [batch*hkv][max_pages / 16 rounded up]
+  float* scores;
+  float4* parts;
   int batch, hq, hkv, group, d, top_k, n_first, n_recent;
   const int32_t* block_table;
   int max_pages, page_size, num_pages;
@@ -76,102 +84,103 @@ __device__ __forceinline__ int page_id(const SelectArgs& A, int b, int p) {
   return checked(A, A.block_table[static_cast<int64_t>(b) * A.max_pages + p]);
 }
 
-// Scores of pages [lo_page, hi_page) of one unit into CTA 0's shared memory (or
-// to L2); kJ = ceil(d / 32): lane quarter qq holds channels [8 qq + 32 j, +8)
-// of rows gq and gq + 8.
+// Scores of 16 pages of one unit by one warp: best[i] of page row gq + 8 i (in
+// every lane quarter), and the largest A seen; pg: the lane's two page ids, -1
+// for none.  kJ = ceil(d / 32): quarter qq holds channels [8 qq + 32 j, +8).
 template <int kJ>
-__device__ __forceinline__ void score_pages(const SelectArgs& A, PickShared& S, int u, int b, int g, int lo_page,
-                                            int hi_page, const int (&first_pg)[2]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, qq = lane & 3;
-  const int rank = static_cast<int>(cluster_ctarank());
-  const int stride = 16 * static_cast<int>(cluster_size()) * kSelWarps;
-  const bool held = hi_page - lo_page <= kHeld;
-  const uint32_t remote = mapa_shared(smem_u32(S.scores), 0);
-  float most = 0.f, least = INFINITY, greatest = -INFINITY;
+__device__ __forceinline__ void score_group(const SelectArgs& A, int b, int g, const int (&pg)[2], float (&best)[2],
+                                            float& most) {
+  const int lane = threadIdx.x & 31, gq = lane >> 2, qq = lane & 3;
   const __nv_bfloat16* q_unit = A.q + (static_cast<int64_t>(b) * A.hq + static_cast<int64_t>(g) * A.group) * A.d;
-  int p0 = lo_page + 16 * (rank * kSelWarps + warp);
-  int pg[2];  // the lane's two pages, looked up one round ahead
+  uint4 lo[2][kJ], hi[2][kJ];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) pg[i] = p0 + gq + 8 * i < hi_page ? checked(A, first_pg[i]) : -1;
-  for (; p0 < hi_page; p0 += stride) {
-    const uint4* row[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      row[i] = pg[i] >= 0 ? reinterpret_cast<const uint4*>(A.bounds + (static_cast<int64_t>(pg[i]) * A.hkv + g) * 2 * A.d)
-                          : nullptr;
-    uint4 lo[2][kJ], hi[2][kJ];
+  for (int i = 0; i < 2; ++i) {
+    const uint4* row = reinterpret_cast<const uint4*>(A.bounds + (static_cast<int64_t>(pg[i]) * A.hkv + g) * 2 * A.d);
 #pragma unroll
     for (int j = 0; j < kJ; ++j) {
       const int chunk = qq + 4 * j;
-      const bool there = 8 * chunk < A.d;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const bool ok = there && row[i] != nullptr;
-        lo[i][j] = ok ? __ldcs(row[i] + chunk) : make_uint4(0, 0, 0, 0);
-        hi[i][j] = ok ? __ldcs(row[i] + A.d / 8 + chunk) : make_uint4(0, 0, 0, 0);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int p = p0 + stride + gq + 8 * i;
-      pg[i] = p < hi_page ? page_id(A, b, p) : -1;
-    }
-    float best[2] = {-INFINITY, -INFINITY};
-    for (int h0 = 0; h0 < A.group; h0 += 8) {  // eight query heads at a time
-      float s[4] = {0.f, 0.f, 0.f, 0.f}, t[4] = {0.f, 0.f, 0.f, 0.f};
-      const bool head_ok = h0 + gq < A.group;
-#pragma unroll
-      for (int j = 0; j < kJ; ++j) {
-        const int chunk = qq + 4 * j;
-        uint4 qv = make_uint4(0, 0, 0, 0);
-        if (head_ok && 8 * chunk < A.d)
-          qv = *(reinterpret_cast<const uint4*>(q_unit + static_cast<int64_t>(h0 + gq) * A.d) + chunk);
-        const uint32_t qr[4] = {qv.x, qv.y, qv.z, qv.w};
-        const uint32_t lr[2][4] = {{lo[0][j].x, lo[0][j].y, lo[0][j].z, lo[0][j].w},
-                                   {lo[1][j].x, lo[1][j].y, lo[1][j].z, lo[1][j].w}};
-        const uint32_t hr[2][4] = {{hi[0][j].x, hi[0][j].y, hi[0][j].z, hi[0][j].w},
-                                   {hi[1][j].x, hi[1][j].y, hi[1][j].z, hi[1][j].w}};
-#pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-          const uint32_t h4[4] = {hr[0][e], hr[1][e], hr[0][e + 1], hr[1][e + 1]};
-          const uint32_t l4[4] = {lr[0][e], lr[1][e], lr[0][e + 1], lr[1][e + 1]};
-          mma16816_bf16(s, h4, bf16x2_max(qr[e], 0u), bf16x2_max(qr[e + 1], 0u));
-          mma16816_bf16(s, l4, bf16x2_min(qr[e], 0u), bf16x2_min(qr[e + 1], 0u));
-          uint32_t a4[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) a4[x] = bf16x2_max(h4[x] & 0x7fff7fffu, l4[x] & 0x7fff7fffu);
-          mma16816_bf16(t, a4, qr[e] & 0x7fff7fffu, qr[e + 1] & 0x7fff7fffu);
-        }
-      }
-      // rows gq, gq + 8; heads h0 + 2 qq, + 1
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        if (h0 + 2 * qq + (x & 1) < A.group) best[x >> 1] = fmaxf(best[x >> 1], s[x]);
-        most = fmaxf(most, t[x]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      best[i] = fmaxf(best[i], __shfl_xor_sync(0xffffffffu, best[i], 1));
-      best[i] = fmaxf(best[i], __shfl_xor_sync(0xffffffffu, best[i], 2));
-      const int p = p0 + gq + 8 * i;
-      if (p >= hi_page) continue;
-      least = fminf(least, best[i]);
-      greatest = fmaxf(greatest, best[i]);
-      if (qq != 0) continue;
-      if (held) {
-        st_cluster_f32(remote + 4 * (p - lo_page), best[i]);
-      } else {
-        A.scores[static_cast<int64_t>(u) * A.max_pages + p] = best[i];
-      }
+      const bool ok = 8 * chunk < A.d && pg[i] >= 0;
+      lo[i][j] = ok ? __ldcs(row + chunk) : make_uint4(0, 0, 0, 0);
+      hi[i][j] = ok ? __ldcs(row + A.d / 8 + chunk) : make_uint4(0, 0, 0, 0);
     }
   }
+  best[0] = best[1] = -INFINITY;
+  for (int h0 = 0; h0 < A.group; h0 += 8) {  // eight query heads at a time
+    float s[4] = {0.f, 0.f, 0.f, 0.f}, t[4] = {0.f, 0.f, 0.f, 0.f};
+    const bool head_ok = h0 + gq < A.group;
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) {
+      const int chunk = qq + 4 * j;
+      uint4 qv = make_uint4(0, 0, 0, 0);
+      if (head_ok && 8 * chunk < A.d)
+        qv = *(reinterpret_cast<const uint4*>(q_unit + static_cast<int64_t>(h0 + gq) * A.d) + chunk);
+      const uint32_t qr[4] = {qv.x, qv.y, qv.z, qv.w};
+      const uint32_t lr[2][4] = {{lo[0][j].x, lo[0][j].y, lo[0][j].z, lo[0][j].w},
+                                 {lo[1][j].x, lo[1][j].y, lo[1][j].z, lo[1][j].w}};
+      const uint32_t hr[2][4] = {{hi[0][j].x, hi[0][j].y, hi[0][j].z, hi[0][j].w},
+                                 {hi[1][j].x, hi[1][j].y, hi[1][j].z, hi[1][j].w}};
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        const uint32_t h4[4] = {hr[0][e], hr[1][e], hr[0][e + 1], hr[1][e + 1]};
+        const uint32_t l4[4] = {lr[0][e], lr[1][e], lr[0][e + 1], lr[1][e + 1]};
+        mma16816_bf16(s, h4, bf16x2_max(qr[e], 0u), bf16x2_max(qr[e + 1], 0u));
+        mma16816_bf16(s, l4, bf16x2_min(qr[e], 0u), bf16x2_min(qr[e + 1], 0u));
+        uint32_t a4[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) a4[x] = bf16x2_max(h4[x] & 0x7fff7fffu, l4[x] & 0x7fff7fffu);
+        mma16816_bf16(t, a4, qr[e] & 0x7fff7fffu, qr[e + 1] & 0x7fff7fffu);
+      }
+    }
+    // rows gq, gq + 8; heads h0 + 2 qq, + 1
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (h0 + 2 * qq + (x & 1) < A.group) best[x >> 1] = fmaxf(best[x >> 1], s[x]);
+      most = fmaxf(most, t[x]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    best[i] = fmaxf(best[i], __shfl_xor_sync(0xffffffffu, best[i], 1));
+    best[i] = fmaxf(best[i], __shfl_xor_sync(0xffffffffu, best[i], 2));
+  }
+}
+
+// A warp's largest A, least and greatest score, the same in every lane.
+__device__ __forceinline__ void warp_stats(float& most, float& least, float& greatest) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
     most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
     least = fminf(least, __shfl_xor_sync(0xffffffffu, least, off));
     greatest = fmaxf(greatest, __shfl_xor_sync(0xffffffffu, greatest, off));
   }
+}
+
+// A cluster's share of pages [lo_page, hi_page) of its unit, at most 16 pages
+// per warp, into block 0's shared memory.
+template <int kJ>
+__device__ __forceinline__ void score_pages(const SelectArgs& A, PickShared& S, int b, int g, int lo_page, int hi_page,
+                                            const int (&first_pg)[2]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, qq = lane & 3;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const uint32_t remote = mapa_shared(smem_u32(S.scores), 0);
+  float most = 0.f, least = INFINITY, greatest = -INFINITY;
+  const int p0 = lo_page + 16 * (rank * kSelWarps + warp);
+  if (p0 < hi_page) {
+    int pg[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) pg[i] = p0 + gq + 8 * i < hi_page ? checked(A, first_pg[i]) : -1;
+    float best[2];
+    score_group<kJ>(A, b, g, pg, best, most);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int p = p0 + gq + 8 * i;
+      if (p >= hi_page) continue;
+      least = fminf(least, best[i]);
+      greatest = fmaxf(greatest, best[i]);
+      if (qq == 0) st_cluster_f32(remote + 4 * (p - lo_page), best[i]);
+    }
+  }
+  warp_stats(most, least, greatest);
   __shared__ float s_part[kSelWarps][3];
   if (lane == 0) {
     s_part[warp][0] = most;
@@ -184,6 +193,80 @@ __device__ __forceinline__ void score_pages(const SelectArgs& A, PickShared& S, 
     float v = s_part[0][x];
     for (int w = 1; w < kSelWarps; ++w) v = x == 1 ? fminf(v, s_part[w][x]) : fmaxf(v, s_part[w][x]);
     st_cluster_f32(mapa_shared(smem_u32(&S.part[rank][x]), 0), v);
+  }
+}
+
+// Pages of sequence b; whether they have to be chosen from is n > top_k.
+__device__ __forceinline__ int pages_of(const SelectArgs& A, int b, bool report) {
+  const int64_t Lr = A.seqlens[b];
+  const int64_t L = Lr < 0 ? 0 : (Lr > A.capacity ? A.capacity : Lr);
+  if (report && L != Lr) record_status(A.wd, kStatusRange);
+  return static_cast<int>((L + A.page_size - 1) / A.page_size);
+}
+
+// Dealt evenly: groups of 16 pages of all units, warp after warp, the KV heads
+// of the same pages next to each other (as their bounds are in memory).
+constexpr int kMaxBatch = 1024;  // sequences per launch
+template <int kJ>
+__global__ void __launch_bounds__(kThreads, kJ == 8 ? 1 : 2) page_score_kernel(const SelectArgs A) {
+  __shared__ int s_pre[kMaxBatch + 1];
+  __shared__ int s_sum[kSelWarps];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, qq = lane & 3;
+  // groups before each sequence
+  const int per = (A.batch + kThreads - 1) / kThreads;
+  const int b0 = min(A.batch, static_cast<int>(threadIdx.x) * per), b1 = min(A.batch, b0 + per);
+  auto groups = [&](int b, bool report) {
+    const int n = pages_of(A, b, report);
+    return n > A.top_k ? (n - A.n_first - A.n_recent + 15) / 16 * A.hkv : 0;
+  };
+  int own = 0;
+  for (int b = b0; b < b1; ++b) own += groups(b, blockIdx.x == 0);
+  int incl = own;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += v;
+  }
+  if (lane == 31) s_sum[warp] = incl;
+  __syncthreads();
+  int at = incl - own, total = 0;
+  for (int w = 0; w < kSelWarps; ++w) {
+    if (w < warp) at += s_sum[w];
+    total += s_sum[w];
+  }
+  for (int b = b0; b < b1; ++b) {
+    s_pre[b] = at;
+    at += groups(b, false);
+  }
+  if (threadIdx.x == 0) s_pre[A.batch] = total;
+  __syncthreads();
+  const int per_unit = (A.max_pages + 15) / 16;
+  for (int x = blockIdx.x * kSelWarps + warp; x < total; x += gridDim.x * kSelWarps) {
+    int b = 0, end = A.batch - 1;  // the last b with s_pre[b] <= x
+    while (b < end) {
+      const int mid = (b + end + 1) >> 1;
+      if (s_pre[mid] <= x) b = mid; else end = mid - 1;
+    }
+    const int y = x - s_pre[b], group = y / A.hkv, g = y - group * A.hkv;
+    const int hi_page = pages_of(A, b, false) - A.n_recent, p0 = A.n_first + 16 * group;
+    int pg[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) pg[i] = p0 + gq + 8 * i < hi_page ? page_id(A, b, p0 + gq + 8 * i) : -1;
+    float best[2], most = 0.f, least = INFINITY, greatest = -INFINITY;
+    score_group<kJ>(A, b, g, pg, best, most);
+    const int64_t u = static_cast<int64_t>(b) * A.hkv + g;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int p = p0 + gq + 8 * i;
+      if (p >= hi_page) continue;
+      least = fminf(least, best[i]);
+      greatest = fmaxf(greatest, best[i]);
+      if (qq == 0) A.scores[u * A.max_pages + p] = best[i];
+    }
+    warp_stats(most, least, greatest);
+    if (lane == 0) A.parts[u * per_unit + group] = make_float4(most, least, greatest, 0.f);
   }
 }
 
@@ -260,18 +343,22 @@ __device__ __forceinline__ void kth_range(PickShared& S, int m, int need, int fe
     __syncthreads();
     // the bin of the need-th key, counted from the top: thread t has bins
     // [kBins - 8 (t + 1), kBins - 8 t)
-    constexpr int kPer = kBins / kThreads;
-    int own = 0;
-    const int top = kBins - kPer * tid;
-#pragma unroll
-    for (int j = 1; j <= kPer; ++j) own += S.hist[top - j];
+    static_assert(kBins == 8 * kThreads, "eight bins a thread");
+    const int first = kBins - 8 * (tid + 1);
+    const int4 u = *reinterpret_cast<const int4*>(&S.hist[first]), v = *reinterpret_cast<const int4*>(&S.hist[first + 4]);
+    const int bins[8] = {v.w, v.z, v.y, v.x, u.w, u.z, u.y, u.x};  // from the top
+    const int own = ((v.w + v.z) + (v.y + v.x)) + ((u.w + u.z) + (u.y + u.x));
     int total, before = above + block_scan(S, own, total);
     if (before < need && before + own >= need) {
-      int j = 1;
-      while (before + S.hist[top - j] < need) before += S.hist[top - j++];
-      S.bin = top - j;
-      S.above = before;
-      S.inside = S.hist[top - j];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (before < need && before + bins[j] >= need) {
+          S.bin = first + 7 - j;
+          S.above = before;
+          S.inside = bins[j];
+        }
+        before += bins[j];
+      }
     }
     __syncthreads();
     above = S.above;
@@ -288,19 +375,18 @@ __device__ __forceinline__ float key_float(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
 }
 
-// CTA 0 of the cluster: the top_k of pages 0 .. n - 1, of which [lo, hi) have scores.
-__device__ __forceinline__ void pick_pages(const SelectArgs& A, PickShared& S, int u, int b, int g, int n, int lo,
-                                           int hi) {
+// One block: the top_k of pages 0 .. n - 1, of which [lo, hi) have scores (sc, by
+// page - lo; overwritten), with the stats of `parts` shares of them in S.part.
+__device__ __forceinline__ void pick_pages(const SelectArgs& A, PickShared& S, float* sc, int parts, int u, int b, int g,
+                                           int n, int lo, int hi) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int m = hi - lo, need = A.top_k - (n - m);  // of the pages with scores
-  float* stored = A.scores + static_cast<int64_t>(u) * A.max_pages + lo;
-  float* sc = m <= kHeld ? S.scores : stored;
   int32_t* out = A.selected + static_cast<int64_t>(u) * A.top_k;
   uint32_t kth = 0xffffffffu;  // pages above this key are taken, and the first `ties` equal to it
   int ties = 0;
   if (need > 0) {
     float e = 0.f, least = INFINITY, greatest = -INFINITY;
-    for (int r = 0; r < static_cast<int>(cluster_size()); ++r) {
+    for (int r = 0; r < parts; ++r) {
       e = fmaxf(e, S.part[r][0]);
       least = fminf(least, S.part[r][1]);
       greatest = fmaxf(greatest, S.part[r][2]);
@@ -391,6 +477,12 @@ __device__ __forceinline__ void pick_pages(const SelectArgs& A, PickShared& S, i
   }
 }
 
+// A sequence of no more pages than top_k: all of them.
+__device__ __forceinline__ void all_pages(const SelectArgs& A, int u, int n) {
+  int32_t* out = A.selected + static_cast<int64_t>(u) * A.top_k;
+  for (int i = threadIdx.x; i < A.top_k; i += kThreads) out[i] = i < n ? i : -1;
+}
+
 template <int kJ>
 __global__ void __launch_bounds__(kThreads, kJ == 8 ? 1 : 2) page_select_kernel(const SelectArgs A) {
   __shared__ PickShared S;
@@ -411,42 +503,105 @@ __global__ void __launch_bounds__(kThreads, kJ == 8 ? 1 : 2) page_select_kernel(
     const int p = A.n_first + 16 * (static_cast<int>(cluster_ctarank()) * kSelWarps + warp) + (lane >> 2) + 8 * i;
     pg[i] = p < A.max_pages ? A.block_table[static_cast<int64_t>(b) * A.max_pages + p] : 0;
   }
-  const int64_t Lr = A.seqlens[b];
-  const int64_t L = Lr < 0 ? 0 : (Lr > A.capacity ? A.capacity : Lr);
-  const int n = static_cast<int>((L + A.page_size - 1) / A.page_size);
-  if (L != Lr && first && threadIdx.x == 0) record_status(A.wd, kStatusRange);
+  const int n = pages_of(A, b, first && threadIdx.x == 0);
   const int lo = A.n_first, hi = n - A.n_recent;
   cluster_wait();  // every block of the cluster has started: CTA 0's shared memory may be written
   const bool choose = n > A.top_k;  // the same for the whole cluster; then lo < hi
-  if (choose) score_pages<kJ>(A, S, u, b, g, lo, hi, pg);
-  cluster_sync_all();  // the cluster's scores are visible to CTA 0
+  if (choose) score_pages<kJ>(A, S, b, g, lo, hi, pg);
+  cluster_sync_all();  // the cluster's scores are visible to block 0
   if (!first) return;
   if (choose) {
-    pick_pages(A, S, u, b, g, n, lo, hi);
+    pick_pages(A, S, S.scores, static_cast<int>(cluster_size()), u, b, g, n, lo, hi);
   } else {
-    int32_t* out = A.selected + static_cast<int64_t>(u) * A.top_k;
-    for (int i = threadIdx.x; i < A.top_k; i += kThreads) out[i] = i < n ? i : -1;
+    all_pages(A, u, n);
   }
 }
 
-// As many CTAs per cluster as the device holds at once (two CTAs per SM): few
-// units are scored faster by many CTAs, many units better by a CTA each than
-// in turns (128 units of 1024 pages on 148 SMs: 36 us with eight, XX with two).
-template <int kJ>
-fa_status launch_width(const SelectArgs& A, const LaunchCtx& ctx) {
-  const int64_t units = static_cast<int64_t>(A.batch) * A.hkv;
-  const int64_t most = static_cast<int64_t>(device_sm_count()) * (kJ == 8 ? 1 : 2);
+// Dealt evenly: the choice of one unit.
+__global__ void __launch_bounds__(kThreads) page_pick_kernel(const SelectArgs A) {
+  __shared__ PickShared S;
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int u = blockIdx.x, b = u / A.hkv, g = u % A.hkv;
+  for (int i = threadIdx.x; i < kBins; i += kThreads) S.hist[i] = 0;
+  if (threadIdx.x == 0) S.n_between = 0;
+  griddep_wait();
+  const int n = pages_of(A, b, false);
+  if (n <= A.top_k) {
+    all_pages(A, u, n);
+    return;
+  }
+  const int lo = A.n_first, hi = n - A.n_recent, m = hi - lo, groups = (m + 15) / 16;
+  const float4* parts = A.parts + static_cast<int64_t>(u) * ((A.max_pages + 15) / 16);
+  float* stored = A.scores + static_cast<int64_t>(u) * A.max_pages + lo;
+  float* sc = m <= kHeld ? S.scores : stored;
+  if (m <= kHeld) {
+    for (int i = threadIdx.x; i < m; i += kThreads) sc[i] = __ldcg(stored + i);
+  }
+  float most = 0.f, least = INFINITY, greatest = -INFINITY;
+  for (int i = threadIdx.x; i < groups; i += kThreads) {
+    const float4 v = __ldcg(parts + i);
+    most = fmaxf(most, v.x);
+    least = fminf(least, v.y);
+    greatest = fmaxf(greatest, v.z);
+  }
+  warp_stats(most, least, greatest);
+  if (lane == 0) {
+    S.part[warp][0] = most;
+    S.part[warp][1] = least;
+    S.part[warp][2] = greatest;
+  }
+  __syncthreads();
+  pick_pages(A, S, sc, kSelWarps, u, b, g, n, lo, hi);
+}
+
+// Blocks per cluster: as many as the device holds at once (two per SM).
+int cluster_of(int64_t units) {
+  const int64_t most = static_cast<int64_t>(device_sm_count()) * 2;
   int cluster = 1;
   while (cluster < kMaxCluster && units * cluster * 2 <= most) cluster *= 2;
-  return launch_dependent(page_select_kernel<kJ>, dim3(static_cast<unsigned>(units * cluster)), kThreads, 0, cluster,
-                          ctx.stream, A);
+  return cluster;
+}
+// Whether a cluster per unit scores its pages in one round of 16 per warp.
+bool one_round(int64_t units, int max_pages) { return cluster_of(units) * kSelWarps * 16 >= max_pages; }
+
+template <int kJ>
+fa_status launch_width(const SelectArgs& all, const LaunchCtx& ctx) {
+  const int64_t units = static_cast<int64_t>(all.batch) * all.hkv;
+  if (one_round(units, all.max_pages)) {
+    const int cluster = cluster_of(units);
+    return launch_dependent(page_select_kernel<kJ>, dim3(static_cast<unsigned>(units * cluster)), kThreads, 0, cluster,
+                            ctx.stream, all);
+  }
+  const int blocks = device_sm_count() * (kJ == 8 ? 1 : 2);
+  for (int b0 = 0; b0 < all.batch; b0 += kMaxBatch) {
+    SelectArgs A = all;
+    A.batch = all.batch - b0 < kMaxBatch ? all.batch - b0 : kMaxBatch;
+    if (static_cast<int64_t>(A.batch) * A.hkv * ((A.max_pages + 15) / 16) >= (int64_t(1) << 31)) return FA_ERR_UNSUPPORTED;
+    A.q += static_cast<int64_t>(b0) * A.hq * A.d;
+    A.seqlens += b0;
+    A.block_table += static_cast<int64_t>(b0) * A.max_pages;
+    A.selected += static_cast<int64_t>(b0) * A.hkv * A.top_k;
+    A.scores += static_cast<int64_t>(b0) * A.hkv * A.max_pages;
+    A.parts += static_cast<int64_t>(b0) * A.hkv * ((A.max_pages + 15) / 16);
+    fa_status st = launch_dependent(page_score_kernel<kJ>, dim3(blocks), kThreads, 0, 0, ctx.stream, A);
+    if (st == FA_OK)
+      st = launch_dependent(page_pick_kernel, dim3(static_cast<unsigned>(A.batch * A.hkv)), kThreads, 0, 0, ctx.stream, A);
+    if (st != FA_OK) return st;
+  }
+  return FA_OK;
 }
 
 }  // namespace
 
+namespace {
+size_t parts_bytes(int64_t units, int max_pages) { return static_cast<size_t>(units) * ((max_pages + 15) / 16) * 16; }
+}  // namespace
+
 size_t page_select_workspace_bytes(int batch, int hkv, int max_pages) {
-  if (max_pages <= kHeld) return 0;
-  return (static_cast<size_t>(batch) * hkv * max_pages * sizeof(float) + 15) / 16 * 16;
+  const int64_t units = static_cast<int64_t>(batch) * hkv;
+  if (one_round(units, max_pages)) return 0;
+  return parts_bytes(units, max_pages) + static_cast<size_t>(units) * max_pages * sizeof(float);
 }
 
 fa_status launch_page_select(const fa_page_select_params& p, const fa_kv_pages& pages, const LaunchCtx& ctx) {
@@ -456,7 +611,9 @@ fa_status launch_page_select(const fa_page_select_params& p, const fa_kv_pages& 
   A.bounds = static_cast<const __nv_bfloat16*>(p.key_bounds);
   A.seqlens = p.cache_seqlens;
   A.selected = p.selected;
-  A.scores = static_cast<float*>(p.workspace);
+  A.parts = static_cast<float4*>(p.workspace);
+  A.scores = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) +
+                                      parts_bytes(static_cast<int64_t>(p.batch) * p.hkv, pages.max_pages));
   A.batch = p.batch;
   A.hq = p.hq;
   A.hkv = p.hkv;

@@ -899,8 +899,13 @@ def page_select(q: torch.Tensor, key_bounds: torch.Tensor, cache_seqlens: torch.
         selected = _operand(out, "out", dev, _INT32, shape)
     nbytes = ws = 0
     if workspace is None:
-        if max_pages > 4096:  # smaller tables need none
-            nbytes = lib.fa_page_select_workspace_size(batch, hkv, max_pages)
+        if max_pages > 128:  # shorter tables need none
+            if _current_device() == dev:
+                nbytes = lib.fa_page_select_workspace_size(batch, hkv, max_pages)
+            else:
+                with torch.cuda.device(dev):  # its count of SMs enters the size
+                    nbytes = lib.fa_page_select_workspace_size(batch, hkv, max_pages)
+        if nbytes:
             workspace = _new(q, nbytes, torch.uint8, stream)
             ws = workspace.data_ptr()
     else:

@@ -520,7 +520,7 @@ FA_API fa_status fa_kv_read_paged(const fa_kv_read_params *p, const fa_kv_pages 
  *             numbers, ascending, then -1 where n_b < top_k
  *   workspace device, >= fa_page_select_workspace_size() bytes, 16-byte
  *             aligned, contents need no initialisation; that size is 0 (and
- *             the workspace may be NULL) for tables of up to 4096 pages
+ *             the workspace may be NULL) for short tables
  * Bounds or queries that are not finite give an unspecified choice (of pages
  * of the sequence).  A page id outside the pool is scored as page 0 and
  * reported as FA_ERR_INVALID.  head_dim a multiple of 16 up to 256; any hq /
@@ -537,6 +537,7 @@ typedef struct {
     size_t workspace_bytes;
 } fa_page_select_params;
 
+/* (the count of SMs of the current device enters it) */
 FA_API size_t fa_page_select_workspace_size(int32_t batch, int32_t hkv, int32_t max_pages);
 FA_API fa_status fa_page_select(const fa_page_select_params *p, const fa_kv_pages *pages, fa_stream_t stream);
 

@@ -135,6 +135,8 @@ SELECT_CASES = [
     ([16000, 12000], 2, 1, 256, 32, 350, 1, 1),
     ([25000], 1, 1, 96, 96, 250, 1, 1),
     ([33000], 4, 1, 32, 32, 1000, 1, 1),
+    # many sequences, one of them long: pages dealt evenly to the device, then a block per sequence and KV head
+    ([9700] + [(977 * i) % 1500 for i in range(39)], 4, 2, 64, 32, 9, 1, 2),
 ]
 
 

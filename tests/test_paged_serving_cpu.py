@@ -122,7 +122,8 @@ def test_page_select_refusals(fa):
     assert call(head_dim=320) == fa.FA_ERR_UNSUPPORTED
     assert call(batch=0, q=None) == fa.FA_OK
     assert fa.lib.fa_page_select_workspace_size(0, 1, 1) == 0
-    assert fa.lib.fa_page_select_workspace_size(4, 8, 4096) == 0  # scores in shared memory
+    assert fa.lib.fa_page_select_workspace_size(4, 8, 1024) == 0  # one kernel
+    assert fa.lib.fa_page_select_workspace_size(1000, 8, 128) == 0
     assert fa.lib.fa_page_select_workspace_size(4, 8, 5000) >= 4 * 4 * 8 * 5000
 
 
