@@ -1052,8 +1052,8 @@ int64_t most_tiles(const PageArgs& A) {
   if (kSel) {
     const int64_t chosen = static_cast<int64_t>(A.top_k) * A.page_size;
     keys = chosen < keys ? chosen : keys;
-  } else if (A.window > 0 && A.window + kKeys < keys) {
-    keys = A.window + kKeys;  // the window may start inside a tile
+  } else if (A.window > 0 && static_cast<int64_t>(A.window) + kKeys < keys) {
+    keys = static_cast<int64_t>(A.window) + kKeys;  // the window may start inside a tile
   }
   return (keys + kKeys - 1) / kKeys;
 }
@@ -1063,7 +1063,11 @@ int64_t most_tiles(const PageArgs& A) {
 // second kernel's merge, is faster.  Counted in tiles one after the other: a
 // cluster's warps take seg_tiles / (4 c) each, in turns where the clusters do
 // not fit at once; an even split the device's share of all tiles, and about
-// four tiles' time for the records, the second launch and its reads.  (XX)
+// four tiles' time for the records, the second launch and its reads.  (One
+// sequence of 257 keys: 8.3 us clustered, 10.3 us split; 128 pairs of 2048
+// chosen 4-bit keys: 16.5 and 23 us.  Long caches the other way round: one of
+// 131071 keys has 8 clusters of 32 warps for a device of 1184.)  Powers of two
+// only: clusters of three made the selection before them wait (43 -> 48 us).
 template <int D, int kKind>
 int cluster_of(int64_t segs, int64_t seg_tiles) {
   const int64_t resident = static_cast<int64_t>(device_sm_count()) * Tile<D, kKind>::kCtas;
@@ -1130,9 +1134,13 @@ fa_status launch_typed(const fa_decode_params& p, const fa_kv_pages& pg, PageArg
     A.n_workers = most < workers ? static_cast<int>((most + kWarps - 1) / kWarps * kWarps) : workers;
     A.rec_o = reinterpret_cast<float*>(ws + plan);
     A.rec_ml = A.rec_o + (static_cast<size_t>(A.batch) * A.hkv + A.n_workers) * A.group * D;
-    st = launch_dependent(kern, dim3(A.n_workers / kWarps), kThreads, TL::kSmem + (A.batch + 1) * 4, 0, ctx.stream, maps.k,
-                          maps.v, maps.k32, maps.v32, A);
-    if (st != FA_OK) return st;
+    // an ordinary launch: blocks that came while an earlier kernel still held
+    // its places would lie unevenly on the SMs (44 -> 51 us with one sequence
+    // of 131071 keys, called back to back)
+    note_variant(reinterpret_cast<const void*>(kern));
+    kern<<<A.n_workers / kWarps, kThreads, TL::kSmem + (A.batch + 1) * 4, ctx.stream>>>(maps.k, maps.v, maps.k32, maps.v32,
+                                                                                        A);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
     st = launch_dependent(merge, dim3(static_cast<unsigned>(A.batch * A.hkv * A.group)), kMergeThreads, 0, 0, ctx.stream, A);
     if (st != FA_OK) return st;
   }

@@ -17,7 +17,7 @@ struct LaunchCtx {
 // Launch with programmatic stream serialisation: the kernel may start while the
 // one before it in the stream still runs (if that one allows it,
 // griddep_launch_dependents), so it calls griddep_wait() in every block before
-// it touches global memory.  cluster > 1: that many blocks per cluster.
+// it touches global memory.  cluster > 0: that many blocks per cluster.
 void note_variant(const void* kernel_fn);
 template <typename... P, typename... A>
 fa_status launch_dependent(void (*kern)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream,

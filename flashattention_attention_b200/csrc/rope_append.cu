@@ -539,13 +539,13 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendArgs A)
     }
     --part;
   }
-  if (A.seqlens != nullptr && blockIdx.x == 0 && part == 0) {
+  if (blockIdx.x == 0 && part == 0) {  // offsets and lengths, once
     for (int b = threadIdx.x; b < A.batch; b += kThreads) {
       const int64_t c0 = A.cu != nullptr ? A.cu[b] : b, c1 = A.cu != nullptr ? A.cu[b + 1] : b + 1;
       const int64_t end = static_cast<int64_t>(A.cur_pos[b]) + (c1 - c0);
       if (c0 < 0 || c1 < c0 || c1 > A.total || A.cur_pos[b] < 0 || end > A.pool.capacity) {
         record_status(A.wd, kStatusRange);
-      } else {
+      } else if (A.seqlens != nullptr) {
         A.seqlens[b] = static_cast<int32_t>(end);
       }
     }
@@ -666,7 +666,7 @@ fa_status launch_append_typed(AppendArgs& A, const LaunchCtx& ctx) {
   A.part_rows = rows_per_item(A.total, A.token_rows, kGroups);
   const int parts = (A.token_rows + A.part_rows - 1) / A.part_rows;
   A.window = A.total <= 4 * device_sm_count() ? 1 : 8;
-  int blocks = A.total / kGroups + 1;  // at least one, for cache_seqlens alone
+  int blocks = A.total / kGroups + 1;  // at least one, for the lengths alone
   const int page_blocks = A.bounds != nullptr ? A.total / A.window + 1 : 0;
   if (blocks < page_blocks) blocks = page_blocks;
   if (parts >= 65535) return FA_ERR_UNSUPPORTED;
@@ -706,7 +706,6 @@ fa_status launch_read(ReadArgs& A, const LaunchCtx& ctx) {
 }  // namespace
 
 fa_status launch_kv_append_rope(const fa_kv_append_rope_params& p, const fa_kv_pages& pages, const LaunchCtx& ctx) {
-  if (p.total == 0 && p.cache_seqlens == nullptr) return FA_OK;
   AppendArgs A;
   A.k_new = p.k_new;
   A.v_new = p.v_new;

@@ -429,12 +429,14 @@ FA_API fa_status fa_kv_append_paged(const fa_kv_append_params *p, const fa_kv_pa
  * A token whose slot is outside [0, capacity) (capacity = max_pages *
  * page_size), at or past rope_rows, or in a page outside [0, num_pages) is
  * skipped (its q_out row too) and reported by fa_check_device_error as
- * FA_ERR_INVALID; so is a whole sequence whose cu_seqlens range is not
- * ascending within [0, total].  Two sequences of one call must not append to
- * the same page.
+ * FA_ERR_INVALID; the cache_seqlens entry of a sequence that leaves [0,
+ * capacity] is not written.  cu_seqlens that do not ascend within [0, total]
+ * are reported too, and which of their tokens go where is unspecified (always
+ * inside the pools).  Two sequences of one call must not append to the same
+ * page.
  * Requirements: head_dim a multiple of 16 up to 256; every row, pool, table
  * and the strides (in bytes) 16-byte aligned; num_pages * hkv * page_size <
- * 2^31.  total = 0 enqueues nothing but the cache_seqlens update.
+ * 2^31.  total = 0 only sets cache_seqlens.
  */
 typedef struct {
     const void *k_new;
@@ -482,8 +484,9 @@ FA_API fa_status fa_rope_table(int32_t rows, int32_t rot_dim, double base, float
  *             were
  *   start     optional device int32 [batch] (NULL: 0 for all)
  * The values: bf16 as stored; code * scale (FA_I8) and code * step + offset
- * (FA_I4), each operation rounded to fp32, then rounded to out_dtype.  A slot
- * outside [0, capacity) or in a page outside the pool leaves its row as it
+ * (FA_I4), each operation rounded to fp32, then rounded to out_dtype.
+ * cu_seqlens ascend from 0 to at most total (other values: unspecified rows of
+ * the outputs are written).  A slot outside [0, capacity) or in a page outside the pool leaves its row as it
  * was and is reported by fa_check_device_error as FA_ERR_INVALID.
  * Requirements as fa_kv_append_rope_paged.
  */

@@ -71,6 +71,7 @@ INT4_CASES = [
     ([25001, 64], 3, 1, 96, 32, 0),
     ([20000, 9001], 8, 1, 256, 32, 0),
     ([30000, 20000], 4, 2, 128, 64, 15000),
+    ([300, 64], 4, 2, 128, 64, 2 ** 31 - 1),     # a window past every key
 ]
 
 

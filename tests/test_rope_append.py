@@ -230,6 +230,55 @@ def test_padding_and_bad_tokens_write_nothing():
     assert fa.check_device_error() == fa.FA_OK
 
 
+def test_empty_calls():
+    """No sequence, or sequences without a new token: nothing moves but the lengths."""
+    fa = _fa()
+    c = plain.Cache(304, "int4", [64, 30], 2, 64, 32, poison=False).cuda()
+    before = [getattr(c, n).clone() for n in ("kp_", "vp_", "ks_", "vs_", "bounds_")]
+    kw = dict(k_scales=c.ks_, v_scales=c.vs_)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    none = torch.empty((0, 2, 64), dtype=torch.bfloat16, device="cuda")
+    lens = i32(-1, -1)
+    q = fa.kv_append_rope_paged(none, none, c.kp_, c.vp_, i32(5, 64), c.table_, q=none, key_bounds=c.bounds_,
+                                rope_table=fa.rope_table(64, 64).cuda(), cu_seqlens=i32(0, 0, 0), cache_seqlens=lens, **kw)
+    assert q.shape == (2, 0, 64) and lens.tolist() == [5, 64]
+    no = torch.empty((0,), dtype=torch.int32, device="cuda")
+    no_table = c.table_[:0].contiguous()
+    assert fa.kv_append_rope_paged(none, none, c.kp_, c.vp_, no, no_table, q=none, **kw).shape == (0, 64)
+    k, v = fa.kv_read_paged(c.kp_, c.vp_, i32(0, 0, 0), c.table_, total=0, **kw)
+    assert k.shape == v.shape == (2, 0, 64)
+    nq = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
+    assert fa.attention_decode_paged(nq, c.kp_, c.vp_, no, no_table, hq=4, hkv=2, **kw).shape == (0, 64)
+    sel = fa.page_select(nq, c.bounds_, no, no_table, hq=4, hkv=2, page_size=32, top_k=3)
+    assert sel.shape == (0, 2, 3)
+    assert fa.attention_decode_selected(nq, c.kp_, c.vp_, no, no_table, sel, hq=4, hkv=2, **kw).shape == (0, 64)
+    assert fa.check_device_error() == fa.FA_OK
+    for n, b in zip(("kp_", "vp_", "ks_", "vs_", "bounds_"), before):
+        assert torch.equal(getattr(c, n), b)
+
+
+@pytest.mark.parametrize("x_dtype", [torch.bfloat16, torch.float32])
+def test_many_tokens_and_heads(x_dtype):
+    """More tokens than a block per token would take, decode steps between prompts, heads beyond one block's groups."""
+    fa = _fa()
+    cur = [0, 61, 7, 0, 130] + [3 * i for i in range(60)]
+    new = [700, 1, 90, 0, 33] + [1] * 60
+    hq, hkv, d, page = 5, 40, 32, 32
+    c = plain.Cache(305, "int4", [a + b for a, b in zip(cur, new)], hkv, d, page, poison=False).cuda()
+    total = sum(new)
+    qkv, q, k, v = _tokens(305, total, hq, hkv, d, x_dtype)
+    table = plain.rope_table(800, d)
+    q_ref, lens = plain.append(c, plain.f32(k), plain.f32(v), plain.f32(q), cur, new, table, False)
+    qg, kg, vg = _cuda_slices(qkv, hq, hkv, d)
+    out = fa.kv_append_rope_paged(kg, vg, c.kp_, c.vp_, torch.tensor(cur, dtype=torch.int32).cuda(), c.table_, q=qg,
+                                  rope_table=torch.from_numpy(table).cuda(), k_scales=c.ks_, v_scales=c.vs_,
+                                  key_bounds=c.bounds_,
+                                  cu_seqlens=torch.tensor([0] + list(np.cumsum(new)), dtype=torch.int32).cuda())
+    assert fa.check_device_error() == fa.FA_OK
+    assert torch.equal(out.cpu(), q_ref.transpose(0, 1))
+    _same_cache(c, "int4")
+
+
 @pytest.mark.parametrize("kind", ["bf16", "int8", "int4"])
 @pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
 def test_read_back(kind, out_dtype):
