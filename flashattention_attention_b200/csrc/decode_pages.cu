@@ -943,6 +943,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_pages_merge_kernel(const
   }
   const int n = range & 0xffffu;
   if (n == 1) return;  // stored by its worker
+  if (n + static_cast<int>(range >> 16) > A.n_workers) return;  // never written: its worker gave up waiting (reported)
   const int64_t rec0 = static_cast<int64_t>(seg) + (range >> 16);
   float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll

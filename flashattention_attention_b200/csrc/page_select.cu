@@ -22,7 +22,7 @@
 // the choosing block's shared memory.  Else the pages of all pairs are dealt
 // evenly to the device's warps and a second kernel chooses, since a pair's own
 // cluster would go over its pages in rounds that each wait for memory (128
-// pairs of up to 1021 pages: 22.6 us in clusters of two, XX us dealt evenly).
+// pairs of up to 1021 pages: 22.6 us in clusters of two, 21.7 us dealt evenly).
 // One pass over the bounds, 4 d bytes a page; the choice works on 4 bytes a page.
 #include "decode_mma.cuh"
 #include "internal.h"
@@ -562,7 +562,9 @@ int cluster_of(int64_t units) {
   while (cluster < kMaxCluster && units * cluster * 2 <= most) cluster *= 2;
   return cluster;
 }
-// Whether a cluster per unit scores its pages in one round of 16 per warp.
+// Whether a cluster per unit scores its pages in one round of 16 per warp (with
+// the attention that follows, one sequence of 8 KV heads: 17.2 us, dealt evenly
+// 20.6; 4 sequences of up to 8192 bf16 keys: 29.4 and 34.9).
 bool one_round(int64_t units, int max_pages) { return cluster_of(units) * kSelWarps * 16 >= max_pages; }
 
 template <int kJ>

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -126,19 +127,19 @@ class PageSelectParams(ctypes.Structure):
 
 
 lib.fa_kv_append_rope_paged.restype = ctypes.c_int
-lib.fa_kv_append_rope_paged.argtypes = [ctypes.POINTER(KvAppendRopeParams), ctypes.POINTER(KvPages), _P]
+lib.fa_kv_append_rope_paged.argtypes = [_P, _P, _P]
 lib.fa_rope_table.restype = ctypes.c_int
 lib.fa_rope_table.argtypes = [_I32, _I32, ctypes.c_double, _P]
 lib.fa_kv_read_paged.restype = ctypes.c_int
-lib.fa_kv_read_paged.argtypes = [ctypes.POINTER(KvReadParams), ctypes.POINTER(KvPages), _P]
+lib.fa_kv_read_paged.argtypes = [_P, _P, _P]
 lib.fa_page_select_workspace_size.restype = ctypes.c_size_t
 lib.fa_page_select_workspace_size.argtypes = [_I32] * 3
 lib.fa_page_select.restype = ctypes.c_int
-lib.fa_page_select.argtypes = [ctypes.POINTER(PageSelectParams), ctypes.POINTER(KvPages), _P]
+lib.fa_page_select.argtypes = [_P, _P, _P]
 lib.fa_decode_pages_workspace_size.restype = ctypes.c_size_t
-lib.fa_decode_pages_workspace_size.argtypes = [ctypes.POINTER(DecodeParams), ctypes.POINTER(KvPages), _I32]
+lib.fa_decode_pages_workspace_size.argtypes = [_P, _P, _I32]
 lib.fa_attention_decode_selected.restype = ctypes.c_int
-lib.fa_attention_decode_selected.argtypes = [ctypes.POINTER(DecodeParams), ctypes.POINTER(KvPages), _P, _I32, _P]
+lib.fa_attention_decode_selected.argtypes = [_P, _P, _P, _I32, _P]
 lib.fa_compress_kv.restype = ctypes.c_int
 lib.fa_compress_kv.argtypes = [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int32,
                                ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
@@ -158,7 +159,7 @@ lib.fa_attention_merge.argtypes = [ctypes.POINTER(MergeParams), ctypes.c_void_p]
 lib.fa_attention_fwd_paged.restype = ctypes.c_int
 lib.fa_attention_fwd_paged.argtypes = [ctypes.POINTER(FwdParams), ctypes.POINTER(KvPages), ctypes.c_void_p]
 lib.fa_attention_decode_paged.restype = ctypes.c_int
-lib.fa_attention_decode_paged.argtypes = [ctypes.POINTER(DecodeParams), ctypes.POINTER(KvPages), ctypes.c_void_p]
+lib.fa_attention_decode_paged.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
 lib.fa_kv_append.restype = ctypes.c_int
 lib.fa_kv_append.argtypes = [ctypes.POINTER(KvAppendParams), ctypes.c_void_p]
 lib.fa_kv_append_paged.restype = ctypes.c_int
@@ -631,8 +632,21 @@ def _append_params(k_new, v_new, k_cache, v_cache, cur_pos, hkv, k_scales, v_sca
 
 _CACHE_DT = {torch.bfloat16: FA_BF16, torch.int8: FA_I8, torch.uint8: FA_I4}
 _BF16, _F32, _INT32 = torch.bfloat16, torch.float32, torch.int32
-_NO_EPILOGUE = (EpiOp * FA_MAX_EPILOGUE)()
 _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+def _packer(cls):
+    """cls(*fields) as bytes with the structure's layout: a quarter of the cost of
+    making the structure (an array field is given as bytes)."""
+    codes = {ctypes.c_void_p: "P", ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_size_t: "N", ctypes.c_float: "f"}
+    s = struct.Struct("@" + "".join(codes.get(c) or f"{ctypes.sizeof(c)}s" for _, c in cls._fields_) + "0P")
+    assert s.size == ctypes.sizeof(cls)
+    return s.pack
+
+
+_pack_append, _pack_read, _pack_select = _packer(KvAppendRopeParams), _packer(KvReadParams), _packer(PageSelectParams)
+_pack_decode, _pack_pages = _packer(DecodeParams), _packer(KvPages)
+_NO_EPILOGUE = bytes(ctypes.sizeof(EpiOp) * FA_MAX_EPILOGUE)
 
 
 def _on_device(dev: int, stream, what: str, fn, *args) -> None:
@@ -687,7 +701,7 @@ def _operand(t, name: str, dev: int, dtype, shape) -> int:
 
 
 def _pool_operands(k_pages, v_pages, k_scales, v_scales, block_table, batch: int, hkv: int, d: int, dev: int):
-    """(cache dtype, KvPages, pool and scale addresses) of page pools; ValueError where they do not fit together."""
+    """(cache dtype, packed KvPages, pool and scale addresses) of page pools; ValueError where they do not fit together."""
     dtype, shape, table_shape = k_pages.dtype, k_pages.shape, block_table.shape
     kind = _CACHE_DT.get(dtype)
     if kind is None:
@@ -703,7 +717,7 @@ def _pool_operands(k_pages, v_pages, k_scales, v_scales, block_table, batch: int
         pool = (num_pages, hkv, page_size, want)
         _refuse(dev, (k_pages, "k_pages", dtype, pool), (v_pages, "v_pages", dtype, pool),
                 (block_table, "block_table", _INT32, (batch, table_shape[1])))
-    pages = KvPages(block_table.data_ptr(), table_shape[1], page_size, num_pages)
+    pages = _pack_pages(block_table.data_ptr(), table_shape[1], page_size, num_pages)
     if kind == FA_BF16:
         if k_scales is not None or v_scales is not None:
             raise ValueError("a bfloat16 cache has no scales")
@@ -785,7 +799,7 @@ def kv_append_rope_paged(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torc
     kn, kts, khs = _rows_operand(k_new, "k_new", dev, xt, rows)
     vn, vts, vhs = _rows_operand(v_new, "v_new", dev, xt, rows)
     kind, pg, kp, vp, ks, vs = _pool_operands(k_pages, v_pages, k_scales, v_scales, block_table, batch, hkv, d, dev)
-    bounds = _operand(key_bounds, "key_bounds", dev, _BF16, (pg.num_pages, hkv, 2, d))
+    bounds = _operand(key_bounds, "key_bounds", dev, _BF16, (k_pages.shape[0], hkv, 2, d))
     pos = _operand(cur_pos, "cur_pos", dev, _INT32, pos_shape)
     cu = _operand(cu_seqlens, "cu_seqlens", dev, _INT32, (batch + 1,))
     lens = _operand(cache_seqlens, "cache_seqlens", dev, _INT32, pos_shape)
@@ -815,7 +829,7 @@ def kv_append_rope_paged(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torc
             qo = q_out.data_ptr()
         else:
             qo = _operand(q_out, "q_out", dev, _BF16, out_shape)
-    p = KvAppendRopeParams(kn, vn, qp, qo, kts, khs, vts, vhs, qts, qhs, ots, ohs, table, kp, vp, ks, vs, bounds, cu, pos,
+    p = _pack_append(kn, vn, qp, qo, kts, khs, vts, vhs, qts, qhs, ots, ohs, table, kp, vp, ks, vs, bounds, cu, pos,
                            lens, FA_BF16 if xt is _BF16 else FA_F32, kind, batch, total, hq, hkv, d, rot,
                            1 if interleaved else 0, table_rows)
     _on_device(dev, stream, "fa_kv_append_rope_paged", lib.fa_kv_append_rope_paged, p, pg)
@@ -840,13 +854,17 @@ def kv_read_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, cu_seqlens: torc
     shape = (hkv, _int(total, "total"), d)
     if k_out is None:
         k_out = _new(k_pages, shape, out_dtype, stream)
+        ko = k_out.data_ptr()
+    else:
+        ko = _operand(k_out, "k_out", dev, out_dtype, shape)
     if v_out is None:
-        v_out = _new(k_pages, shape, out_dtype, stream)
-    p = KvReadParams(kp, vp, ks, vs, _operand(k_out, "k_out", dev, out_dtype, shape),
-                     _operand(v_out, "v_out", dev, out_dtype, shape),
-                     _operand(cu_seqlens, "cu_seqlens", dev, _INT32, (batch + 1,)),
-                     _operand(start, "start", dev, _INT32, (batch,)), kind,
-                     FA_BF16 if out_dtype is _BF16 else FA_F32, batch, shape[1], hkv, d)
+        v_out = torch.empty_like(k_out) if stream is None else _new(k_pages, shape, out_dtype, stream)
+        vo = v_out.data_ptr()
+    else:
+        vo = _operand(v_out, "v_out", dev, out_dtype, shape)
+    p = _pack_read(kp, vp, ks, vs, ko, vo, _operand(cu_seqlens, "cu_seqlens", dev, _INT32, (batch + 1,)),
+                   _operand(start, "start", dev, _INT32, (batch,)), kind, FA_BF16 if out_dtype is _BF16 else FA_F32,
+                   batch, shape[1], hkv, d)
     _on_device(dev, stream, "fa_kv_read_paged", lib.fa_kv_read_paged, p, pg)
     return k_out, v_out
 
@@ -910,10 +928,10 @@ def page_select(q: torch.Tensor, key_bounds: torch.Tensor, cache_seqlens: torch.
             ws = workspace.data_ptr()
     else:
         nbytes, ws = workspace.numel() * workspace.element_size(), _workspace(workspace, dev)
-    p = PageSelectParams(qp, bounds, lens, selected, batch, hq, hkv, d, top_k, _int(n_first, "n_first"),
-                         _int(n_recent, "n_recent"), ws, nbytes)
+    p = _pack_select(qp, bounds, lens, selected, batch, hq, hkv, d, top_k, _int(n_first, "n_first"),
+                     _int(n_recent, "n_recent"), ws, nbytes)
     _on_device(dev, stream, "fa_page_select", lib.fa_page_select, p,
-               KvPages(table, max_pages, _int(page_size, "page_size", 1), num_pages))
+               _pack_pages(table, max_pages, _int(page_size, "page_size", 1), num_pages))
     return out
 
 
@@ -934,30 +952,33 @@ def _decode_pages(q, k_pages, v_pages, cache_seqlens, block_table, selected, hq,
     dev = _cuda_device(q, "q")
     batch, d, qp, lens = _decode_queries(q, cache_seqlens, hq, hkv, dev)
     kind, pg, kp, vp, ks, vs = _pool_operands(k_pages, v_pages, k_scales, v_scales, block_table, batch, hkv, d, dev)
-    capacity = pg.max_pages * pg.page_size
+    capacity = block_table.shape[1] * k_pages.shape[2]
     if out is None:
         out = torch.empty_like(q) if stream is None else _new(q, q.shape, _BF16, stream)
         op = out.data_ptr()
     else:
         op = _operand(out, "out", dev, _BF16, q.shape)
-    nbytes = ws = 0
-    if workspace is not None:
-        nbytes, ws = workspace.numel() * workspace.element_size(), _workspace(workspace, dev)
-    p = DecodeParams(qp, kp, vp, ks, vs, lens, op, kind, batch, hq, hkv, d, capacity, _int(max_seqlen, "max_seqlen"),
-                     _int(window, "window") if window > 0 else 0, 1.0 / math.sqrt(d) if scale is None else float(scale),
-                     0, 0, _NO_EPILOGUE, ws, nbytes)
+    n_epilogue, ops = 0, _NO_EPILOGUE
     if epilogue:
-        p.n_epilogue = _fill_epilogue(p.epilogue, epilogue)
+        array = (EpiOp * FA_MAX_EPILOGUE)()
+        n_epilogue = _fill_epilogue(array, epilogue)
+        ops = bytes(array)
+    fields = (qp, kp, vp, ks, vs, lens, op, kind, batch, hq, hkv, d, _int(capacity, "max_pages * page_size"),
+              _int(max_seqlen, "max_seqlen"), _int(window, "window") if window > 0 else 0,
+              1.0 / math.sqrt(d) if scale is None else float(scale), 0, n_epilogue, ops)
     if selected is None:
-        top_k, what, call = 0, "fa_attention_decode_paged", (lib.fa_attention_decode_paged, p, pg)
+        top_k, what, fn, more = 0, "fa_attention_decode_paged", lib.fa_attention_decode_paged, ()
     else:
         shape = selected.shape
         if len(shape) != 3 or shape[0] != batch or shape[1] != hkv:
             raise ValueError(f"selected must be [{batch}, {hkv}, top_k]; got {tuple(shape)}")
-        top_k, what = shape[2], "fa_attention_decode_selected"
-        call = (lib.fa_attention_decode_selected, p, pg, _operand(selected, "selected", dev, _INT32, shape), top_k)
-    if workspace is None:
+        top_k, what, fn = shape[2], "fa_attention_decode_selected", lib.fa_attention_decode_selected
+        more = (_operand(selected, "selected", dev, _INT32, shape), top_k)
+    if workspace is not None:
+        p = _pack_decode(*fields, _workspace(workspace, dev), workspace.numel() * workspace.element_size())
+    else:
         # only problems too long for one kernel need a workspace (the count of SMs decides)
+        p = _pack_decode(*fields, 0, 0)
         if _current_device() == dev:
             nbytes = lib.fa_decode_pages_workspace_size(p, pg, top_k)
         else:
@@ -965,8 +986,8 @@ def _decode_pages(q, k_pages, v_pages, cache_seqlens, block_table, selected, hq,
                 nbytes = lib.fa_decode_pages_workspace_size(p, pg, top_k)
         if nbytes:
             workspace = _new(q, nbytes, torch.uint8, stream)
-            p.workspace, p.workspace_bytes = workspace.data_ptr(), nbytes
-    _on_device(dev, stream, what, *call)
+            p = _pack_decode(*fields, workspace.data_ptr(), nbytes)
+    _on_device(dev, stream, what, fn, p, pg, *more)
     return out
 
 

@@ -138,15 +138,20 @@ def attend(cache, q, hq, keys_of, scale, epilogue=()):
 
     The tolerance counts the roundings between the cached values and the bf16
     result.  (1) The result: half a bf16 step, 2^-8 |out|.  (2) The weights,
-    rounded before the second product: to bf16 (bf16 cache, 2^-8) or fp16
-    (2^-11, and 2^-25 of the largest weight below fp16's normal range) -- at
-    most that share of the largest |v| (after fp16: of code * scale, or of
-    (code - 8) * step, at most 8 steps).  (3) The logits: sums of d products
-    in fp32, whose error is at most (d + 8) 2^-23 of the sum of the absolute
-    terms (for 4 bits: of (code - 8) step and of offset + 8 step apart); an
+    rounded before the second product: to two bf16 terms (bf16 cache: the
+    second holds what the first left, to half a step, 2^-8 2^-8) or to fp16
+    (2^-11, and 2^-25 of the largest weight for each key below fp16's normal
+    range) -- at most that share of the largest |v|, for 4 bits of the largest
+    |code * step|, 15 steps (the offsets' part stays in fp32).  (3) The logits:
+    sums of d products in fp32, whose error is at most (d + 8) 2^-23 of the sum
+    of the absolute terms, for 4 bits step |q| . code + |offset| sum |q| <=
+    sum |q| (15 step + |offset|), since code and offset are summed apart; an
     error e of every logit moves a weight by at most the factor exp(2e), and
     the result by twice that of the largest |v|.  (4) 2^-20 of the largest |v|
-    for the exponentials, sums and merges in fp32."""
+    for the exponentials, the weights' sum and merges in fp32, and the second
+    product's sums: one addition per 16 keys (two for a bf16 cache's two
+    terms), each losing at most 2^-22 of a partial sum, which is at most the
+    largest |v|, or |code * step|, times the weights' sum."""
     B, d = q.shape[0], q.shape[-1]
     group = hq // cache.hkv
     out, tol = np.zeros((B, hq, d)), np.zeros((B, hq, d))
@@ -165,18 +170,20 @@ def attend(cache, q, hq, keys_of, scale, epilogue=()):
             vmax = np.abs(v).max(0)
             terms = (np.abs(q[b, hs]) @ np.abs(k).T).max()
             wide = vmax
-            weights = 2.0 ** -8 if cache.kind == "bf16" else 2.0 ** -11 + 2.0 ** -25 * len(keys)
+            weights = 2.0 ** -16 if cache.kind == "bf16" else 2.0 ** -11 + 2.0 ** -25 * len(keys)
+            sums = (len(keys) / 8 + 2) * 2.0 ** -22
             if cache.kind == "int4":
                 p, o = cache.table[b].numpy()[np.asarray(keys) // cache.page], np.asarray(keys) % cache.page
                 step_k, off_k = (cache.ks[p, g, o].double().numpy()[:, i] for i in (0, 1))
-                terms = (np.abs(q[b, hs]).sum(-1).max() * (8 * step_k + np.abs(off_k + 8 * step_k)).max())
-                wide = np.full(d, 8 * cache.vs[p, g, o].double().numpy()[:, 0].max())
+                terms = (np.abs(q[b, hs]).sum(-1).max() * (15 * step_k + np.abs(off_k)).max())
+                wide = np.full(d, 15 * cache.vs[p, g, o].double().numpy()[:, 0].max())
             logit = (d + 8) * 2.0 ** -23 * terms * scale
             gain = np.prod([v_ for op, v_ in epilogue if op == "mul"]) if epilogue else 1.0
             y = epilogue_of(y, epilogue)
             out[b, hs] = y
             tol[b, hs] = (2.0 ** -8 * np.abs(y)
-                          + abs(gain) * (weights * wide + 2 * (math.exp(2 * logit) - 1) * vmax + 2.0 ** -20 * vmax))
+                          + abs(gain) * ((weights + sums) * wide + 2 * (math.exp(2 * logit) - 1) * vmax
+                                         + 2.0 ** -20 * vmax))
     return out, tol
 
 
