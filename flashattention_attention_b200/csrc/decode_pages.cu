@@ -1,11 +1,12 @@
 // decode_pages.cu -- single-query attention over page pools: every page of a
 // 4-bit cache, or the chosen pages of a bf16, int8 or 4-bit one.
 //
-// The tiles (64 keys of a 4-bit cache, else 32) of all (sequence, KV head)
-// segments are laid end to end and a grid of P warps ("workers") takes equal
-// contiguous ranges of them.  A
-// worker looks up its next 32 tiles at a time, one lane a tile (page list,
-// block table), and keeps a ring of tiles in flight in its own shared memory.
+// The tiles (64 keys of a 4-bit cache up to D = 128, else 32) of all (sequence,
+// KV head) segments are laid end to end and a grid of P warps ("workers") takes
+// equal contiguous ranges of them.  A worker looks up its next 32 tiles at a
+// time, one lane a tile (page list, block table), and keeps a ring of tiles in
+// flight in its own shared memory.  Where that is faster, a cluster serves each
+// segment instead (see cluster_of).
 // Per tile, keys on the M side of mma.sync m16n8k16 and heads on N:
 //   S^T[keys x 8 heads] = K[keys x d] . Q^T,  online softmax per head in fp32,
 //   O^T[d x 8 heads] += V^T[d x keys] . P'
@@ -27,6 +28,14 @@
 // whatever the values are, and the tensor core's additions to a large number
 // lose bits to one side: every 16 tiles the part all channels share is moved
 // from the accumulators into one number per head.
+//
+// A 4-bit row of 128 is 72 bytes and as much arithmetic as 256 bytes of bf16, so
+// the kernel is bound by its instructions and their latencies: about 430 per 32
+// keys and 8 head columns (128 of them the ANDs), ALU pipe 54 % and issue slots
+// 49 % busy at the 12 warps an SM that 150 registers and 72 KB a CTA leave room
+// for.  16 sequences, 274,568 keys, 32 query heads on 8: 66 us, 4.8 TB/s (73 %
+// of a plain copy); one of 131,071 keys, 64 heads on 8: 43 us, 3.5 TB/s (its
+// records leave room for eight warps an SM; twelve, with larger ones: 43 us).
 #include <atomic>
 #include <type_traits>
 
@@ -90,8 +99,10 @@ struct Tile {
   using G = Geom<D, kKind == FA_BF16>;
   static constexpr bool kI4 = kKind == FA_I4;
   // A tile is one or two runs of 32 keys, each within one page.  A 4-bit run is
-  // small, and what a tile costs beside its keys' arithmetic is spread over two.
-  static constexpr int kRuns = kI4 ? 2 : 1;
+  // small, and what a tile costs beside its keys' arithmetic is spread over two
+  // -- but not at D = 256, where two stages of 64 keys leave room for one CTA an
+  // SM (12 sequences of up to 1056 keys in 8 heads: 18.4 us, with 32 keys 16.1).
+  static constexpr int kRuns = kI4 && D < 256 ? 2 : 1;
   static constexpr int kKeys = kTile * kRuns;
   static constexpr int kBytes = kI4 ? kKeys * D / 2 : G::kTileBytes;  // of K, and of V
   static constexpr int kScaleBytes = kI4 ? kKeys * 8 : kKind == FA_I8 ? kTile * 4 : 0;
@@ -313,20 +324,20 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
     uint8_t* st = stage_ptr(s);
     if constexpr (kI4) {
       // the runs of one page are copied as one
-      const bool one = row[1] == row[0] + kTile && row[0] >= 0;
-      const int n = one ? 2 : (row[0] >= 0) + (row[1] >= 0);
+      const bool one = TL::kRuns == 2 && row[TL::kRuns - 1] == row[0] + kTile && row[0] >= 0;
+      const int n = one ? 2 : (row[0] >= 0) + (TL::kRuns == 2 && row[TL::kRuns - 1] >= 0);
       if (n == 0) {
         mbar_arrive(bar);
         return;
       }
-      mbar_expect_tx(bar, n * ((2 * TL::kBytes + 2 * TL::kScaleBytes) / 2));
+      mbar_expect_tx(bar, n * ((2 * TL::kBytes + 2 * TL::kScaleBytes) / TL::kRuns));
 #pragma unroll 1
-      for (int r = 0; r < 2; ++r) {
-        const int from = r ? row[1] : row[0];
+      for (int r = 0; r < TL::kRuns; ++r) {
+        const int from = r ? row[TL::kRuns - 1] : row[0];
         if (from < 0 || (r == 1 && one)) continue;
-        const uint32_t bytes = TL::kBytes / (one ? 1 : 2), scale_bytes = TL::kScaleBytes / (one ? 1 : 2);
-        uint8_t* codes = st + r * (TL::kBytes / 2);
-        uint8_t* steps = st + TL::kScaleOff + r * (TL::kScaleBytes / 2);
+        const uint32_t parts = one ? 1 : TL::kRuns, bytes = TL::kBytes / parts, scale_bytes = TL::kScaleBytes / parts;
+        uint8_t* codes = st + r * (TL::kBytes / TL::kRuns);
+        uint8_t* steps = st + TL::kScaleOff + r * (TL::kScaleBytes / TL::kRuns);
         const int64_t at = static_cast<int64_t>(from);
         bulk_load(codes, A.k_cache + at * (D / 2), bytes, bar);
         bulk_load(steps, A.k_scales + at * 2, scale_bytes, bar);

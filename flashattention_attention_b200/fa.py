@@ -830,8 +830,8 @@ def kv_append_rope_paged(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torc
         else:
             qo = _operand(q_out, "q_out", dev, _BF16, out_shape)
     p = _pack_append(kn, vn, qp, qo, kts, khs, vts, vhs, qts, qhs, ots, ohs, table, kp, vp, ks, vs, bounds, cu, pos,
-                           lens, FA_BF16 if xt is _BF16 else FA_F32, kind, batch, total, hq, hkv, d, rot,
-                           1 if interleaved else 0, table_rows)
+                     lens, FA_BF16 if xt is _BF16 else FA_F32, kind, batch, total, hq, hkv, d, rot,
+                     1 if interleaved else 0, table_rows)
     _on_device(dev, stream, "fa_kv_append_rope_paged", lib.fa_kv_append_rope_paged, p, pg)
     return q_out
 
