@@ -22,7 +22,10 @@
 // the choosing block's shared memory.  Else the pages of all pairs are dealt
 // evenly to the device's warps and a second kernel chooses, since a pair's own
 // cluster would go over its pages in rounds that each wait for memory (128
-// pairs of up to 1021 pages: 22.6 us in clusters of two, 21.7 us dealt evenly).
+// pairs of up to 1021 pages: 22.6 us in clusters of two, 21.7 us dealt evenly,
+// both before the choice became 2 us shorter).  Bound by latency: 37 MB of
+// bounds are 6 us, the choosing block's steps (two reads of the scores, a
+// histogram, the few pages between summed again, the list) about 5 us.
 // One pass over the bounds, 4 d bytes a page; the choice works on 4 bytes a page.
 #include "decode_mma.cuh"
 #include "internal.h"
@@ -49,7 +52,7 @@ struct PickShared {
   int between[kBetween];
   uint32_t exact[kBetween];
   int warp_sum[kSelWarps];
-  int bin, above, inside, n_between;
+  int bin, above, inside, n_in, n_between;
 };
 
 struct SelectArgs {
@@ -270,6 +273,12 @@ __global__ void __launch_bounds__(kThreads, kJ == 8 ? 1 : 2) page_score_kernel(c
   }
 }
 
+// Two consecutive bf16 values.
+__device__ __forceinline__ float2 pair_at(const __nv_bfloat16* p) {
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
 // The exact score of page p by one warp: fp64 sums of exact products, rounded
 // once; four heads' sums at a time.
 __device__ float exact_score(const SelectArgs& A, int b, int g, int p) {
@@ -281,12 +290,13 @@ __device__ float exact_score(const SelectArgs& A, int b, int g, int p) {
   for (int h = 0; h < A.group; h += 4, q += 4 * A.d) {
     double sum[4] = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll 2
-    for (int c = lane; c < A.d; c += 32) {
-      const float lo = __bfloat162float(row[c]), hi = __bfloat162float(row[A.d + c]);
+    for (int c = 2 * lane; c < A.d; c += 64) {
+      const float2 lo = pair_at(row + c), hi = pair_at(row + A.d + c);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float qv = h + k < A.group ? __bfloat162float(q[k * A.d + c]) : 0.f;
-        sum[k] += fmaxf(qv * lo, qv * hi);
+        const float2 qv = h + k < A.group ? pair_at(q + k * A.d + c) : make_float2(0.f, 0.f);
+        sum[k] += fmaxf(qv.x * lo.x, qv.x * hi.x);
+        sum[k] += fmaxf(qv.y * lo.y, qv.y * hi.y);
       }
     }
 #pragma unroll
@@ -410,9 +420,10 @@ __device__ __forceinline__ void pick_pages(const SelectArgs& A, PickShared& S, f
         if (at < kBetween) S.between[at] = i;
       }
     }
-    int taken;
-    block_scan(S, in, taken);
-    const int n_between = S.n_between;
+    in = __reduce_add_sync(0xffffffffu, in);
+    if (lane == 0 && in > 0) atomicAdd(&S.n_in, in);
+    __syncthreads();
+    const int taken = S.n_in, n_between = S.n_between;
     if (n_between == need - taken && out_to > -INFINITY) {  // no choice to make: what is not out is in
       kth = order_key(-INFINITY);
     } else if (n_between <= kBetween) {
@@ -453,19 +464,24 @@ __device__ __forceinline__ void pick_pages(const SelectArgs& A, PickShared& S, f
   const int per = (n + kThreads - 1) / kThreads;
   const int p0 = min(n, tid * per), p1 = min(n, p0 + per);
   int above = 0, equal = 0, total;
+  uint32_t taken_bits = 0;  // of a thread's first 32 pages
   for (int p = p0; p < p1; ++p) {
-    if (p < lo || p >= hi) {
-      ++above;
-    } else if (need > 0) {
+    bool take = p < lo || p >= hi;
+    if (!take && need > 0) {
       const uint32_t k = order_key(sc[p - lo]);
-      above += k > kth;
+      take = k > kth;
       equal += k == kth;
     }
+    above += take;
+    if (p - p0 < 32) taken_bits |= static_cast<uint32_t>(take) << (p - p0);
   }
   int at = block_scan(S, above, total), tied = 0;
   if (ties > 0) {  // the same for the whole block
     tied = block_scan(S, equal, total);
     at += min(tied, ties);
+  } else if (per <= 32) {
+    for (; taken_bits != 0; taken_bits &= taken_bits - 1) out[at++] = p0 + __ffs(taken_bits) - 1;
+    return;
   }
   for (int p = p0; p < p1; ++p) {
     bool take = p < lo || p >= hi;
@@ -493,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, kJ == 8 ? 1 : 2) page_select_kernel(
   const int u = blockIdx.x / cluster_size(), b = u / A.hkv, g = u % A.hkv;
   if (first) {
     for (int i = threadIdx.x; i < kBins; i += kThreads) S.hist[i] = 0;
-    if (threadIdx.x == 0) S.n_between = 0;
+    if (threadIdx.x == 0) S.n_in = S.n_between = 0;
   }
   griddep_wait();
   // the first round's pages, looked up together with the length
@@ -524,7 +540,7 @@ __global__ void __launch_bounds__(kThreads) page_pick_kernel(const SelectArgs A)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int u = blockIdx.x, b = u / A.hkv, g = u % A.hkv;
   for (int i = threadIdx.x; i < kBins; i += kThreads) S.hist[i] = 0;
-  if (threadIdx.x == 0) S.n_between = 0;
+  if (threadIdx.x == 0) S.n_in = S.n_between = 0;
   griddep_wait();
   const int n = pages_of(A, b, false);
   if (n <= A.top_k) {
@@ -535,8 +551,11 @@ __global__ void __launch_bounds__(kThreads) page_pick_kernel(const SelectArgs A)
   const float4* parts = A.parts + static_cast<int64_t>(u) * ((A.max_pages + 15) / 16);
   float* stored = A.scores + static_cast<int64_t>(u) * A.max_pages + lo;
   float* sc = m <= kHeld ? S.scores : stored;
-  if (m <= kHeld) {
-    for (int i = threadIdx.x; i < m; i += kThreads) sc[i] = __ldcg(stored + i);
+  float first[4];  // on their way with the statistics
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int i = threadIdx.x + k * kThreads;
+    first[k] = i < m ? __ldcg(stored + i) : 0.f;
   }
   float most = 0.f, least = INFINITY, greatest = -INFINITY;
   for (int i = threadIdx.x; i < groups; i += kThreads) {
@@ -544,6 +563,12 @@ __global__ void __launch_bounds__(kThreads) page_pick_kernel(const SelectArgs A)
     most = fmaxf(most, v.x);
     least = fminf(least, v.y);
     greatest = fmaxf(greatest, v.z);
+  }
+  if (m <= kHeld) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (threadIdx.x + k * kThreads < m) sc[threadIdx.x + k * kThreads] = first[k];
+    for (int i = threadIdx.x + 4 * kThreads; i < m; i += kThreads) sc[i] = __ldcg(stored + i);
   }
   warp_stats(most, least, greatest);
   if (lane == 0) {
@@ -563,8 +588,8 @@ int cluster_of(int64_t units) {
   return cluster;
 }
 // Whether a cluster per unit scores its pages in one round of 16 per warp (with
-// the attention that follows, one sequence of 8 KV heads: 17.2 us, dealt evenly
-// 20.6; 4 sequences of up to 8192 bf16 keys: 29.4 and 34.9).
+// the attention that follows, one sequence of 8 KV heads and 513 pages: 17.2 us,
+// dealt evenly 20.6; 4 sequences of up to 1024 pages: 29.4 and 34.9).
 bool one_round(int64_t units, int max_pages) { return cluster_of(units) * kSelWarps * 16 >= max_pages; }
 
 template <int kJ>
