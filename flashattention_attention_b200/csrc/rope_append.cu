@@ -658,7 +658,7 @@ PoolArgs pool_args(const fa_kv_pages& pg, int hkv, int d) {
 
 // Rows of a token per group: four, and twice that while the groups fill the
 // device several times over (the lookups of a token are then spread over more
-// rows).  One token of 8 + 8 heads: 4.2 us with four rows, 6.2 with eight; a
+// rows).  One token of 32 + 8 + 8 heads: 4.2 us with four rows, 6.2 with eight; a
 // 16384-token prompt: 124 us with four, 115 with eight, 107 with this rule.
 int rows_per_item(int64_t total, int rows, int groups) {
   const int64_t enough = static_cast<int64_t>(device_sm_count()) * 8 * groups;
@@ -673,7 +673,7 @@ fa_status launch_append_typed(AppendArgs& A, const LaunchCtx& ctx) {
   A.token_rows = A.hq + (A.bounds != nullptr ? 1 : 2) * A.pool.hkv;
   A.part_rows = rows_per_item(A.total, A.token_rows, kGroups);
   const int parts = (A.token_rows + A.part_rows - 1) / A.part_rows;
-  // page role: a CTA per token where there are few (64 sequences of one token
+  // page role: a CTA per token where there are few (96 sequences of one token
   // each, read back too: 12.7 us, eight tokens a CTA 22), else per eight
   // tokens, of which most open no page (16384-token prompt: 107 us, one a CTA 164)
   A.window = A.total <= 4 * device_sm_count() ? 1 : 8;
