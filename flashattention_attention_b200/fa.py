@@ -965,7 +965,7 @@ def _decode_pages(q, k_pages, v_pages, cache_seqlens, block_table, selected, hq,
         ops = bytes(array)
     fields = (qp, kp, vp, ks, vs, lens, op, kind, batch, hq, hkv, d, _int(capacity, "max_pages * page_size"),
               _int(max_seqlen, "max_seqlen"), _int(window, "window") if window > 0 else 0,
-              1.0 / math.sqrt(d) if scale is None else float(scale), 0, n_epilogue, ops)
+              1.0 / math.sqrt(d) if scale is None else ctypes.c_float(scale).value, 0, n_epilogue, ops)
     if selected is None:
         top_k, what, fn, more = 0, "fa_attention_decode_paged", lib.fa_attention_decode_paged, ()
     else:

@@ -221,7 +221,7 @@ def test_binding_refuses_append_tensors_that_do_not_fit(fa):
             fa.kv_append_rope_paged(*args, **kw)
 
 
-def test_binding_refuses_decode_tensors_that_do_not_fit(fa):
+def test_binding_refuses_decode_tensors_that_do_not_fit(fa, monkeypatch):
     bf, i32, f32, u8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
     other = torch.device("cuda", 1)
 
@@ -257,6 +257,30 @@ def test_binding_refuses_decode_tensors_that_do_not_fit(fa):
                 Fake(0xa000, (3, 2, 4), i32, other)):
         with pytest.raises(ValueError):
             fa.attention_decode_selected(*args, sel, **kw)
+
+
+    # a scale that fp32 does not hold is the library's to refuse
+    for scale in (1e39, float("inf"), float("nan")):
+        with monkeypatch.context() as m:
+            m.setattr(fa, "_on_device", lambda dev, stream, what, fn, *a: statuses.append(fn(*a, None)))
+            statuses = []
+            fa.attention_decode_paged(*args, scale=scale, **kw)
+            assert statuses == [fa.FA_ERR_INVALID]
+
+
+def test_packed_arguments_have_the_structures_layout(fa):
+    for cls, pack in ((fa.KvAppendRopeParams, fa._pack_append), (fa.KvReadParams, fa._pack_read),
+                      (fa.PageSelectParams, fa._pack_select), (fa.DecodeParams, fa._pack_decode),
+                      (fa.KvPages, fa._pack_pages)):
+        values = []
+        for i, (_, c) in enumerate(cls._fields_):
+            whole = c in (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t)
+            values.append(i + 1 if whole else i + 0.5 if c is ctypes.c_float
+                          else bytes((7 * i + j) % 251 for j in range(ctypes.sizeof(c))))
+        packed = cls.from_buffer_copy(pack(*values))
+        for (name, _), v in zip(cls._fields_, values):
+            got = getattr(packed, name)
+            assert (bytes(got) if isinstance(v, bytes) else got) == v, (cls, name)
 
 
 def test_binding_refuses_select_and_read_tensors_that_do_not_fit(fa):
