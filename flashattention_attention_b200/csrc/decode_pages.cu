@@ -19,15 +19,19 @@
 //   q . k = step (q . code) + offset sum(q),
 //   sum_j p_j v_j = sum_j (p_j step_j) code_j + sum_j p_j offset_j
 // where the second terms stay in fp32.  p_j step_j is rounded to fp16 after
-// division by the power of two below the largest step seen so far (rescaled
-// like the running maximum), so no step is too small or too large for fp16.
+// multiplication by a power of two, the head's unit, that follows the largest
+// products up and down (softmax below), so that no step or weight is too small
+// or too large for fp16 beside what came before it.
 // int8 rows: the same without offsets.  A word of eight codes holds channels
 // 0 .. 7 of its four bytes: the low halves of bytes 0 and 2 are channels 0 and
 // 4, in an order that Q's fragments (and the output's addresses) follow.
-// Codes are not centred, so sum (p step) code grows with the number of keys
-// whatever the values are, and the tensor core's additions to a large number
-// lose bits to one side: every 16 tiles the part all channels share is moved
-// from the accumulators into one number per head.
+// Codes are not centred (0 .. 15), so
+//   sum_j w_j code_j + sum_j p_j offset_j  with w_j the rounded p_j step_j
+// would multiply the roundings of w by numbers about three times as large as the
+// values' spread, and the tensor core's additions to a large number would lose
+// bits to one side.  So the second sum takes p_j (offset_j + 7.5 step_j), one
+// more MMA with ones adds up w_j, and every 8 tiles (and at the end) 7.5 times
+// that leaves the accumulators, which then hold sums of w_j (code_j - 7.5).
 //
 // A 4-bit row of 128 is 72 bytes and as much arithmetic as 256 bytes of bf16, so
 // the kernel is bound by its instructions and their latencies: about 430 per 32
@@ -47,6 +51,8 @@ namespace {
 
 constexpr int kThreads = kWarps * 32;
 constexpr float kSlack = 8.f;    // binary orders a weight may pass its reference by
+constexpr uint32_t kOnes = 0x3c003c00u;  // fp16 1, twice
+constexpr float kTop = 32768.f;  // no weight as large as this enters fp16
 constexpr int kMaxBatch = 256;  // sequences per launch (their tile prefix is in shared memory)
 
 // Division of 0 <= x < 2^31 by a number known on the host: x / d =
@@ -382,17 +388,58 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
   float m_run[2];                         // reference of each head's weights
   float2 nref = make_float2(0.f, 0.f);  // its negative, 0 where there is none
   float2 l_run;
-  float2 om;          // 4 bits: sum of p * offset (heads 2qq, 2qq + 1)
-  float2 moved;       // 4 bits: what was taken from this thread's accumulators of low codes
-  float cap = 0.f;    // quantised: power of two below the largest V step so far,
-  float to_unit = 0.f;  // and its inverse
+  float2 om;    // 4 bits: sum of p * (offset + 7.5 step) (heads 2qq, 2qq + 1)
+  float2 unit;  // quantised: power of two by which p * step enters the MMA
+  [[maybe_unused]] float2 seen;  // quantised: this thread's largest p * step * unit since the units were looked at
+  [[maybe_unused]] float sw[4];  // 4 bits: sum of the rounded p * step (rows gq and gq + 8 alike)
   auto reset = [&]() {
 #pragma unroll
     for (int m = 0; m < kMT; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
     m_run[0] = m_run[1] = -INFINITY;
     nref = make_float2(0.f, 0.f);
-    l_run = om = moved = make_float2(0.f, 0.f);
-    cap = to_unit = 0.f;
+    l_run = om = seen = make_float2(0.f, 0.f);
+    unit = make_float2(0x1p118f, 0x1p118f);  // the largest: any ordinary tile sets it
+    sw[0] = sw[1] = sw[2] = sw[3] = 0.f;
+  };
+  // 4 bits: the accumulators' sums of code become sums of code - 7.5
+  auto centre = [&]() {
+    const float2 c = mul2(make_float2(sw[0], sw[1]), make_float2(-7.5f / kLowUnit, -7.5f / kLowUnit));
+#pragma unroll
+    for (int mi = 0; mi < kMT; ++mi) {
+      o[mi][0] += c.x;
+      o[mi][1] += c.y;
+      o[mi][2] = fmaf(16.f, c.x, o[mi][2]);
+      o[mi][3] = fmaf(16.f, c.y, o[mi][3]);
+    }
+    sw[0] = sw[1] = sw[2] = sw[3] = 0.f;
+  };
+  // Head j's unit so that `top` (any thread's, in the present unit) comes to [2^7,
+  // 2^8) if it is not in [1, 2^15), and the head's accumulators in that unit:
+  // powers of two, so nothing is rounded.  A unit that grows stops where the
+  // accumulators would pass 2^100.
+  auto refit = [&](int j, float top) {
+    float& u = j ? unit.y : unit.x;
+    float most = 0.f;
+#pragma unroll
+    for (int m = 0; m < kMT; ++m) most = fmaxf(most, fmaxf(fabsf(o[m][j]), fabsf(o[m][j + 2])));
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+    }
+    if (top == 0.f || (top >= 1.f && top < kTop)) return;
+    // exponent bits: u's are 1 .. 245, so 1 / u is a normal number too
+    const int had = static_cast<int>(__float_as_uint(u) >> 23);
+    int to = had + 134 - static_cast<int>(__float_as_uint(top) >> 23);
+    to = min(to, had + min(120, 227 - static_cast<int>(__float_as_uint(most) >> 23)));
+    to = max(1, min(to, 245));
+    u = __uint_as_float(static_cast<uint32_t>(to) << 23);
+    const float ratio = u * __uint_as_float(static_cast<uint32_t>(254 - had) << 23);
+#pragma unroll
+    for (int m = 0; m < kMT; ++m) {
+      o[m][j] *= ratio;
+      o[m][j + 2] *= ratio;
+    }
   };
   auto load_q = [&](int b, int g) {
     const bool head_ok = gq < A.group;
@@ -464,6 +511,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
   // its record (segment + worker; cluster: in this warp's ring, [group][D]).
   float* held = reinterpret_cast<float*>(stage_ptr(0));
   auto finish = [&](int seg, bool whole) {
+    if constexpr (kI4) centre();
     float l0 = l_run.x, l1 = l_run.y, m0 = om.x, m1 = om.y;
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {
@@ -481,17 +529,17 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
       const int h = 2 * qq + j;
       if (h >= A.group) break;
       const float add = j ? m1 : m0, l = j ? l1 : l0;
+      [[maybe_unused]] const float back = 1.f / (j ? unit.y : unit.x);
       float y[2 * kMT];
 #pragma unroll
       for (int mi = 0; mi < kMT; ++mi) {
         const float lo = j ? o[mi][1] : o[mi][0], hi = j ? o[mi][3] : o[mi][2];
         if constexpr (kI4) {
-          const float back = j ? moved.y : moved.x;
-          y[2 * mi] = fmaf((lo + back) * kLowUnit, cap, add);
-          y[2 * mi + 1] = fmaf((hi + 16.f * back) * kHighUnit, cap, add);
+          y[2 * mi] = fmaf(lo * kLowUnit, back, add);
+          y[2 * mi + 1] = fmaf(hi * kHighUnit, back, add);
         } else {
-          y[2 * mi] = kI8 ? lo * cap : lo;
-          y[2 * mi + 1] = kI8 ? hi * cap : hi;
+          y[2 * mi] = kI8 ? lo * back : lo;
+          y[2 * mi + 1] = kI8 ? hi * back : hi;
         }
       }
       if (!whole) {
@@ -666,7 +714,6 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
         float2 x[2][2];                             // [mt][key half], heads 2qq and 2qq + 1
         [[maybe_unused]] float vs[2][2], vo[2][2];  // quantised: V step, 4 bits: V offset
         float mx0 = -INFINITY, mx1 = -INFINITY;
-        [[maybe_unused]] float top = 0.f;
         const float2 qs = make_float2(qs0, qs1);
         [[maybe_unused]] const float2 qm = make_float2(qm0, qm1);
 #pragma unroll
@@ -681,13 +728,11 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
               const float step = __uint_as_float(sk.x), off = __uint_as_float(sk.y);
               v = fma2(v, make_float2(step, step), mul2(make_float2(off, off), qm));
               vs[mt][hf] = ok ? __uint_as_float(sv.x) : 0.f;
-              vo[mt][hf] = ok ? __uint_as_float(sv.y) : 0.f;
-              top = fmaxf(top, vs[mt][hf]);
+              vo[mt][hf] = ok ? fmaf(7.5f, __uint_as_float(sv.x), __uint_as_float(sv.y)) : 0.f;  // of code 7.5
             } else if constexpr (kI8) {
               const float step = __uint_as_float(lds32(ksc + 4 * kl));
               v = mul2(v, make_float2(step, step));
               vs[mt][hf] = ok ? __uint_as_float(lds32(vsc + 4 * kl)) : 0.f;
-              top = fmaxf(top, vs[mt][hf]);
             }
             if (kMasked && !ok) v = make_float2(-INFINITY, -INFINITY);
             x[mt][hf] = v;
@@ -696,11 +741,9 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
           }
         }
         // A head's reference moves, and O is rescaled, only when a logit passes
-        // it by more than 8 (weights then reach 2^8, far inside fp16's range
-        // and exact as factors); likewise the V unit when a step reaches 16 of
-        // it.  So most tiles need no maximum across lanes.
-        bool up = mx0 > m_run[0] + kSlack || mx1 > m_run[1] + kSlack;
-        if constexpr (!kBF) up |= top >= 16.f * cap && top > 0.f;
+        // it by more than 8 (weights then reach 2^8, exact as factors), so most
+        // tiles need no maximum across lanes.
+        const bool up = mx0 > m_run[0] + kSlack || mx1 > m_run[1] + kSlack;
         if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) {
@@ -709,20 +752,14 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
           }
           const float mn0 = fmaxf(m_run[0], mx0), mn1 = fmaxf(m_run[1], mx1);
           nref = make_float2(mn0 == -INFINITY ? 0.f : -mn0, mn1 == -INFINITY ? 0.f : -mn1);
-          float2 al = make_float2(ex2_approx(m_run[0] + nref.x), ex2_approx(m_run[1] + nref.y));
+          const float2 al = make_float2(ex2_approx(m_run[0] + nref.x), ex2_approx(m_run[1] + nref.y));
           m_run[0] = mn0;
           m_run[1] = mn1;
           l_run = mul2(l_run, al);
-          if constexpr (!kBF) {
-            // steps are not negative, so their bits order like the numbers
-            const unsigned bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-            const float unit = fmaxf(cap, __uint_as_float(bits & 0x7f800000u));
-            const float ratio = unit > 0.f ? cap / unit : 0.f;
+          if constexpr (kI4) {
             om = mul2(om, al);
-            al = mul2(al, make_float2(ratio, ratio));
-            moved = mul2(moved, al);
-            cap = unit;
-            to_unit = unit > 0.f ? 1.f / unit : 0.f;
+            sw[0] *= al.x;
+            sw[1] *= al.y;
           }
 #pragma unroll
           for (int m = 0; m < kMT; ++m) {
@@ -730,31 +767,61 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
             o[m][1] *= al.y; o[m][3] *= al.y;
           }
         }
+        float2 p[2][2];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
-          uint32_t packed[2];
-          [[maybe_unused]] uint32_t rest[2];
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const float2 y = add2(x[mt][hf], nref);
-            float2 p = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-            l_run = add2(l_run, p);
-            if constexpr (kBF) {
-              packed[hf] = pack_bf16x2(p.x, p.y);
-              rest[hf] = pack_bf16x2(p.x - __uint_as_float(packed[hf] << 16),
-                                     p.y - __uint_as_float(packed[hf] & 0xffff0000u));
-            } else {
-              if constexpr (kI4) om = fma2(p, make_float2(vo[mt][hf], vo[mt][hf]), om);
-              const float u = vs[mt][hf] * to_unit;
-              p = mul2(p, make_float2(u, u));
-              packed[hf] = pack_f16x2(p.x, p.y);
+            p[mt][hf] = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+            l_run = add2(l_run, p[mt][hf]);
+            if constexpr (kI4) om = fma2(p[mt][hf], make_float2(vo[mt][hf], vo[mt][hf]), om);
+          }
+        }
+        // pb: S rows 2qq, 2qq + 1 and 8 + 2qq, 9 + 2qq of head gq
+        if constexpr (kBF) {
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const float2 v = p[mt][hf];
+              const uint32_t packed = pack_bf16x2(v.x, v.y);
+              pb[mt][hf] = transpose8x8(packed);
+              pl[mt][hf] = transpose8x8(pack_bf16x2(v.x - __uint_as_float(packed << 16),
+                                                    v.y - __uint_as_float(packed & 0xffff0000u)));
             }
           }
-          pb[mt][0] = transpose8x8(packed[0]);  // (head gq; S rows 2qq, 2qq+1)
-          pb[mt][1] = transpose8x8(packed[1]);  // (head gq; S rows 8+2qq, 8+2qq+1)
-          if constexpr (kBF) {
-            pl[mt][0] = transpose8x8(rest[0]);
-            pl[mt][1] = transpose8x8(rest[1]);
+        } else {
+          // p * step enters the MMA as fp16 (half a step of it, 2^-11 of a
+          // weight; what 4-bit codes share is added in fp32, so it falls on
+          // code - 7.5) after multiplication by the head's unit.  The unit is
+          // set anew, and O rescaled with it, when a weight reaches 2^15, and
+          // every 8 tiles where none of their weights reached 1: so what fp16
+          // drops or rounds by its smallest step, 2^-25 of a unit, is small
+          // beside a weight at most 16 tiles before it, however large those of
+          // other tiles are.
+          auto weigh = [&]() {
+            float2 w[2][2];
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                w[mt][hf] = mul2(p[mt][hf], mul2(unit, make_float2(vs[mt][hf], vs[mt][hf])));
+                pb[mt][hf] = transpose8x8(pack_f16x2(w[mt][hf].x, w[mt][hf].y));
+              }
+            }
+            seen.x = max3f(seen.x, w[0][0].x, max3f(w[0][1].x, w[1][0].x, w[1][1].x));
+            seen.y = max3f(seen.y, w[0][0].y, max3f(w[0][1].y, w[1][0].y, w[1][1].y));
+          };
+          weigh();
+          // once; up to three times where a product with the old unit is infinite (four: a step is)
+#pragma unroll 1
+          for (int tries = 0; tries < 4 && __any_sync(0xffffffffu, fmaxf(seen.x, seen.y) >= kTop); ++tries) {
+            if constexpr (kI4) centre();
+            refit(0, seen.x);
+            refit(1, seen.y);
+            seen = make_float2(0.f, 0.f);
+            weigh();
           }
         }
       };
@@ -816,6 +883,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
         };
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
+          mma16816(sw, kOnes, kOnes, kOnes, kOnes, pb[mt][0], pb[mt][1]);
           const uint32_t a0 = vt + gq * (D / 16) + 16 * mt * (D / 2);
           uint32_t at[4];
 #pragma unroll
@@ -856,22 +924,16 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
         }
       }
     }
-    if constexpr (kI4) {
-      if ((i & 15) == 15) {
-        // what the channels share: the mean over this thread's low codes
-        // (about 7.5 2^-24 sum of P'; 16 times that in the high ones)
-        float2 mean = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int mi = 0; mi < kMT; ++mi) mean = add2(mean, make_float2(o[mi][0], o[mi][1]));
-        mean = mul2(mean, make_float2(1.f / kMT, 1.f / kMT));
-        moved = add2(moved, mean);
-#pragma unroll
-        for (int mi = 0; mi < kMT; ++mi) {
-          o[mi][0] -= mean.x;
-          o[mi][1] -= mean.y;
-          o[mi][2] = fmaf(-16.f, mean.x, o[mi][2]);
-          o[mi][3] = fmaf(-16.f, mean.y, o[mi][3]);
+    if constexpr (!kBF) {
+      if ((i & 7) == 7) {
+        if constexpr (kI4) centre();
+        const unsigned same = 0x11111111u << qq;  // the lanes of this thread's heads
+        const unsigned x = __ballot_sync(0xffffffffu, seen.x >= 1.f), y = __ballot_sync(0xffffffffu, seen.y >= 1.f);
+        if (__any_sync(0xffffffffu, (x & same) == 0 || (y & same) == 0)) {
+          refit(0, seen.x);
+          refit(1, seen.y);
         }
+        seen = make_float2(0.f, 0.f);
       }
     }
     // the stage is free: the tile kStages on goes there
