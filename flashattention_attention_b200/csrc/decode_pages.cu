@@ -184,6 +184,7 @@ __device__ __forceinline__ TileInfo<kRuns> tile_at(const PageArgs& A, int b, int
       key0 = (first_key<kSel>(A, L) / (kRuns * kTile) + t) * (kRuns * kTile) + r * kTile;
       lp = A.by_page.div(key0);
       off = key0 - lp * A.page_size;
+      if (key0 + kTile <= first_key<kSel>(A, L)) continue;  // before the window, perhaps in a page that is gone
     }
     if (key0 >= L) continue;
     int pg = A.block_table[static_cast<int64_t>(b) * A.max_pages + lp];
@@ -598,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
       left = my_tiles;
       key_end = length_of(A, the_b);
       k_lo = first_key<kSel>(A, key_end);
-      tile_key = __shfl_sync(0xffffffffu, cur.key0[0], 0);
+      tile_key = (k_lo / TL::kKeys + t_first) * TL::kKeys;
     }
     if (!kCluster && left == 0) {
       seg = __shfl_sync(0xffffffffu, cur.seg, i & 31);
@@ -614,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
       }
       key_end = length_of(A, b);
       k_lo = first_key<kSel>(A, key_end);
-      tile_key = __shfl_sync(0xffffffffu, cur.key0[0], i & 31);
+      tile_key = (k_lo / TL::kKeys + done) * TL::kKeys;
     }
     // every lane polls; whether to go on is a decision of the whole warp
     const bool ready = wait_parity(&bars[s], parity, A.wd);
@@ -627,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
 #pragma unroll 1
     for (int r = 0; r < TL::kRuns; ++r) {
       const int key0 = kSel ? __shfl_sync(0xffffffffu, cur_key0(r), i & 31) : tile_key + r * kTile;
-      if (kSel ? key0 == kNoKey : key0 >= key_end) continue;
+      if (kSel ? key0 == kNoKey : key0 >= key_end || key0 + kTile <= k_lo) continue;
       const uint32_t kt = smem_u32(stage_ptr(s)) + r * (TL::kBytes / TL::kRuns);
       const uint32_t vt = kt + TL::kBytes;
       const uint32_t ksc = smem_u32(stage_ptr(s)) + TL::kScaleOff + r * (TL::kScaleBytes / TL::kRuns);
