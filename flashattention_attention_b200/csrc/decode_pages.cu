@@ -145,7 +145,7 @@ template <int kKeys, bool kSel>
 __device__ __forceinline__ int tiles_in(const PageArgs& A, int L) {
   if constexpr (kSel)
     return (min(A.top_k, pages_in(A, L)) * static_cast<int>(A.by_page_runs.d) + kKeys / kTile - 1) / (kKeys / kTile);
-  return L > 0 ? (L + kKeys - 1) / kKeys - first_key<kSel>(A, L) / kKeys : 0;
+  return L > 0 ? (L - 1) / kKeys + 1 - first_key<kSel>(A, L) / kKeys : 0;  // (L + kKeys may not be an int)
 }
 __device__ __forceinline__ int length_of(const PageArgs& A, int b) { return max(0, min(A.seqlens[b], A.capacity)); }
 
@@ -184,7 +184,8 @@ __device__ __forceinline__ TileInfo<kRuns> tile_at(const PageArgs& A, int b, int
       key0 = (first_key<kSel>(A, L) / (kRuns * kTile) + t) * (kRuns * kTile) + r * kTile;
       lp = A.by_page.div(key0);
       off = key0 - lp * A.page_size;
-      if (key0 + kTile <= first_key<kSel>(A, L)) continue;  // before the window, perhaps in a page that is gone
+      // behind the last key, or before the window, perhaps in a page that is gone
+      if (key0 >= L || key0 + kTile <= first_key<kSel>(A, L)) continue;
     }
     if (key0 >= L) continue;
     int pg = A.block_table[static_cast<int64_t>(b) * A.max_pages + lp];
@@ -945,7 +946,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, kKind>::kCtas)
       s = 0;
       parity ^= 1;
     }
-    tile_key += TL::kKeys;
+    if (left > 1) tile_key += TL::kKeys;
     if (--left == 0) finish(seg, whole);
   }
   if constexpr (kCluster) {
