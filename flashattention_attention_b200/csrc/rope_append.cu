@@ -239,8 +239,10 @@ __device__ __forceinline__ uint32_t codes4_fast(float2 x0, float2 x1, float lo, 
 __device__ __noinline__ uint32_t codes4_any(float2 x0, float2 x1, float lo, float r) {
   const float x[4] = {x0.x, x0.y, x1.x, x1.y};
   uint32_t w = 0;
+  // a power of two that keeps 15 (x - lo) finite and leaves the quotient as it is
+  const float k = r > 0x1p60f ? 0x1p-8f : 1.0f, kr = __fmul_rn(r, k);
   for (int e = 0; e < 4; ++e) {
-    const float q = r > 0.0f ? __fdiv_rn(__fmul_rn(__fsub_rn(x[e], lo), 15.0f), r) : 0.0f;
+    const float q = r > 0.0f ? __fdiv_rn(__fmul_rn(__fmul_rn(__fsub_rn(x[e], lo), k), 15.0f), kr) : 0.0f;
     w |= (static_cast<uint32_t>(__float2int_rn(q)) & 15u) << (4 * e);
   }
   return w;

@@ -424,8 +424,9 @@ FA_API fa_status fa_kv_append_paged(const fa_kv_append_params *p, const fa_kv_pa
  * and hi the row's least and greatest value and r = hi - lo, channel c's code
  * is round_half_even(15 (x_c - lo) / r) in 0 .. 15, step = r / 15, offset = lo
  * (each operation rounded to fp32; r = 0 gives codes 0); the code of channel
- * 2j is the low half of byte j of the row.  Rows whose values or range are
- * not finite give unspecified codes.
+ * 2j is the low half of byte j of the row (a range so wide that 15 r passes
+ * fp32's largest number is quantised as if it did not).  Rows whose values or
+ * range are not finite give unspecified codes.
  * A token whose slot is outside [0, capacity) (capacity = max_pages *
  * page_size), at or past rope_rows, or in a page outside [0, num_pages) is
  * skipped (its q_out row too) and reported by fa_check_device_error as
