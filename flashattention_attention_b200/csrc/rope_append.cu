@@ -551,7 +551,8 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendArgs A)
     for (int b = threadIdx.x; b < A.batch; b += kThreads) {
       const int64_t c0 = A.cu != nullptr ? A.cu[b] : b, c1 = A.cu != nullptr ? A.cu[b + 1] : b + 1;
       const int64_t end = static_cast<int64_t>(A.cur_pos[b]) + (c1 - c0);
-      if (c0 < 0 || c1 < c0 || c1 > A.total || A.cur_pos[b] < 0 || end > A.pool.capacity) {
+      const bool past_table = A.rot > 0 && c1 > c0 && end > A.rope_rows;  // its last tokens are not written
+      if (c0 < 0 || c1 < c0 || c1 > A.total || A.cur_pos[b] < 0 || end > A.pool.capacity || past_table) {
         record_status(A.wd, kStatusRange);
       } else if (A.seqlens != nullptr) {
         A.seqlens[b] = static_cast<int32_t>(end);

@@ -431,7 +431,9 @@ FA_API fa_status fa_kv_append_paged(const fa_kv_append_params *p, const fa_kv_pa
  * page_size), at or past rope_rows, or in a page outside [0, num_pages) is
  * skipped (its q_out row too) and reported by fa_check_device_error as
  * FA_ERR_INVALID; the cache_seqlens entry of a sequence that leaves [0,
- * capacity] is not written.  cu_seqlens that do not ascend within [0, total]
+ * capacity], or whose new tokens pass rope_rows, is not written.  (A page
+ * outside the pool does not hold it back: the table itself is wrong then, and
+ * every call that reads that page reports it.)  cu_seqlens that do not ascend within [0, total]
  * are reported too, and which of their tokens go where is unspecified (always
  * inside the pools).  Two sequences of one call must not append to the same
  * page.
