@@ -41,6 +41,8 @@ constexpr int kBins = 2048;
 // k-steps (d / 16 of hi and of lo) have 17 addends, each of which may lose
 // 2^-22 of the largest partial sum (at most A).
 __device__ __forceinline__ float error_share(int d) { return static_cast<float>(d / 8 * 17) * 0x1p-22f; }
+// And what they may lose below fp32's normal range: 2^-126 for each addend (d <= 256).
+constexpr float kErrorFloor = 0x1p-116f;
 
 constexpr int kHeld = 4096;    // scores a block holds in shared memory (more stay in L2)
 constexpr int kBetween = 256;  // pages next to the border that are ranked directly
@@ -279,8 +281,9 @@ __device__ __forceinline__ float2 pair_at(const __nv_bfloat16* p) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// The exact score of page p by one warp: fp64 sums of exact products, rounded
-// once; four heads' sums at a time.
+// The exact score of page p by one warp: fp64 sums of exact products (in fp32
+// they might pass its range at either end), rounded once; four heads' sums at a
+// time.
 __device__ float exact_score(const SelectArgs& A, int b, int g, int p) {
   const int lane = threadIdx.x & 31;
   const __nv_bfloat16* row = A.bounds + (static_cast<int64_t>(page_id(A, b, p)) * A.hkv + g) * 2 * A.d;
@@ -292,11 +295,12 @@ __device__ float exact_score(const SelectArgs& A, int b, int g, int p) {
 #pragma unroll 2
     for (int c = 2 * lane; c < A.d; c += 64) {
       const float2 lo = pair_at(row + c), hi = pair_at(row + A.d + c);
+      const double lx = lo.x, ly = lo.y, hx = hi.x, hy = hi.y;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float2 qv = h + k < A.group ? pair_at(q + k * A.d + c) : make_float2(0.f, 0.f);
-        sum[k] += fmaxf(qv.x * lo.x, qv.x * hi.x);
-        sum[k] += fmaxf(qv.y * lo.y, qv.y * hi.y);
+        sum[k] = fma(static_cast<double>(qv.x), qv.x > 0.f ? hx : lx, sum[k]);
+        sum[k] = fma(static_cast<double>(qv.y), qv.y > 0.f ? hy : ly, sum[k]);
       }
     }
 #pragma unroll
@@ -401,7 +405,7 @@ __device__ __forceinline__ void pick_pages(const SelectArgs& A, PickShared& S, f
       least = fminf(least, S.part[r][1]);
       greatest = fmaxf(greatest, S.part[r][2]);
     }
-    e *= 2.f * error_share(A.d);
+    e = 2.f * (error_share(A.d) * e + kErrorFloor);
     uint32_t k0 = order_key(least), k1 = order_key(greatest);
     int above;
     kth_range(S, m, need, 4, [&](int i) { return order_key(sc[i]); }, k0, k1, above);
@@ -443,8 +447,9 @@ __device__ __forceinline__ void pick_pages(const SelectArgs& A, PickShared& S, f
     } else {
       // many equal or nearly equal pages: all exactly, then a second selection
       for (int i0 = 32 * warp; i0 < m; i0 += kThreads) {
-        const float v = i0 + lane < m ? sc[i0 + lane] : INFINITY;
-        for (unsigned left = __ballot_sync(0xffffffffu, fabsf(v) != INFINITY); left != 0; left &= left - 1) {
+        // (where sums passed fp32's range, e with them, nothing is in or out yet)
+        const bool open = i0 + lane < m && (fabsf(sc[i0 + lane]) != INFINITY || !(e < INFINITY));
+        for (unsigned left = __ballot_sync(0xffffffffu, open); left != 0; left &= left - 1) {
           const int i = i0 + __ffs(left) - 1;
           const float x = exact_score(A, b, g, lo + i);
           if (lane == 0) sc[i] = x;
