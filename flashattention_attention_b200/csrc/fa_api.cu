@@ -616,7 +616,7 @@ fa_status fa_page_select(const fa_page_select_params* p, const fa_kv_pages* page
   if (p->top_k < 1 || p->top_k > kMaxTopPages || p->n_first < 0 || p->n_recent < 0 ||
       static_cast<int64_t>(p->n_first) + p->n_recent > p->top_k)
     return FA_ERR_INVALID;
-  if (pages->max_pages > 65536) return FA_ERR_UNSUPPORTED;
+  if (pages->max_pages > 65536 || !page_select_fits(p->batch, p->hkv, pages->max_pages)) return FA_ERR_UNSUPPORTED;
   if (p->batch == 0) return FA_OK;
   const void* ptrs[] = {p->q, p->key_bounds, p->cache_seqlens, p->selected};
   for (const void* q : ptrs)

@@ -70,6 +70,7 @@ fa_status launch_merge(float* o_acc, float* lse_acc, const void* o_part, int par
 fa_status launch_kv_append_rope(const fa_kv_append_rope_params& p, const fa_kv_pages& pages, const LaunchCtx& ctx);
 fa_status launch_kv_read(const fa_kv_read_params& p, const fa_kv_pages& pages, const LaunchCtx& ctx);
 size_t page_select_workspace_bytes(int batch, int hkv, int max_pages);
+bool page_select_fits(int batch, int hkv, int max_pages);  // whether one call can hold as many pages
 fa_status launch_page_select(const fa_page_select_params& p, const fa_kv_pages& pages, const LaunchCtx& ctx);
 // FA_I4 pools, or (top_k > 0) the chosen pages of any pool: whether the call
 // needs its workspace, and the launch

@@ -609,7 +609,6 @@ fa_status launch_width(const SelectArgs& all, const LaunchCtx& ctx) {
   for (int b0 = 0; b0 < all.batch; b0 += kMaxBatch) {
     SelectArgs A = all;
     A.batch = all.batch - b0 < kMaxBatch ? all.batch - b0 : kMaxBatch;
-    if (static_cast<int64_t>(A.batch) * A.hkv * ((A.max_pages + 15) / 16) >= (int64_t(1) << 31)) return FA_ERR_UNSUPPORTED;
     A.q += static_cast<int64_t>(b0) * A.hq * A.d;
     A.seqlens += b0;
     A.block_table += static_cast<int64_t>(b0) * A.max_pages;
@@ -629,6 +628,12 @@ fa_status launch_width(const SelectArgs& all, const LaunchCtx& ctx) {
 namespace {
 size_t parts_bytes(int64_t units, int max_pages) { return static_cast<size_t>(units) * ((max_pages + 15) / 16) * 16; }
 }  // namespace
+
+bool page_select_fits(int batch, int hkv, int max_pages) {
+  // a launch's groups of 16 pages, and one round of the device's warps past them, are counted in an int
+  const int64_t groups = static_cast<int64_t>(batch < kMaxBatch ? batch : kMaxBatch) * hkv * ((max_pages + 15) / 16);
+  return one_round(static_cast<int64_t>(batch) * hkv, max_pages) || groups < (int64_t(1) << 31) - (1 << 16);
+}
 
 size_t page_select_workspace_bytes(int batch, int hkv, int max_pages) {
   const int64_t units = static_cast<int64_t>(batch) * hkv;
