@@ -632,7 +632,10 @@ def _append_params(k_new, v_new, k_cache, v_cache, cur_pos, hkv, k_scales, v_sca
 
 _CACHE_DT = {torch.bfloat16: FA_BF16, torch.int8: FA_I8, torch.uint8: FA_I4}
 _BF16, _F32, _INT32 = torch.bfloat16, torch.float32, torch.int32
-_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# torch's own accessors, several times as fast as the public ones; a torch
+# without them (one built without CUDA) still imports this module
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _packer(cls):
