@@ -127,19 +127,19 @@ class PageSelectParams(ctypes.Structure):
 
 
 lib.fa_kv_append_rope_paged.restype = ctypes.c_int
-lib.fa_kv_append_rope_paged.argtypes = [_P, _P, _P]
+lib.fa_kv_append_rope_paged.argtypes = [ctypes.POINTER(KvAppendRopeParams), ctypes.POINTER(KvPages), _P]
 lib.fa_rope_table.restype = ctypes.c_int
 lib.fa_rope_table.argtypes = [_I32, _I32, ctypes.c_double, _P]
 lib.fa_kv_read_paged.restype = ctypes.c_int
-lib.fa_kv_read_paged.argtypes = [_P, _P, _P]
+lib.fa_kv_read_paged.argtypes = [ctypes.POINTER(KvReadParams), ctypes.POINTER(KvPages), _P]
 lib.fa_page_select_workspace_size.restype = ctypes.c_size_t
 lib.fa_page_select_workspace_size.argtypes = [_I32] * 3
 lib.fa_page_select.restype = ctypes.c_int
-lib.fa_page_select.argtypes = [_P, _P, _P]
+lib.fa_page_select.argtypes = [ctypes.POINTER(PageSelectParams), ctypes.POINTER(KvPages), _P]
 lib.fa_decode_pages_workspace_size.restype = ctypes.c_size_t
-lib.fa_decode_pages_workspace_size.argtypes = [_P, _P, _I32]
+lib.fa_decode_pages_workspace_size.argtypes = [ctypes.POINTER(DecodeParams), ctypes.POINTER(KvPages), _I32]
 lib.fa_attention_decode_selected.restype = ctypes.c_int
-lib.fa_attention_decode_selected.argtypes = [_P, _P, _P, _I32, _P]
+lib.fa_attention_decode_selected.argtypes = [ctypes.POINTER(DecodeParams), ctypes.POINTER(KvPages), _P, _I32, _P]
 lib.fa_compress_kv.restype = ctypes.c_int
 lib.fa_compress_kv.argtypes = [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int32,
                                ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
@@ -159,7 +159,7 @@ lib.fa_attention_merge.argtypes = [ctypes.POINTER(MergeParams), ctypes.c_void_p]
 lib.fa_attention_fwd_paged.restype = ctypes.c_int
 lib.fa_attention_fwd_paged.argtypes = [ctypes.POINTER(FwdParams), ctypes.POINTER(KvPages), ctypes.c_void_p]
 lib.fa_attention_decode_paged.restype = ctypes.c_int
-lib.fa_attention_decode_paged.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
+lib.fa_attention_decode_paged.argtypes = [ctypes.POINTER(DecodeParams), ctypes.POINTER(KvPages), ctypes.c_void_p]
 lib.fa_kv_append.restype = ctypes.c_int
 lib.fa_kv_append.argtypes = [ctypes.POINTER(KvAppendParams), ctypes.c_void_p]
 lib.fa_kv_append_paged.restype = ctypes.c_int
@@ -649,6 +649,19 @@ def _packer(cls):
 
 _pack_append, _pack_read, _pack_select = _packer(KvAppendRopeParams), _packer(KvReadParams), _packer(PageSelectParams)
 _pack_decode, _pack_pages = _packer(DecodeParams), _packer(KvPages)
+
+
+def _packed(name: str):
+    """The library's function for structures packed as bytes (lib.<name> itself takes the structures only)."""
+    fn = lib[name]  # another object than lib.<name>
+    typed = getattr(lib, name)
+    fn.restype, fn.argtypes = typed.restype, [_P if issubclass(a, ctypes._Pointer) else a for a in typed.argtypes]
+    return fn
+
+
+_append_call, _read_call = _packed("fa_kv_append_rope_paged"), _packed("fa_kv_read_paged")
+_select_call, _decode_size_call = _packed("fa_page_select"), _packed("fa_decode_pages_workspace_size")
+_decode_call, _selected_call = _packed("fa_attention_decode_paged"), _packed("fa_attention_decode_selected")
 _NO_EPILOGUE = bytes(ctypes.sizeof(EpiOp) * FA_MAX_EPILOGUE)
 
 
@@ -835,7 +848,7 @@ def kv_append_rope_paged(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torc
     p = _pack_append(kn, vn, qp, qo, kts, khs, vts, vhs, qts, qhs, ots, ohs, table, kp, vp, ks, vs, bounds, cu, pos,
                      lens, FA_BF16 if xt is _BF16 else FA_F32, kind, batch, total, hq, hkv, d, rot,
                      1 if interleaved else 0, table_rows)
-    _on_device(dev, stream, "fa_kv_append_rope_paged", lib.fa_kv_append_rope_paged, p, pg)
+    _on_device(dev, stream, "fa_kv_append_rope_paged", _append_call, p, pg)
     return q_out
 
 
@@ -868,7 +881,7 @@ def kv_read_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, cu_seqlens: torc
     p = _pack_read(kp, vp, ks, vs, ko, vo, _operand(cu_seqlens, "cu_seqlens", dev, _INT32, (batch + 1,)),
                    _operand(start, "start", dev, _INT32, (batch,)), kind, FA_BF16 if out_dtype is _BF16 else FA_F32,
                    batch, shape[1], hkv, d)
-    _on_device(dev, stream, "fa_kv_read_paged", lib.fa_kv_read_paged, p, pg)
+    _on_device(dev, stream, "fa_kv_read_paged", _read_call, p, pg)
     return k_out, v_out
 
 
@@ -933,7 +946,7 @@ def page_select(q: torch.Tensor, key_bounds: torch.Tensor, cache_seqlens: torch.
         nbytes, ws = workspace.numel() * workspace.element_size(), _workspace(workspace, dev)
     p = _pack_select(qp, bounds, lens, selected, batch, hq, hkv, d, top_k, _int(n_first, "n_first"),
                      _int(n_recent, "n_recent"), ws, nbytes)
-    _on_device(dev, stream, "fa_page_select", lib.fa_page_select, p,
+    _on_device(dev, stream, "fa_page_select", _select_call, p,
                _pack_pages(table, max_pages, _int(page_size, "page_size", 1), num_pages))
     return out
 
@@ -970,12 +983,12 @@ def _decode_pages(q, k_pages, v_pages, cache_seqlens, block_table, selected, hq,
               _int(max_seqlen, "max_seqlen"), _int(window, "window") if window > 0 else 0,
               1.0 / math.sqrt(d) if scale is None else ctypes.c_float(scale).value, 0, n_epilogue, ops)
     if selected is None:
-        top_k, what, fn, more = 0, "fa_attention_decode_paged", lib.fa_attention_decode_paged, ()
+        top_k, what, fn, more = 0, "fa_attention_decode_paged", _decode_call, ()
     else:
         shape = selected.shape
         if len(shape) != 3 or shape[0] != batch or shape[1] != hkv:
             raise ValueError(f"selected must be [{batch}, {hkv}, top_k]; got {tuple(shape)}")
-        top_k, what, fn = shape[2], "fa_attention_decode_selected", lib.fa_attention_decode_selected
+        top_k, what, fn = shape[2], "fa_attention_decode_selected", _selected_call
         more = (_operand(selected, "selected", dev, _INT32, shape), top_k)
     if workspace is not None:
         p = _pack_decode(*fields, _workspace(workspace, dev), workspace.numel() * workspace.element_size())
@@ -983,10 +996,10 @@ def _decode_pages(q, k_pages, v_pages, cache_seqlens, block_table, selected, hq,
         # only problems too long for one kernel need a workspace (the count of SMs decides)
         p = _pack_decode(*fields, 0, 0)
         if _current_device() == dev:
-            nbytes = lib.fa_decode_pages_workspace_size(p, pg, top_k)
+            nbytes = _decode_size_call(p, pg, top_k)
         else:
             with torch.cuda.device(dev):
-                nbytes = lib.fa_decode_pages_workspace_size(p, pg, top_k)
+                nbytes = _decode_size_call(p, pg, top_k)
         if nbytes:
             workspace = _new(q, nbytes, torch.uint8, stream)
             p = _pack_decode(*fields, workspace.data_ptr(), nbytes)
