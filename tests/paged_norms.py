@@ -6,7 +6,7 @@ import numpy as np
 import paged_plain as plain
 
 
-def attend(cache, q, hq, keys_of, scale):
+def attend(cache, q, hq, keys_of, scale, span=None):
     """(out, tolerance) [batch, hq, d] in fp64 of the softmax attention of q
     [batch, hq, d] over the keys keys_of(b, g) (some for every head).
 
@@ -24,9 +24,11 @@ def attend(cache, q, hq, keys_of, scale):
     within (exp(2 e) - 1) (P(v) + |out|).
     (4) exponentials, and the merges' few products: 2^-20 of the same.
     (5) sums over keys in fp32: a thread adds every eighth key's weight (and
-    offset) to a sum: n / 8 roundings, and a few for the lanes and the merges;
-    the second product adds 16 keys at a time (twice for two terms), each
-    addition losing at most 2^-22 of a partial sum of |p code step|."""
+    offset) to a sum: one rounding each, and a few for the lanes; the second
+    product adds 16 keys at a time (twice for two terms), each addition losing
+    at most 2^-22 of a partial sum of |p code step|.  So over the `span` keys
+    that one warp has at most (None: all); then the n / span warps' sums are
+    merged, every eighth by one warp, with a rounding each (two for l)."""
     B, d = q.shape[0], q.shape[-1]
     group = hq // cache.hkv
     out, tol = np.zeros((B, hq, d)), np.zeros((B, hq, d))
@@ -34,6 +36,8 @@ def attend(cache, q, hq, keys_of, scale):
         for g in range(cache.hkv):
             keys = np.asarray(keys_of(b, g))
             n = len(keys)
+            m = min(n, span or n)
+            merge = (n / m / 4 + 16) * 2.0 ** -24
             hs = slice(g * group, (g + 1) * group)
             k, v = cache.rows(b, g, keys)
             p, o = cache.table[b].numpy()[keys // cache.page], keys % cache.page
@@ -47,18 +51,18 @@ def attend(cache, q, hq, keys_of, scale):
                 steps = (w @ vs[:, 0])[:, None]
                 terms = (qa.sum(-1)[:, None] * (15 * ks[:, 0] + np.abs(ks[:, 1]))).max()
                 weights = (2.0 ** -11 + 2.0 ** -15) * 7.5 * steps
-                sums = ((n / 8 + 16) * 2.0 ** -24 * (w @ np.abs(vs[:, 1] + 7.5 * vs[:, 0]))[:, None]
-                        + (n / 16 + 16) * 2.0 ** -22 * 15 * steps)
+                sums = ((m / 8 + 16) * 2.0 ** -24 * (w @ np.abs(vs[:, 1] + 7.5 * vs[:, 0]))[:, None]
+                        + (m / 16 + 16) * 2.0 ** -22 * 15 * steps)
             else:
                 terms = (qa @ np.abs(k).T).max()
                 if cache.kind == "int8":
                     steps = (w @ cache.vs[p, g, o].double().numpy())[:, None]
                     weights = 2.0 ** -11 * pv + 2.0 ** -15 * 127 * steps
-                    sums = (n / 16 + 16) * 2.0 ** -22 * pv
+                    sums = (m / 16 + 16) * 2.0 ** -22 * pv
                 else:
                     weights = 2.0 ** -16 * pv
-                    sums = (n / 8 + 16) * 2.0 ** -22 * pv
-            sums = sums + (n / 8 + 16) * 2.0 ** -24 * np.abs(y)
+                    sums = (m / 8 + 16) * 2.0 ** -22 * pv
+            sums = sums + (m / 8 + 16) * 2.0 ** -24 * np.abs(y) + merge * (pv + np.abs(y))
             logit = (d + 8) * 2.0 ** -23 * terms * scale
             out[b, hs] = y
             tol[b, hs] = (2.0 ** -8 * np.abs(y) + weights + sums
@@ -66,11 +70,11 @@ def attend(cache, q, hq, keys_of, scale):
     return out, tol
 
 
-def repack(cache, k, v):
-    """The cache's first sequence's keys and values become k, v [hkv, n, d] fp32 (rounded to bf16, quantised)."""
+def repack(cache, k, v, b=0):
+    """Sequence b's keys and values become k, v [hkv, n, d] fp32 (rounded to bf16, quantised)."""
     n = k.shape[1]
     at = np.arange(n)
-    p, o = cache.table[0].numpy()[at // cache.page], at % cache.page
+    p, o = cache.table[b].numpy()[at // cache.page], at % cache.page
     for x, pool, scales in ((k, cache.kp, cache.ks), (v, cache.vp, cache.vs)):
         x = x.bfloat16()
         if cache.kind == "bf16":
