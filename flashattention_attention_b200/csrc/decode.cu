@@ -115,9 +115,11 @@ __device__ __forceinline__ int effective_workers(const SkArgs& A, long long T) {
   return static_cast<int>(p);
 }
 
-// Programmatic dependent launch: the plan kernel lets the decode kernel
-// start at once; the decode kernel waits for the plan's completion (its
-// zeroed counters) only where it first needs them.
+// The worker whose range [w*T/P, (w+1)*T/P) holds tile x.
+__device__ __forceinline__ int worker_of(long long x, long long T, long long P) {
+  return static_cast<int>((x * P + P - 1) / T);
+}
+__device__ __forceinline__ long long worker_begin(long long w, long long T, long long P) { return (w * T) / P; }
 
 // ---------------------------------------------------------------- plan
 // prefix[b] = sum over earlier sequences of (tiles x hkv); prefix[B] = T.
@@ -130,7 +132,7 @@ __global__ void __launch_bounds__(1024) decode_plan_kernel(const int32_t* __rest
                                                            int32_t* __restrict__ counters,
                                                            __nv_bfloat16* __restrict__ out, Epilogue epi,
                                                            unsigned int* status) {
-  griddep_launch_dependents();
+  griddep_launch_dependents();  // the decode kernel starts at once and waits where it first needs the plan
   __shared__ int32_t warp_sums[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nthreads = blockDim.x;

@@ -1,6 +1,6 @@
 // decode_mma.cuh -- what the single-query attention kernels share: geometry of
 // bf16 and int8 cache tiles in shared memory, shared-memory and mma.sync
-// wrappers, exact widening of codes, and the even split of tiles over workers.
+// wrappers, and exact widening of codes.
 #pragma once
 
 #include "device.cuh"
@@ -149,11 +149,5 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
 }
-
-// The worker whose range [w*T/P, (w+1)*T/P) holds tile x.
-__device__ __forceinline__ int worker_of(long long x, long long T, long long P) {
-  return static_cast<int>((x * P + P - 1) / T);
-}
-__device__ __forceinline__ long long worker_begin(long long w, long long T, long long P) { return (w * T) / P; }
 
 }  // namespace fa

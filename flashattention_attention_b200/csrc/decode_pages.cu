@@ -12,7 +12,8 @@
 //   O^T[d x 8 heads] += V^T[d x keys] . P'
 // A segment that lies within one worker's range is normalised and stored at
 // once; one that is split leaves a record (m, l, O) per worker, which a second
-// kernel merges (launched early, it waits for the first one's end).
+// kernel merges (launched early, it waits for the first one's end; a worker that
+// gave up waiting leaves no record, and its rows are meaningless, as reported).
 //
 // 4-bit rows (value = code * step + offset): codes enter the MMA exactly, as
 // subnormal fp16 numbers (one AND for two of them), and
@@ -34,12 +35,15 @@
 // that leaves the accumulators, which then hold sums of w_j (code_j - 7.5).
 //
 // A 4-bit row of 128 is 72 bytes and as much arithmetic as 256 bytes of bf16, so
-// the kernel is bound by its instructions and their latencies: about 430 per 32
-// keys and 8 head columns (128 of them the ANDs), ALU pipe 54 % and issue slots
-// 49 % busy at the 12 warps an SM that 150 registers and 72 KB a CTA leave room
-// for.  16 sequences, 274,568 keys, 32 query heads on 8: 66 us, 4.8 TB/s (73 %
-// of a plain copy); one of 131,071 keys, 64 heads on 8: 43 us, 3.5 TB/s (its
-// records leave room for eight warps an SM; twelve, with larger ones: 43 us).
+// the kernel is bound by its instructions and their latencies: about 450 per 32
+// keys and 8 head columns (128 of them the ANDs), ALU pipe 55 % and issue slots
+// 50 % busy at the 12 warps an SM that 152 registers and 72 KB a CTA leave room
+// for.  16 sequences, 274,568 keys, 32 query heads on 8: 67.6 us, 4.7 TB/s (72 %
+// of a plain copy); one of 131,071 keys, 64 heads on 8: 44.3 us, 3.4 TB/s (its
+// records leave room for eight warps an SM; twelve, with larger ones, were as
+// fast).  Weights in two fp16 terms, as bf16 caches have them, would double the
+// 16 MMAs of the second product to take the 1 % that their rounding adds to the
+// error of the bf16 result.
 #include <atomic>
 #include <type_traits>
 
@@ -55,7 +59,8 @@ constexpr uint32_t kOnes = 0x3c003c00u;  // fp16 1, twice
 constexpr float kTop = 32768.f;  // no weight as large as this enters fp16
 constexpr int kMaxBatch = 256;  // sequences per launch (their tile prefix is in shared memory)
 
-// Division of 0 <= x < 2^31 by a number known on the host: x / d =
+// Division of 0 <= x < 2^31 by a number known on the host, by multiplication
+// (Granlund and Montgomery, division by invariant integers): x / d =
 // (x * mul) >> (32 + shift) with mul = ceil(2^(32 + shift) / d), 2^shift >= d
 // (mul has up to 33 bits; its low 32 are kept and x is added back).
 struct FastDiv {
@@ -107,7 +112,7 @@ struct Tile {
   // A tile is one or two runs of 32 keys, each within one page.  A 4-bit run is
   // small, and what a tile costs beside its keys' arithmetic is spread over two
   // -- but not at D = 256, where two stages of 64 keys leave room for one CTA an
-  // SM (12 sequences of up to 1056 keys in 8 heads: 18.4 us, with 32 keys 16.1).
+  // SM (12 sequences of up to 1056 keys in 8 heads: 18.5 us, with 32 keys 16.4).
   static constexpr int kRuns = kI4 && D < 256 ? 2 : 1;
   static constexpr int kKeys = kTile * kRuns;
   static constexpr int kBytes = kI4 ? kKeys * D / 2 : G::kTileBytes;  // of K, and of V
@@ -1018,7 +1023,10 @@ __global__ void __launch_bounds__(kMergeThreads) decode_pages_merge_kernel(const
   }
   const int n = range & 0xffffu;
   if (n == 1) return;  // stored by its worker
-  if (n + static_cast<int>(range >> 16) > A.n_workers) return;  // never written: its worker gave up waiting (reported)
+  // A range that no worker wrote, since one gave up waiting (reported), is
+  // whatever the workspace held: past the workers it is not followed, and any
+  // other leads to records inside the workspace and a meaningless row.
+  if (n + static_cast<int>(range >> 16) > A.n_workers) return;
   const int64_t rec0 = static_cast<int64_t>(seg) + (range >> 16);
   float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
@@ -1139,11 +1147,13 @@ int64_t most_tiles(const PageArgs& A) {
 // second kernel's merge, is faster.  Counted in tiles one after the other: a
 // cluster's warps take seg_tiles / (4 c) each, in turns where the clusters do
 // not fit at once; an even split the device's share of all tiles, and about
-// four tiles' time for the records, the second launch and its reads.  (One
-// sequence of 257 keys: 8.3 us clustered, 10.3 us split; 128 pairs of 2048
-// chosen 4-bit keys: 16.5 and 23 us.  Long caches the other way round: one of
-// 131071 keys has 8 clusters of 32 warps for a device of 1184.)  Powers of two
-// only: clusters of three made the selection before them wait (43 -> 48 us).
+// four tiles' time for the records, the second launch and its reads.
+// Clustered and split, us, 4 bits, 8 KV heads of 128: one sequence of 257 keys
+// 8.3 and 10.3, 8192: 14.4 and 12.6, 10,240: 15.1 and 16.4, 12,288 (split from
+// here on): 16.5 and 15.1, 16,384: 20.5 and 18.4, 32,768: 32 and 21; 16 of 4096:
+// 22.6 and 26.7, of 8192: 41.0 and 41.7; 128 pairs of 2048 chosen keys: 16.4 and
+// 22.  Powers of two only: clusters of three made the selection before them wait
+// (43 -> 48 us).
 template <int D, int kKind>
 int cluster_of(int64_t segs, int64_t seg_tiles) {
   const int64_t resident = static_cast<int64_t>(device_sm_count()) * Tile<D, kKind>::kCtas;

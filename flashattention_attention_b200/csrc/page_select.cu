@@ -623,9 +623,6 @@ fa_status launch_width(const SelectArgs& all, const LaunchCtx& ctx) {
   return FA_OK;
 }
 
-}  // namespace
-
-namespace {
 size_t parts_bytes(int64_t units, int max_pages) { return static_cast<size_t>(units) * ((max_pages + 15) / 16) * 16; }
 }  // namespace
 

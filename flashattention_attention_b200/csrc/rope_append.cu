@@ -12,17 +12,20 @@
 //
 // One launch does everything.  A group of W lanes takes one token and some of
 // its rows: the token's sequence, slot, page and angles are found once and
-// four rows' loads are in flight at a time.  Keys whose page bounds are kept
+// two rows' loads are in flight at a time.  Keys whose page bounds are kept
 // go another way, since all new keys of a page have to meet: a CTA per page
 // (of the first new token in it), its groups spread over KV heads and slices
 // of the page's tokens, the slices' bounds joined in shared memory.  No page
 // is touched by two CTAs, so there are no atomics and no order to depend on.
 //
-// Bound by memory latency at three CTAs an SM (85 registers a thread), two rows
-// in flight a group: 16,384 tokens of 32 + 8 + 8 heads of 128 rotated, quantised
-// to 4 bits and read back move 450 MB in 107 us, 4.2 TB/s (64 % of a plain
-// copy).  Two CTAs an SM: 125 us; four, with fewer registers: 110; four rows in
-// flight: 108.
+// Waits for memory at three CTAs an SM, two rows in flight a group: 16,384 tokens
+// of 32 + 8 + 8 heads of 128 rotated, quantised to 4 bits and read back move 450
+// MB in 107 us, 4.2 TB/s (64 % of a plain copy).  Both roles share one kernel and
+// its 80 registers a thread, which do not hold all of it: 168 bytes a thread are
+// spilled for bf16 rows into 4 bits at d = 128 (-Xptxas -v; 112 into int8, 56 into
+// bf16, up to 188 for fp32 rows).  Two CTAs an SM: 125 us; four, with fewer
+// registers: 110; four rows in flight: 108; roles in kernels of their own have not
+// been tried.
 #include <type_traits>
 
 #include "internal.h"
@@ -676,9 +679,12 @@ fa_status launch_append_typed(AppendArgs& A, const LaunchCtx& ctx) {
   A.token_rows = A.hq + (A.bounds != nullptr ? 1 : 2) * A.pool.hkv;
   A.part_rows = rows_per_item(A.total, A.token_rows, kGroups);
   const int parts = (A.token_rows + A.part_rows - 1) / A.part_rows;
-  // page role: a CTA per token where there are few (96 sequences of one token
-  // each, read back too: 12.7 us, eight tokens a CTA 22), else per eight
-  // tokens, of which most open no page (16384-token prompt: 107 us, one a CTA 164)
+  // page role: a CTA per token where there are few, else per eight tokens.
+  // One and eight a CTA, us, 32 + 8 + 8 heads of 128 into 4 bits: 148 sequences
+  // of one token 8.3 and 16.5, 592 (the border on 148 SMs) 16.5 and 16.5, 740:
+  // 18.5 and 18.5, 1184: 26.7 and 20.5; a prompt of 592 tokens 22.2 and 20.5, of
+  // 2368: 37 and 24.7, of 16,384, most of which open no page, 164 and 107 with
+  // the read-back
   A.window = A.total <= 4 * device_sm_count() ? 1 : 8;
   int blocks = A.total / kGroups + 1;  // at least one, for the lengths alone
   const int page_blocks = A.bounds != nullptr ? A.total / A.window + 1 : 0;

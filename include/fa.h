@@ -416,8 +416,9 @@ FA_API fa_status fa_kv_append_paged(const fa_kv_append_params *p, const fa_kv_pa
  *   k_cache, v_cache, k_scales, v_scales  page pools as for
  *             fa_attention_decode_paged, cache_dtype FA_BF16, FA_I8 or FA_I4
  *   key_bounds  optional bf16 [num_pages, hkv, 2, head_dim]: per channel the
- *             least and the greatest of the page's stored keys, each key
- *             rounded to bf16.  A page whose slot 0 is among the new tokens
+ *             least and the greatest of the page's keys, each rotated and
+ *             rounded to bf16, whatever the cache then makes of it: a key of an
+ *             FA_I8 or FA_I4 pool may lie past them by half a step.  A page whose slot 0 is among the new tokens
  *             starts afresh, any other adds the new keys to what it holds
  * A bf16 pool gets each value rounded once.  FA_I8 rows are quantised exactly
  * as fa_compress_kv does (from the rotated fp32 values).  FA_I4 rows: with lo
@@ -513,11 +514,12 @@ FA_API fa_status fa_kv_read_paged(const fa_kv_read_params *p, const fa_kv_pages 
  * pages worth attending to.  Page p of sequence b (n_b = ceil(L_b /
  * page_size) pages) has for KV head g the score
  *   max over the group's query heads h of  sum_d max(q_hd lo_d, q_hd hi_d),
- * an upper bound of the unscaled q . k over the page's keys, with lo and hi
- * the page's key_bounds; the sum is taken to far more than fp32's precision
- * and rounded to fp32 once.  The first n_first and the last n_recent pages
- * are always kept, the rest of top_k goes to the highest scores, the lower
- * page number first where scores are equal.
+ * an upper bound of the unscaled q . k over the page's keys as they were
+ * bounded (before their quantisation), with lo <= hi the page's key_bounds; the
+ * sum is taken to far more than fp32's precision and range and rounded to fp32
+ * once.  The first n_first and the last n_recent pages are always kept, the
+ * rest of top_k goes to the highest scores, the lower page number first where
+ * scores are equal.
  *   q         [batch*hq, head_dim] bf16 (a decode step's queries)
  *   key_bounds  bf16 [num_pages, hkv, 2, head_dim] (fa_kv_append_rope_paged)
  *   cache_seqlens device int32 [batch]; a length outside [0, capacity] is
