@@ -52,9 +52,9 @@ KERNEL_SOURCES = {
     "prefill_tc_kernel<128,bf16>": ["prefill_tc.cu", "umma.cuh", "device.cuh", "layout.cuh"],
     "prefill_tc_kernel<128,int8>": ["prefill_tc.cu", "umma.cuh", "device.cuh", "layout.cuh"],
     "prefill_tc_kernel<64,bf16>": ["prefill_tc.cu", "umma.cuh", "device.cuh", "layout.cuh"],
-    "decode_sk_kernel<128>": ["decode.cu", "device.cuh"],
-    "decode_sk_kernel<128,bf16>": ["decode.cu", "device.cuh"],
-    "compress_rows8_kernel<bf16,16>": ["quant.cu", "device.cuh"],
+    "decode_sk_kernel<128>": ["decode.cu", "decode_mma.cuh", "device.cuh"],
+    "decode_sk_kernel<128,bf16>": ["decode.cu", "decode_mma.cuh", "device.cuh"],
+    "compress_rows8_kernel<bf16,16>": ["quant.cu", "quant.cuh", "device.cuh"],
 }
 
 
